@@ -325,6 +325,153 @@ int epl_expert_scale(const epl_problem *p, const uint16_t *rows_in,
                      const int32_t *m_indices, int64_t capacity_rows,
                      uint16_t *rows_out, const void *workspace, void *stream);
 
+/* ======================================================================= *
+ * The layer around the dispatch: the router before it, the experts'
+ * products between scatter and combine, and their gradients. A layer runs
+ *   epl_route -> epl_dispatch -> epl_expert_product (twice) -> epl_combine
+ * and backwards
+ *   epl_combine_backward -> epl_expert_product with a gradient activation and
+ *   EPL_WEIGHT_IN_OUT, epl_expert_weight_grad -> epl_combine with unit weights
+ *   (the gradient of the dispatch: the rows of a token summed) and
+ *   epl_route_backward.
+ * The conventions above hold: device pointers to dense row-major arrays, the
+ * caller owns every buffer, calls only enqueue on `stream`, arguments are
+ * checked on the host first. These calls need no workspace, so captured
+ * graphs and concurrent streams share nothing. No output may overlap an
+ * input unless it says so. Results are deterministic, bit for bit.
+ * ======================================================================= */
+
+/* ---- router ------------------------------------------------------------- */
+#define EPL_SCORE_SOFTMAX 0
+#define EPL_SCORE_SIGMOID 1
+
+typedef struct epl_router {
+    int64_t num_tokens;   /* T >= 0, T * K <= INT32_MAX                        */
+    int32_t num_topk;     /* K, 1 <= K <= 64, K <= E                           */
+    int32_t num_experts;  /* E, 1 <= E <= 2048                                 */
+    int32_t score;        /* EPL_SCORE_*                                       */
+    int32_t num_groups;   /* G: 1 = no groups; G <= 64, E % G == 0, group g is
+                             the experts [g*E/G, (g+1)*E/G)                    */
+    int32_t topk_groups;  /* groups that stay, 1 .. G, with room for K experts */
+    int32_t group_top;    /* 1 or 2: a group scores its largest choice score,
+                             or the sum of its two largest                     */
+    int32_t renormalize;  /* 1: weights divided by their sum over the choice   */
+    int32_t logits_type;  /* EPL_OUT_F32 or EPL_OUT_BF16                       */
+    float   scale;        /* finite; multiplies the weights                    */
+    int32_t reserved;     /* must be 0                                         */
+} epl_router;
+
+/* Host-only check of a router description. Needs no GPU. */
+int epl_router_validate(const epl_router *p);
+
+/* Routing. For every token t with logits l [E] (rows of `logits` [T, E]):
+ *   s = softmax(l) or sigmoid(l);  choice score c = s + bias (bias [E] fp32,
+ *   NULL = 0);  the topk_groups groups of the largest group score stay; the
+ *   K largest c among their experts, in descending order, are the choice;
+ *   topk_idx[t, k] = the expert, topk_weights[t, k] = scale * s, divided by
+ *   the sum of the choice's s with `renormalize` (0 where that sum is 0).
+ * Equal scores go to the lower index (of group or expert). Without a bias
+ * (and without sums of two over groups) the order is the exact order of the
+ * logits; otherwise scores are binary64 and compare to 41 bits.
+ * An expert whose logit or bias is -inf or NaN is never chosen and has score
+ * 0; a +inf logit or bias counts as the largest finite one; the lowest
+ * finite logit is a candidate like any other. Where fewer than K candidates
+ * are left, and in every slot of a token with token_mask[t] == 0 (uint8 [T],
+ * NULL = all tokens live), topk_idx is -1 and the weight 0: "no selection"
+ * to the dispatch. */
+int epl_route(const epl_router *p, const void *logits, const float *bias,
+              const uint8_t *token_mask, int64_t *topk_idx, float *topk_weights, void *stream);
+
+/* Gradient of the logits: grad_logits [T, E] (of logits_type, every element
+ * written) from grad_weights [T, K] fp32, for the choice topk_idx that
+ * epl_route made (the choice itself has no gradient, nor has the bias). A
+ * slot outside [0, E) is no selection: its grad_weights is not used. Slots
+ * of a token that name the same expert add up. Only score, renormalize and
+ * scale of the description matter, besides its sizes and type. */
+int epl_route_backward(const epl_router *p, const void *logits, const int64_t *topk_idx,
+                       const float *grad_weights, void *grad_logits, void *stream);
+
+/* ---- experts' products ---------------------------------------------------- */
+#define EPL_ACT_NONE        0   /* y = z                                        */
+#define EPL_ACT_SILU        1   /* y = z * sigmoid(z)                           */
+#define EPL_ACT_GELU        2   /* y = z * (1 + erf(z / sqrt 2)) / 2            */
+#define EPL_ACT_SWIGLU      3   /* y [rows, N/2] = silu(z[:, :N/2]) * z[:, N/2:];
+                                   N % 16 == 0                                  */
+#define EPL_ACT_SILU_GRAD   4   /* y = z * silu'(pre)                           */
+#define EPL_ACT_GELU_GRAD   5   /* y = z * gelu'(pre)                           */
+#define EPL_ACT_SWIGLU_GRAD 6   /* pre, y [rows, 2N]: with a = pre[:, :N] and
+                                   u = pre[:, N:], y[:, :N] = z * u * silu'(a)
+                                   and y[:, N:] = z * silu(a)                   */
+#define EPL_WEIGHT_OUT_IN 0     /* weight [E, N, K]: z = x W^T                  */
+#define EPL_WEIGHT_IN_OUT 1     /* weight [E, K, N]: z = x W (the data gradient
+                                   of a product with the same array as [E, out,
+                                   in])                                         */
+
+typedef struct epl_product_desc {
+    int64_t num_rows;      /* rows of the ragged buffers, 0 .. INT32_MAX        */
+    int64_t expected_rows; /* rows that the experts together are expected to
+                              have, 0 = num_rows. Chooses the kernel only: the
+                              results hold for any counts. Give it where the
+                              buffers have many more rows than are routed.      */
+    int32_t num_experts;   /* E, 1 <= E <= 2048                                 */
+    int32_t in_cols;       /* K, 8 .. 2^20, K % 8 == 0                          */
+    int32_t out_cols;      /* N, 8 .. 2^20, N % 8 == 0, K * N <= 2^29           */
+    int32_t weight_layout; /* EPL_WEIGHT_*                                      */
+    int32_t activation;    /* EPL_ACT_*                                         */
+    int32_t out_type;      /* y: EPL_OUT_F32 or EPL_OUT_BF16                    */
+    int32_t reserved;      /* must be 0                                         */
+} epl_product_desc;
+
+/* Host-only check of a product description. Needs no GPU. */
+int epl_product_validate(const epl_product_desc *p);
+
+/* Product of every expert's rows with its weight. For expert e and its rows
+ * p in [expert_start_loc[e], expert_start_loc[e] + num_tokens_per_expert[e])
+ * (both int32 [E] on the GPU, as the dispatch writes them):
+ *   z[p, :] = x[p, :] . weight[e] + bias[e]      (fp32 sums)
+ *   y[p, :] = act(z[p, :]) + residual[p, :]
+ * x bf16 [num_rows, K]; bias fp32 [E, N] or NULL; residual bf16, of y's
+ * shape, or NULL (may be y itself when y is bf16). `pre` bf16 [num_rows, N]:
+ * with activations NONE .. SWIGLU it receives z (rounded to nearest even) if
+ * it is not NULL, for the backward pass; the *_GRAD activations read there
+ * what the forward pass left, take no bias and no residual, and z is the
+ * gradient with respect to the activation's output. Rows that belong to no
+ * expert (padding, capacity beyond the total) are left as they were in y and
+ * pre; a block is cut to the buffer's rows. Blocks of different experts must
+ * not share rows. All pointers 16-byte aligned but the int32 ones. */
+int epl_expert_product(const epl_product_desc *p, const uint16_t *x, const uint16_t *weight,
+                       const float *bias, const uint16_t *residual,
+                       const int32_t *expert_start_loc, const int32_t *num_tokens_per_expert,
+                       uint16_t *pre, void *y, void *stream);
+
+/* Gradient of the weights and the bias of a product (weight_layout OUT_IN,
+ * activation NONE): for every expert
+ *   grad_weight[e] [N, K] = sum over its rows p of grad[p, :]^T x[p, :]
+ *   grad_bias[e]   [N]    = sum over its rows p of grad[p, :]
+ * with grad bf16 [num_rows, N] (the gradient of z), x bf16 [num_rows, K],
+ * grad_weight of out_type, grad_bias fp32 or NULL. An expert without rows
+ * gets zeros. With `accumulate` 1 both are added to what the arrays hold
+ * (in fp32, one rounding). */
+int epl_expert_weight_grad(const epl_product_desc *p, const uint16_t *grad, const uint16_t *x,
+                           const int32_t *expert_start_loc, const int32_t *num_tokens_per_expert,
+                           int accumulate, void *grad_weight, float *grad_bias, void *stream);
+
+/* ---- gradient of the combine ---------------------------------------------- */
+/* For y = epl_combine(expert_out, output_index, topk_weights):
+ *   grad_rows[output_index[t, k], :] = bf16_rne(topk_weights[t, k] * grad_y[t, :])
+ *   grad_weights[t, k] = sum_h grad_y[t, h] * expert_out[output_index[t, k], h]
+ * grad_y is fp32 or bf16 [T, H] per `grad_type` (EPL_OUT_*), grad_rows bf16
+ * [expert_rows, H], grad_weights fp32 [T, K] (every element written; 0 for a
+ * slot without a row). Rows that no slot names are left as they were. A row
+ * may be named by one slot only, as the dispatch makes them (a row named
+ * twice would get the gradient of one of its slots). An output_index >=
+ * expert_rows is skipped and recorded in `workspace` as in epl_combine. */
+int epl_combine_backward(const epl_problem *p, int grad_type, const void *grad_y,
+                         const uint16_t *expert_out, int64_t expert_rows,
+                         const int32_t *output_index, const float *topk_weights,
+                         uint16_t *grad_rows, float *grad_weights, void *workspace,
+                         void *stream);
+
 /* Synchronises `stream`, then returns the status recorded in `workspace`
  * since the last epl_layout / epl_dispatch: EPL_OK, EPL_ERANGE or
  * EPL_ECAPACITY (EPL_ERANGE first if both occurred), or EPL_EHIP. */

@@ -26,7 +26,12 @@ __all__ = [
     "EPL_OK", "EPL_EINVAL", "EPL_ERANGE", "EPL_ECAPACITY", "EPL_EHIP", "EPL_OUT_F32",
     "EPL_OUT_BF16", "prepare", "epl_scatter_fp8", "epl_dispatch_fp8", "EPL_SCALE_NONE",
     "EPL_SCALE_F32", "EPL_SCALE_UE8M0", "epl_dispatch_static", "StaticWorkspace",
-    "EPL_STATIC_WORKSPACE_BYTES",
+    "EPL_STATIC_WORKSPACE_BYTES", "Router", "Product", "epl_router_validate", "epl_route",
+    "epl_route_backward", "epl_product_validate", "epl_expert_product", "epl_expert_weight_grad",
+    "epl_combine_backward", "route", "route_backward", "expert_product", "expert_weight_grad",
+    "combine_backward", "dispatch_backward", "EPL_SCORE_SOFTMAX", "EPL_SCORE_SIGMOID",
+    "EPL_ACT_NONE", "EPL_ACT_SILU", "EPL_ACT_GELU", "EPL_ACT_SWIGLU", "EPL_ACT_SILU_GRAD",
+    "EPL_ACT_GELU_GRAD", "EPL_ACT_SWIGLU_GRAD", "EPL_WEIGHT_OUT_IN", "EPL_WEIGHT_IN_OUT",
 ]
 
 EPL_OK = 0
@@ -40,6 +45,17 @@ EPL_SCALE_NONE = 0
 EPL_SCALE_F32 = 1
 EPL_SCALE_UE8M0 = 2
 EPL_STATIC_WORKSPACE_BYTES = 8 << 20
+EPL_SCORE_SOFTMAX = 0
+EPL_SCORE_SIGMOID = 1
+EPL_ACT_NONE = 0
+EPL_ACT_SILU = 1
+EPL_ACT_GELU = 2
+EPL_ACT_SWIGLU = 3
+EPL_ACT_SILU_GRAD = 4
+EPL_ACT_GELU_GRAD = 5
+EPL_ACT_SWIGLU_GRAD = 6
+EPL_WEIGHT_OUT_IN = 0
+EPL_WEIGHT_IN_OUT = 1
 
 # Every function include/epl.h declares; tests check the library exports them.
 C_ENTRY_POINTS = (
@@ -47,6 +63,8 @@ C_ENTRY_POINTS = (
     "epl_scatter", "epl_dispatch", "epl_scatter_fp8", "epl_dispatch_fp8", "epl_combine",
     "epl_expert_scale", "epl_status", "epl_total", "epl_strerror", "epl_version",
     "epl_ll_workspace_bytes", "epl_ll_dispatch", "epl_dispatch_static",
+    "epl_router_validate", "epl_route", "epl_route_backward", "epl_product_validate",
+    "epl_expert_product", "epl_expert_weight_grad", "epl_combine_backward",
 )
 
 
@@ -90,6 +108,41 @@ class Problem(ctypes.Structure):
         return (f"Problem(T={self.num_tokens}, K={self.num_topk}, E={self.num_experts}, "
                 f"R={self.num_ranks}, H={self.hidden}, S={self.scale_cols}, "
                 f"a={self.expert_alignment}, G={self.ranks_per_node})")
+
+
+class Router(ctypes.Structure):
+    """epl_router: sizes and rules of the routing (see include/epl.h)."""
+
+    _fields_ = [
+        ("num_tokens", ctypes.c_int64),
+        ("num_topk", ctypes.c_int32),
+        ("num_experts", ctypes.c_int32),
+        ("score", ctypes.c_int32),
+        ("num_groups", ctypes.c_int32),
+        ("topk_groups", ctypes.c_int32),
+        ("group_top", ctypes.c_int32),
+        ("renormalize", ctypes.c_int32),
+        ("logits_type", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class Product(ctypes.Structure):
+    """epl_product_desc: sizes and epilogue of an experts' product (see
+    include/epl.h)."""
+
+    _fields_ = [
+        ("num_rows", ctypes.c_int64),
+        ("expected_rows", ctypes.c_int64),
+        ("num_experts", ctypes.c_int32),
+        ("in_cols", ctypes.c_int32),
+        ("out_cols", ctypes.c_int32),
+        ("weight_layout", ctypes.c_int32),
+        ("activation", ctypes.c_int32),
+        ("out_type", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
 
 
 _LIB: Optional[ctypes.CDLL] = None
@@ -160,6 +213,21 @@ def load() -> ctypes.CDLL:
     lib.epl_combine.restype = i32
     lib.epl_expert_scale.argtypes = [_PP, _P, _P, i64, _P, _P, _P]
     lib.epl_expert_scale.restype = i32
+    pr, pp = ctypes.POINTER(Router), ctypes.POINTER(Product)
+    lib.epl_router_validate.argtypes = [pr]
+    lib.epl_router_validate.restype = i32
+    lib.epl_route.argtypes = [pr, _P, _P, _P, _P, _P, _P]
+    lib.epl_route.restype = i32
+    lib.epl_route_backward.argtypes = [pr, _P, _P, _P, _P, _P]
+    lib.epl_route_backward.restype = i32
+    lib.epl_product_validate.argtypes = [pp]
+    lib.epl_product_validate.restype = i32
+    lib.epl_expert_product.argtypes = [pp, _P, _P, _P, _P, _P, _P, _P, _P, _P]
+    lib.epl_expert_product.restype = i32
+    lib.epl_expert_weight_grad.argtypes = [pp, _P, _P, _P, _P, i32, _P, _P, _P]
+    lib.epl_expert_weight_grad.restype = i32
+    lib.epl_combine_backward.argtypes = [_PP, i32, _P, _P, i64, _P, _P, _P, _P, _P, _P]
+    lib.epl_combine_backward.restype = i32
     lib.epl_status.argtypes = [_P, _P]
     lib.epl_status.restype = i32
     lib.epl_total.argtypes = [_P, _P]
@@ -556,6 +624,132 @@ def epl_expert_scale(p: Problem, rows_in, m_indices, capacity_rows, rows_out, wo
            "epl_expert_scale")
 
 
+def _launch(name: str, dev, stream, *args):
+    """Call C entry point `name` with `dev` as the current device (kernels are
+    launched on the current device, which need not be the tensors') and the
+    stream last."""
+    torch = _torch()
+    fn = getattr(load(), name)
+    if dev.index is None or torch.cuda.current_device() == dev.index:
+        rc = fn(*args, _stream(stream, dev))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, _stream(stream, dev))
+    if rc != EPL_OK:
+        raise EplError(rc, name)
+
+
+def _type_code(dtype, name) -> int:
+    torch = _torch()
+    if dtype == torch.float32:
+        return EPL_OUT_F32
+    if dtype == torch.bfloat16:
+        return EPL_OUT_BF16
+    raise TypeError(f"{name} must be torch.float32 or torch.bfloat16, got {dtype}")
+
+
+def epl_router_validate(p: Router) -> int:
+    return load().epl_router_validate(ctypes.byref(p))
+
+
+def _router_dtype(p: Router):
+    return _torch().bfloat16 if p.logits_type == EPL_OUT_BF16 else _torch().float32
+
+
+def epl_route(p: Router, logits, bias, token_mask, topk_idx, topk_weights, stream=None):
+    torch = _torch()
+    T, K, E = p.num_tokens, p.num_topk, p.num_experts
+    _need(logits, "logits", _router_dtype(p), (T, E))
+    dev = logits.device
+    _need(bias, "bias", torch.float32, (E,), dev, allow_none=True)
+    _need(token_mask, "token_mask", torch.uint8, (T,), dev, allow_none=True)
+    _need(topk_idx, "topk_idx", torch.int64, (T, K), dev)
+    _need(topk_weights, "topk_weights", torch.float32, (T, K), dev)
+    _launch("epl_route", dev, stream, ctypes.byref(p), _ptr(logits), _ptr(bias), _ptr(token_mask),
+            _ptr(topk_idx), _ptr(topk_weights))
+
+
+def epl_route_backward(p: Router, logits, topk_idx, grad_weights, grad_logits, stream=None):
+    torch = _torch()
+    T, K, E = p.num_tokens, p.num_topk, p.num_experts
+    dt = _router_dtype(p)
+    _need(logits, "logits", dt, (T, E))
+    dev = logits.device
+    _need(topk_idx, "topk_idx", torch.int64, (T, K), dev)
+    _need(grad_weights, "grad_weights", torch.float32, (T, K), dev)
+    _need(grad_logits, "grad_logits", dt, (T, E), dev)
+    _launch("epl_route_backward", dev, stream, ctypes.byref(p), _ptr(logits), _ptr(topk_idx),
+            _ptr(grad_weights), _ptr(grad_logits))
+
+
+def epl_product_validate(p: Product) -> int:
+    return load().epl_product_validate(ctypes.byref(p))
+
+
+def _blocks(p: Product, expert_start_loc, num_tokens_per_expert, dev):
+    torch = _torch()
+    _need(expert_start_loc, "expert_start_loc", torch.int32, (p.num_experts,), dev)
+    _need(num_tokens_per_expert, "num_tokens_per_expert", torch.int32, (p.num_experts,), dev)
+
+
+def epl_expert_product(p: Product, x, weight, bias, residual, expert_start_loc,
+                       num_tokens_per_expert, pre, y, stream=None):
+    torch = _torch()
+    rows, E, K, N = p.num_rows, p.num_experts, p.in_cols, p.out_cols
+    bf16 = torch.bfloat16
+    _need(x, "x", bf16, (rows, K))
+    dev = x.device
+    _need(weight, "weight", bf16, (E, K, N) if p.weight_layout == EPL_WEIGHT_IN_OUT else (E, N, K),
+          dev)
+    _need(bias, "bias", torch.float32, (E, N), dev, allow_none=True)
+    grad = p.activation >= EPL_ACT_SILU_GRAD
+    cols = N // 2 if p.activation == EPL_ACT_SWIGLU else \
+        2 * N if p.activation == EPL_ACT_SWIGLU_GRAD else N
+    _need(residual, "residual", bf16, (rows, cols), dev, allow_none=True)
+    _need(pre, "pre", bf16, (rows, cols if grad else N), dev, allow_none=not grad)
+    _need(y, "y", bf16 if p.out_type == EPL_OUT_BF16 else torch.float32, (rows, cols), dev)
+    _blocks(p, expert_start_loc, num_tokens_per_expert, dev)
+    _launch("epl_expert_product", dev, stream, ctypes.byref(p), _ptr(x), _ptr(weight), _ptr(bias),
+            _ptr(residual), _ptr(expert_start_loc), _ptr(num_tokens_per_expert), _ptr(pre),
+            _ptr(y))
+
+
+def epl_expert_weight_grad(p: Product, grad, x, expert_start_loc, num_tokens_per_expert,
+                           accumulate, grad_weight, grad_bias=None, stream=None):
+    torch = _torch()
+    rows, E, K, N = p.num_rows, p.num_experts, p.in_cols, p.out_cols
+    _need(grad, "grad", torch.bfloat16, (rows, N))
+    dev = grad.device
+    _need(x, "x", torch.bfloat16, (rows, K), dev)
+    _need(grad_weight, "grad_weight",
+          torch.bfloat16 if p.out_type == EPL_OUT_BF16 else torch.float32, (E, N, K), dev)
+    _need(grad_bias, "grad_bias", torch.float32, (E, N), dev, allow_none=True)
+    _blocks(p, expert_start_loc, num_tokens_per_expert, dev)
+    _launch("epl_expert_weight_grad", dev, stream, ctypes.byref(p), _ptr(grad), _ptr(x),
+            _ptr(expert_start_loc), _ptr(num_tokens_per_expert), int(bool(accumulate)),
+            _ptr(grad_weight), _ptr(grad_bias))
+
+
+def epl_combine_backward(p: Problem, grad_y, expert_out, expert_rows, output_index, topk_weights,
+                         grad_rows, grad_weights, workspace=None, stream=None):
+    torch = _torch()
+    T, K, H = p.num_tokens, p.num_topk, p.hidden
+    _need(output_index, "output_index", torch.int32, (T, K))
+    dev = output_index.device
+    code = _type_code(getattr(grad_y, "dtype", None), "grad_y")
+    _need(grad_y, "grad_y", grad_y.dtype, (T, H), dev)
+    _need(expert_out, "expert_out", torch.bfloat16, (expert_rows, H), dev)
+    _need(topk_weights, "topk_weights", torch.float32, (T, K), dev)
+    _need(grad_rows, "grad_rows", torch.bfloat16, (expert_rows, H), dev)
+    _need(grad_weights, "grad_weights", torch.float32, (T, K), dev)
+    _need_ws_arg(workspace, dev, allow_none=True)
+    if workspace is not None:
+        _need_workspace(workspace, WS_HEADER_BYTES, "epl_combine_backward")
+    _launch("epl_combine_backward", dev, stream, _prob(p), code, _ptr(grad_y), _ptr(expert_out),
+            int(expert_rows), _ptr(output_index), _ptr(topk_weights), _ptr(grad_rows),
+            _ptr(grad_weights), _ptr(workspace))
+
+
 def epl_status(workspace, stream=None) -> int:
     _need_workspace(workspace, WS_HEADER_BYTES, "epl_status")
     return int(load().epl_status(_ptr(workspace), _stream(stream, workspace.device)))
@@ -698,3 +892,148 @@ def expert_scale(res: DispatchResult, rows_in=None, stream=None):
     epl_expert_scale(res.problem, rows_in, res.m_indices, rows_in.shape[0], out, res.workspace,
                      stream)
     return out
+
+
+_SCORES = {"softmax": EPL_SCORE_SOFTMAX, "sigmoid": EPL_SCORE_SIGMOID}
+_ACTIVATIONS = {"none": EPL_ACT_NONE, "silu": EPL_ACT_SILU, "gelu": EPL_ACT_GELU,
+                "swiglu": EPL_ACT_SWIGLU, "silu_grad": EPL_ACT_SILU_GRAD,
+                "gelu_grad": EPL_ACT_GELU_GRAD, "swiglu_grad": EPL_ACT_SWIGLU_GRAD}
+
+
+def _named(table, name, what):
+    try:
+        return table[name]
+    except (KeyError, TypeError):
+        raise ValueError(f"unknown {what} {name!r}; choose from {sorted(table)}") from None
+
+
+def _matrix(t, name, dims):
+    if not isinstance(t, _torch().Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got {tuple(t.shape)}")
+
+
+def route(logits, num_topk: int, score: str = "softmax", bias=None, num_groups: int = 1,
+          topk_groups: int = 1, group_top: int = 1, renormalize: bool = False, scale: float = 1.0,
+          token_mask=None, stream=None):
+    """Router: (topk_idx int64 [T, K], topk_weights fp32 [T, K]) from logits
+    [T, E] (fp32 or bf16), as `dispatch` and `combine` take them; the rules
+    are those of epl_route in include/epl.h. `token_mask` (uint8 [T], 0 =
+    padding) gives a token no selection at all."""
+    torch = _torch()
+    _matrix(logits, "logits", 2)
+    T, E = logits.shape
+    p = Router(T, int(num_topk), E, _named(_SCORES, score, "score"), int(num_groups),
+               int(topk_groups), int(group_top), int(bool(renormalize)),
+               _type_code(logits.dtype, "logits"), float(scale), 0)
+    _check(epl_router_validate(p), "epl_router_validate")
+    idx = torch.empty((T, p.num_topk), dtype=torch.int64, device=logits.device)
+    w = torch.empty((T, p.num_topk), dtype=torch.float32, device=logits.device)
+    epl_route(p, logits, bias, token_mask, idx, w, stream)
+    return idx, w
+
+
+def route_backward(logits, topk_idx, grad_weights, score: str = "softmax",
+                   renormalize: bool = False, scale: float = 1.0, stream=None):
+    """Gradient of `route`'s logits (their dtype) from that of its weights,
+    for the choice topk_idx it made."""
+    torch = _torch()
+    _matrix(logits, "logits", 2)
+    _matrix(topk_idx, "topk_idx", 2)
+    T, E = logits.shape
+    p = Router(T, topk_idx.shape[1], E, _named(_SCORES, score, "score"), 1, 1, 1,
+               int(bool(renormalize)), _type_code(logits.dtype, "logits"), float(scale), 0)
+    _check(epl_router_validate(p), "epl_router_validate")
+    grad = torch.empty_like(logits)
+    epl_route_backward(p, logits, topk_idx, grad_weights, grad, stream)
+    return grad
+
+
+def expert_product(x, weight, expert_start_loc, num_tokens_per_expert, bias=None,
+                   activation: str = "none", residual=None, pre=None, out=None, out_dtype=None,
+                   transposed: bool = False, expected_rows: int = 0, stream=None):
+    """act(x @ weight[e]^T + bias[e]) + residual for the rows of each expert
+    (x [rows, K] bf16, e.g. DispatchResult.out; weight [E, N, K] bf16), as
+    epl_expert_product in include/epl.h. transposed=True takes weight as
+    [E, K, N] and multiplies by it as it is: with the forward pass's array
+    that is the data gradient. `pre` (bf16 [rows, N]) receives the product
+    before the activation, or feeds a "..._grad" activation. Rows outside the
+    experts' blocks are not written: pass `out` to choose what they hold."""
+    torch = _torch()
+    _matrix(x, "x", 2)
+    _matrix(weight, "weight", 3)
+    E = weight.shape[0]
+    N = weight.shape[2] if transposed else weight.shape[1]
+    act = _named(_ACTIVATIONS, activation, "activation")
+    if out is not None:
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise ValueError(f"out is {out.dtype}, out_dtype {out_dtype}")
+        out_dtype = out.dtype
+    elif out_dtype is None:
+        out_dtype = torch.bfloat16
+    p = Product(x.shape[0], int(expected_rows), E, x.shape[1], N,
+                EPL_WEIGHT_IN_OUT if transposed else EPL_WEIGHT_OUT_IN, act,
+                _type_code(out_dtype, "out"), 0)
+    _check(epl_product_validate(p), "epl_product_validate")
+    if out is None:
+        cols = N // 2 if act == EPL_ACT_SWIGLU else 2 * N if act == EPL_ACT_SWIGLU_GRAD else N
+        out = torch.empty((x.shape[0], cols), dtype=out_dtype, device=x.device)
+    epl_expert_product(p, x, weight, bias, residual, expert_start_loc, num_tokens_per_expert, pre,
+                       out, stream)
+    return out
+
+
+def expert_weight_grad(grad, x, expert_start_loc, num_tokens_per_expert, out=None, out_dtype=None,
+                       bias_grad=None, accumulate: bool = False, stream=None):
+    """Gradient of expert_product's weight, [E, N, K], from that of its
+    product `grad` (bf16 [rows, N]) and its input x (bf16 [rows, K]).
+    `bias_grad` (fp32 [E, N]) receives the bias's. accumulate=True adds to
+    what `out` and `bias_grad` hold."""
+    torch = _torch()
+    _matrix(grad, "grad", 2)
+    _matrix(x, "x", 2)
+    _matrix(expert_start_loc, "expert_start_loc", 1)
+    E, N, K = expert_start_loc.shape[0], grad.shape[1], x.shape[1]
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        out = torch.empty((E, N, K), dtype=torch.bfloat16 if out_dtype is None else out_dtype,
+                          device=x.device)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError(f"out is {out.dtype}, out_dtype {out_dtype}")
+    p = Product(grad.shape[0], 0, E, K, N, EPL_WEIGHT_OUT_IN, EPL_ACT_NONE,
+                _type_code(out.dtype, "out"), 0)
+    _check(epl_product_validate(p), "epl_product_validate")
+    epl_expert_weight_grad(p, grad, x, expert_start_loc, num_tokens_per_expert, accumulate, out,
+                           bias_grad, stream)
+    return out
+
+
+def combine_backward(grad_y, expert_out, output_index, topk_weights, grad_rows=None,
+                     workspace=None, stream=None):
+    """Gradients of `combine`: (grad_rows bf16 like expert_out, grad_weights
+    fp32 [T, K]). Rows that no slot names are not written: pass `grad_rows` to
+    choose what they hold."""
+    torch = _torch()
+    _matrix(output_index, "output_index", 2)
+    _matrix(expert_out, "expert_out", 2)
+    T, K = output_index.shape
+    rows, H = expert_out.shape
+    p = Problem.make(T, K, 1, 1, H, 0)
+    _check(epl_validate(p), "epl_validate")
+    if grad_rows is None:
+        grad_rows = torch.empty_like(expert_out)
+    grad_weights = torch.empty((T, K), dtype=torch.float32, device=expert_out.device)
+    epl_combine_backward(p, grad_y, expert_out, rows, output_index, topk_weights, grad_rows,
+                         grad_weights, workspace, stream)
+    return grad_rows, grad_weights
+
+
+def dispatch_backward(grad_rows, output_index, out_dtype=None, workspace=None, stream=None):
+    """Gradient of `dispatch`'s x [T, H]: the sum of a token's rows of
+    grad_rows, i.e. `combine` with unit weights."""
+    torch = _torch()
+    _matrix(output_index, "output_index", 2)
+    ones = torch.ones(output_index.shape, dtype=torch.float32, device=output_index.device)
+    return combine(grad_rows, output_index, ones, out_dtype, workspace, stream)

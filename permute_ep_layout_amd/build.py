@@ -13,8 +13,11 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 INCLUDE = os.path.join(ROOT, "include")
 CSRC = os.path.join(PKG, "csrc")
-SOURCES = [os.path.join(CSRC, "epl.hip")]
-DEPENDS = SOURCES + [os.path.join(CSRC, "epl_kernels.h"), os.path.join(INCLUDE, "epl.h")]
+SOURCES = [os.path.join(CSRC, name) for name in
+           ("epl.hip", "epl_router.hip", "epl_product.hip", "epl_combine_backward.hip")]
+DEPENDS = SOURCES + [os.path.join(CSRC, "epl_kernels.h"),
+                     os.path.join(CSRC, "epl_router_kernels.h"),
+                     os.path.join(CSRC, "epl_product_kernels.h"), os.path.join(INCLUDE, "epl.h")]
 LIB = os.path.join(PKG, "libepl.so")
 ARCH = "gfx950"
 

@@ -763,7 +763,7 @@ int static_workspace(void **ws)
 
 extern "C" {
 
-int epl_version(void) { return 0x000300; }
+int epl_version(void) { return 0x000400; }
 
 int epl_validate(const epl_problem *p) { return problem_ok(p) ? EPL_OK : EPL_EINVAL; }
 

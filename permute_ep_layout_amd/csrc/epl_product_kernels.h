@@ -1,0 +1,730 @@
+// Device kernels of the experts' matrix products for gfx950 (CDNA4): the
+// product of each expert's block of rows with that expert's weight, its
+// gradients, and the column sums of the bias gradient.
+//
+// All of them are one contraction per expert,
+//     out[m, n] = sum_k P[m, k] * Q[n, k],   n contiguous in memory,
+// and differ in which operand has its contraction index contiguous:
+//     forward        P = rows [M, K]             Q = weight [N, K]
+//     data gradient  P = rows [M, K]             Q = weight [K, N]  (strided)
+//     weight grad.   P = d rows [K, M] (strided) Q = rows [K, N]    (strided)
+// The matrix instruction is v_mfma_f32_16x16x32_bf16: products of bf16 are
+// exact in binary32 and sums are kept in binary32.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "epl.h"
+
+namespace epl_product {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) void lds_void;
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+constexpr int kMaxExperts = 2048;
+constexpr int kTileThreads = 512;      // 8 waves: one workgroup fills a CU's four SIMDs twice
+constexpr int kTileK = 64;             // contraction depth of one LDS stage
+constexpr int kNumXcd = 8;
+
+struct Args {
+    const __bf16 *p;          // rows (forward, data gradient) or d rows (weight gradient)
+    const __bf16 *q;          // weights, or rows (weight gradient)
+    const float *bias;        // [E, N] or null
+    const __bf16 *residual;   // [rows, cols of y] or null
+    __bf16 *pre;              // [rows, .] or null: written by forward activations, read by gradient ones
+    void *y;                  // output
+    const int32_t *start, *count;
+    int64_t rows;             // rows of the ragged buffers
+    int E;
+    int K;                    // contraction (columns of x); weight gradient: columns of x = output columns
+    int N;                    // columns of the product; weight gradient: columns of d = output rows
+    int act;                  // EPL_ACT_*
+    int out_f32;
+    int accumulate;           // weight gradient: add to y
+};
+
+// An expert's block, cut to the buffer: [lo, lo + n).
+__device__ __forceinline__ int block_of(const Args &a, int e, int64_t &lo)
+{
+    const int64_t s = a.start[e], c = a.count[e];
+    lo = s < 0 ? 0 : s > a.rows ? a.rows : s;
+    int64_t hi = c <= 0 ? lo : s + c;
+    hi = hi > a.rows ? a.rows : hi;
+    return hi > lo ? (int)(hi - lo) : 0;
+}
+
+// ------------------------------------------------------------- epilogue --
+
+template <int C>
+__device__ __forceinline__ void load_bf16(const __bf16 *p, float (&v)[C])
+{
+    typedef __bf16 vec __attribute__((ext_vector_type(C)));
+    const vec r = *reinterpret_cast<const vec *>(p);
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+        v[i] = (float)r[i];
+}
+
+// One rounding to nearest even, of the finished binary32 value.
+template <int C>
+__device__ __forceinline__ void store_bf16(__bf16 *p, const float (&v)[C])
+{
+    typedef __bf16 vec __attribute__((ext_vector_type(C)));
+    vec r;
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+        r[i] = (__bf16)v[i];
+    *reinterpret_cast<vec *>(p) = r;
+}
+
+template <int C>
+__device__ __forceinline__ void store_out(const Args &a, int64_t at, const float (&v)[C])
+{
+    if (a.out_f32) {
+        float *y = static_cast<float *>(a.y) + at;
+#pragma unroll
+        for (int i = 0; i < C; i += 4)
+            *reinterpret_cast<f32x4 *>(y + i) = f32x4{v[i], v[i + 1], v[i + 2], v[i + 3]};
+    } else {
+        store_bf16<C>(static_cast<__bf16 *>(a.y) + at, v);
+    }
+}
+
+// 1 / (1 + exp(-z)): exp overflows to infinity for z below -88, where the
+// quotient is its limit 0.
+__device__ __forceinline__ float sigmoidf(float z) { return 1.0f / (1.0f + __expf(-z)); }
+
+// z * sigmoid(z); -inf gives the limit 0 rather than -inf * 0.
+__device__ __forceinline__ float silu(float z) { return z == -INFINITY ? 0.0f : z * sigmoidf(z); }
+
+__device__ __forceinline__ float silu_slope(float z)
+{
+    const float p = sigmoidf(z);
+    const float t = z * (1.0f - p);           // both limits are finite: 0 at +inf, p * t -> 0 at -inf
+    return fabsf(z) > 80.0f ? (z > 0.0f ? 1.0f : 0.0f) : p * (1.0f + t);
+}
+
+constexpr float kSqrtHalf = 0.70710678118654752f;
+constexpr float kInvSqrt2Pi = 0.39894228040143268f;
+
+__device__ __forceinline__ float gelu(float z)
+{
+    // erfc keeps the relative precision of the left tail, where 1 + erf cancels
+    return z == -INFINITY ? 0.0f : 0.5f * z * erfcf(-z * kSqrtHalf);
+}
+
+__device__ __forceinline__ float gelu_slope(float z)
+{
+    if (fabsf(z) > 15.0f)
+        return z > 0.0f ? 1.0f : 0.0f;
+    return 0.5f * erfcf(-z * kSqrtHalf) + z * kInvSqrt2Pi * __expf(-0.5f * z * z);
+}
+
+// C columns n .. n + C - 1 of one row of the finished product (without bias).
+template <int C>
+__device__ __forceinline__ void emit(const Args &a, int e, int64_t row, int n, float (&z)[C])
+{
+    if (a.act == EPL_ACT_SWIGLU_GRAD) {
+        // saved [rows, 2 N]: gate, up; y likewise
+        float gate[C], up[C], dg[C], du[C];
+        const int64_t at = row * 2 * a.N + n;
+        load_bf16<C>(a.pre + at, gate);
+        load_bf16<C>(a.pre + at + a.N, up);
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            dg[i] = z[i] * up[i] * silu_slope(gate[i]);
+            du[i] = z[i] * silu(gate[i]);
+        }
+        store_out<C>(a, at, dg);
+        store_out<C>(a, at + a.N, du);
+        return;
+    }
+    const int64_t at = row * a.N + n;
+    if (a.act == EPL_ACT_SILU_GRAD || a.act == EPL_ACT_GELU_GRAD) {
+        float s[C];
+        load_bf16<C>(a.pre + at, s);
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+            z[i] *= a.act == EPL_ACT_SILU_GRAD ? silu_slope(s[i]) : gelu_slope(s[i]);
+        store_out<C>(a, at, z);
+        return;
+    }
+    if (a.bias) {
+        const float *b = a.bias + (int64_t)e * a.N + n;
+#pragma unroll
+        for (int i = 0; i < C; i += 4) {
+            const f32x4 v = *reinterpret_cast<const f32x4 *>(b + i);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                z[i + j] += v[j];
+        }
+    }
+    if (a.pre)
+        store_bf16<C>(a.pre + at, z);
+    if (a.act == EPL_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+            z[i] = silu(z[i]);
+    } else if (a.act == EPL_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+            z[i] = gelu(z[i]);
+    }
+    if (a.residual) {
+        float r[C];
+        load_bf16<C>(a.residual + at, r);
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+            z[i] += r[i];
+    }
+    store_out<C>(a, at, z);
+}
+
+// The gated activation: columns f .. f + C - 1 of the gate half and of the up half.
+template <int C>
+__device__ __forceinline__ void emit_pair(const Args &a, int e, int64_t row, int f, float (&g)[C],
+                                          float (&u)[C])
+{
+    const int F = a.N / 2;
+    if (a.bias) {
+        const float *b = a.bias + (int64_t)e * a.N + f;
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            g[i] += b[i];
+            u[i] += b[F + i];
+        }
+    }
+    if (a.pre) {
+        store_bf16<C>(a.pre + row * a.N + f, g);
+        store_bf16<C>(a.pre + row * a.N + F + f, u);
+    }
+    float v[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+        v[i] = silu(g[i]) * u[i];
+    if (a.residual) {
+        float r[C];
+        load_bf16<C>(a.residual + row * F + f, r);
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+            v[i] += r[i];
+    }
+    store_out<C>(a, row * F + f, v);
+}
+
+// ----------------------------------------------------------- tile kernel --
+//
+// A workgroup of 8 waves computes BM x BN outputs, 64 deep at a time, from
+// two LDS stages that buffer loads fill directly (16 bytes a lane) while the
+// other stage is multiplied. Q is the matrix instruction's A operand and P
+// its B operand, so a lane's accumulator registers run along n, the
+// contiguous index of the output: with the rows of Q taken in the order
+//     n(r, j) = (r / 4) * 16 + j * 4 + r % 4      (r: lane % 16, j: 0 .. 3)
+// the 16 values of a lane are 16 neighbouring columns, and a row leaves as
+// 128 contiguous bytes of bf16 without a pass through LDS.
+//
+// LDS layouts (XOR swizzles on 16-byte pieces so that the 16 lanes of a read
+// fall on different banks; a DMA writes LDS in lane order, so the swizzle is
+// applied to the global address that the lane reads):
+//   contiguous operand: [rows][64], piece c of row r at c ^ f(r)
+//   strided operand:    [64][cols], piece c of row k at c ^ g(k), read with
+//                       ds_read_b64_tr_b16, which hands lane r column r of a
+//                       4-row block, 4 consecutive k
+
+__device__ __forceinline__ int swz_p(int row) { return (row >> 1) & 7; }
+__device__ __forceinline__ int swz_q(int row) { return ((row >> 1) & 1) | (((row >> 4) & 3) << 1); }
+__device__ __forceinline__ int swz_pt(int k) { return ((k & 3) << 1) | (((k >> 3) & 1) << 3); }
+__device__ __forceinline__ int swz_qt(int k) { return (k & 1) | (((k >> 1) & 1) << 3); }
+
+// Where a lane's 16-byte pieces of one operand lie: the byte offset of its
+// piece of DMA number 0, and the step from one DMA (8 KB of LDS) to the next.
+struct Piece {
+    uint32_t off, step;
+    int k;            // contraction index of the piece within a stage
+};
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void *base, int64_t bytes)
+{
+    const int n = bytes <= 0 ? 0 : bytes > 0x7fffffff ? 0x7fffffff : (int)bytes;
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, n, 0x00020000);
+}
+
+// `ISSUES` DMAs of 16 bytes a lane into lds + wave * 1 KB. A lane whose
+// offset lies beyond the descriptor's bytes gets zeros.
+template <int ISSUES>
+__device__ __forceinline__ void dma(__amdgpu_buffer_rsrc_t r, uint16_t *lds, int wave,
+                                    const uint32_t (&off)[ISSUES], uint32_t outside)
+{
+#pragma unroll
+    for (int i = 0; i < ISSUES; ++i)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)(lds + i * 4096 + wave * 512), 16,
+                                                 (int)(off[i] | outside), 0, 0, 0);
+}
+
+enum Form { kForward, kDataGrad, kWeightGrad };
+
+// The m tiles of the experts before each expert, for experts in LDS order.
+template <int BM>
+__device__ __forceinline__ void tile_prefix(const Args &a, int32_t *pre, int32_t *sums)
+{
+    constexpr int per = kMaxExperts / kTileThreads;
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    int n[per], own = 0;
+#pragma unroll
+    for (int i = 0; i < per; ++i) {
+        const int e = t * per + i;
+        int64_t lo;
+        n[i] = e < a.E ? (block_of(a, e, lo) + BM - 1) / BM : 0;
+        own += n[i];
+    }
+    int up = own;
+    for (int d = 1; d < 64; d <<= 1) {
+        const int v = __shfl_up(up, d);
+        up += lane >= d ? v : 0;
+    }
+    if (lane == 63)
+        sums[wave] = up;
+    __syncthreads();
+    int before = up - own;
+    for (int w = 0; w < wave; ++w)
+        before += sums[w];
+#pragma unroll
+    for (int i = 0; i < per; ++i) {
+        const int e = t * per + i;
+        if (e <= a.E)
+            pre[e] = before;
+        before += n[i];
+    }
+    if (t == kTileThreads - 1 && a.E == kMaxExperts)
+        pre[a.E] = before;
+    __syncthreads();
+}
+
+template <int BM, int BN, Form FORM>
+__global__ __launch_bounds__(kTileThreads) void tile_kernel(Args a)
+{
+    constexpr bool PT = FORM == kWeightGrad;             // P strided
+    constexpr bool QT = FORM != kForward;                // Q strided
+    constexpr int WN = BN / 64, WM = 8 / WN;             // waves along n and m
+    constexpr int IP = BM / WM / 16;                     // 16-row pieces of P a wave
+    constexpr int ISP = BM / 64, ISQ = BN / 64;          // DMAs a stage
+    __shared__ __align__(1024) uint16_t sp0[BM * kTileK], sp1[BM * kTileK];
+    __shared__ __align__(1024) uint16_t sq0[BN * kTileK], sq1[BN * kTileK];
+    __shared__ int32_t pre[FORM == kWeightGrad ? 1 : kMaxExperts + 1];
+    __shared__ int32_t sums[8];
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / WN, wn = wave % WN, r = lane & 15, q = lane >> 4;
+    const bool paired = a.act == EPL_ACT_SWIGLU;
+
+    // tiles along m and n, over all experts
+    const int ntn = FORM == kWeightGrad ? (a.K + BN - 1) / BN : (a.N + BN - 1) / BN;
+    int ntm = 0;
+    int64_t total;
+    if (FORM == kWeightGrad) {
+        ntm = (a.N + BM - 1) / BM;
+        total = (int64_t)a.E * ntm * ntn;
+    } else {
+        tile_prefix<BM>(a, pre, sums);
+        total = (int64_t)pre[a.E] * ntn;
+    }
+
+    // workgroups of one XCD (every eighth) take neighbouring tiles
+    const int64_t grid = gridDim.x;
+    int64_t first = blockIdx.x;
+    if (grid % kNumXcd == 0)
+        first = (first % kNumXcd) * (grid / kNumXcd) + first / kNumXcd;
+
+    for (int64_t t = first; t < total; t += grid) {
+        int e;
+        int64_t lo;
+        int cnt, tm, ntm_e;
+        int64_t in_e;
+        if (FORM == kWeightGrad) {
+            e = (int)(t / ((int64_t)ntm * ntn));
+            in_e = t - (int64_t)e * ntm * ntn;
+            ntm_e = ntm;
+        } else {
+            int l = 0, h = a.E;                 // last expert with pre[e] * ntn <= t
+            while (h - l > 1) {
+                const int mid = (l + h) >> 1;
+                if ((int64_t)pre[mid] * ntn <= t)
+                    l = mid;
+                else
+                    h = mid;
+            }
+            e = __builtin_amdgcn_readfirstlane(l);
+            in_e = t - (int64_t)__builtin_amdgcn_readfirstlane(pre[e]) * ntn;
+            ntm_e = __builtin_amdgcn_readfirstlane(pre[e + 1]) - __builtin_amdgcn_readfirstlane(pre[e]);
+        }
+        cnt = block_of(a, e, lo);
+        // within an expert: bands of up to 8 m tiles, m fastest, so that the
+        // tiles in flight on an XCD share both operands in its L2
+        const int band = (int)(in_e / (8 * (int64_t)ntn));
+        const int bh = min(8, ntm_e - band * 8);
+        const int rest = (int)(in_e - (int64_t)band * 8 * ntn);
+        tm = band * 8 + rest % bh;
+        const int tn = rest / bh;
+
+        // operands: base, bytes, and the lane's pieces
+        const int depth = FORM == kWeightGrad ? cnt : a.K;
+        const int steps = (depth + kTileK - 1) / kTileK;
+        uint32_t op[ISP], oq[ISQ];
+        int kp, kq;                          // contraction index of the lane's pieces
+        const __bf16 *bp, *bq;
+        int64_t np, nq;                      // bytes from the base to the operand's end
+        int64_t sp, sq;                      // base step a stage, in bytes
+        if (PT) {
+            const int cols = a.N;
+            const int kk = (tid * 8) / BM, c = (tid * 8 % BM) / 8;
+#pragma unroll
+            for (int i = 0; i < ISP; ++i) {
+                const int k = kk + i * (4096 / BM);
+                op[i] = (uint32_t)k * cols * 2 + (tm * BM + (c ^ swz_pt(k)) * 8) * 2;
+            }
+            kp = 0;
+            bp = a.p + lo * cols;
+            np = (int64_t)cnt * cols * 2;
+            sp = (int64_t)kTileK * cols * 2;
+        } else {
+            const int row = tid >> 3, c = (tid & 7) ^ swz_p(row);
+#pragma unroll
+            for (int i = 0; i < ISP; ++i)
+                op[i] = (uint32_t)(row + i * 64) * a.K * 2 + c * 16;
+            kp = c * 8;
+            bp = a.p + (lo + (int64_t)tm * BM) * a.K;
+            np = (int64_t)(cnt - tm * BM) * a.K * 2;
+            sp = kTileK * 2;
+        }
+        if (QT) {
+            const int cols = FORM == kWeightGrad ? a.K : a.N;
+            const int kk = (tid * 8) / BN, c = (tid * 8 % BN) / 8;
+#pragma unroll
+            for (int i = 0; i < ISQ; ++i) {
+                const int k = kk + i * (4096 / BN), cc = c ^ swz_qt(k);
+                const int col = paired ? tn * (BN / 2) + (cc >> 1) * 8 + (cc & 1) * (a.N / 2)
+                                       : tn * BN + cc * 8;
+                oq[i] = ((uint32_t)k * cols + col) * 2;
+            }
+            kq = 0;
+            bq = FORM == kWeightGrad ? a.q + lo * cols : a.q + (int64_t)e * a.K * a.N;
+            nq = (int64_t)depth * cols * 2;
+            sq = (int64_t)kTileK * cols * 2;
+        } else {
+            const int row = tid >> 3, c = (tid & 7) ^ swz_q(row);
+#pragma unroll
+            for (int i = 0; i < ISQ; ++i) {
+                const int n = row + i * 64;
+                const int g = paired ? tn * (BN / 2) + (n >> 4) * 8 + (n & 7) + (n & 8 ? a.N / 2 : 0)
+                                     : tn * BN + n;
+                oq[i] = ((uint32_t)g * a.K + c * 8) * 2;
+            }
+            kq = c * 8;
+            bq = a.q + (int64_t)e * a.K * a.N;
+            nq = (int64_t)a.N * a.K * 2;
+            sq = kTileK * 2;
+        }
+
+        f32x4 acc[IP][4];
+#pragma unroll
+        for (int i = 0; i < IP; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                acc[i][j] = f32x4{0, 0, 0, 0};
+
+        auto fetch = [&](int s, uint16_t *lp, uint16_t *lq) {
+            // pieces past the contraction's end must read as zero: whole rows
+            // of a strided operand lie beyond its bytes, pieces of a
+            // contiguous one are pointed there
+            const int k0 = s * kTileK;
+            const uint32_t zp = !PT && k0 + kp >= depth ? 0x80000000u : 0u;
+            const uint32_t zq = !QT && k0 + kq >= depth ? 0x80000000u : 0u;
+            const char *gp = reinterpret_cast<const char *>(bp) + s * sp;
+            const char *gq = reinterpret_cast<const char *>(bq) + s * sq;
+            dma<ISP>(rsrc(gp, np - s * sp), lp, wave, op, zp);
+            dma<ISQ>(rsrc(gq, nq - s * sq), lq, wave, oq, zq);
+        };
+        auto multiply = [&](const uint16_t *lp, const uint16_t *lq) {
+#pragma unroll
+            for (int kb = 0; kb < kTileK / 32; ++kb) {
+                bf16x8 fq[4], fp[IP];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (QT) {
+                        s16x4 h[2];
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            const int k = kb * 32 + q * 8 + u * 4 + (r >> 2);
+                            const int c = (wn * 8 + (r & 3) * 2 + (j >> 1)) ^ swz_qt(k);
+                            h[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                (lds_s16x4 *)(lq + k * BN + c * 8 + (j & 1) * 4));
+                        }
+                        fq[j] = __builtin_bit_cast(
+                            bf16x8, __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
+                    } else {
+                        const int n = wn * 64 + (r >> 2) * 16 + j * 4 + (r & 3);
+                        const int c = (kb * 4 + q) ^ swz_q(n);
+                        fq[j] = *reinterpret_cast<const bf16x8 *>(lq + n * kTileK + c * 8);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < IP; ++i) {
+                    if (PT) {
+                        s16x4 h[2];
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            const int k = kb * 32 + q * 8 + u * 4 + (r >> 2);
+                            const int c = (wm * (BM / WM / 8) + i * 2 + ((r & 3) >> 1)) ^ swz_pt(k);
+                            h[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                (lds_s16x4 *)(lp + k * BM + c * 8 + (r & 1) * 4));
+                        }
+                        fp[i] = __builtin_bit_cast(
+                            bf16x8, __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
+                    } else {
+                        const int m = wm * (BM / WM) + i * 16 + r;
+                        const int c = (kb * 4 + q) ^ swz_p(m);
+                        fp[i] = *reinterpret_cast<const bf16x8 *>(lp + m * kTileK + c * 8);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < IP; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fq[j], fp[i], acc[i][j],
+                                                                            0, 0, 0);
+            }
+        };
+
+        if (steps > 0)
+            fetch(0, sp0, sq0);
+        __builtin_amdgcn_s_waitcnt(0);
+        __syncthreads();
+        for (int s = 0; s < steps; s += 2) {
+            if (s + 1 < steps)
+                fetch(s + 1, sp1, sq1);
+            multiply(sp0, sq0);
+            __builtin_amdgcn_s_waitcnt(0);
+            __syncthreads();
+            if (s + 1 >= steps)
+                break;
+            if (s + 2 < steps)
+                fetch(s + 2, sp0, sq0);
+            multiply(sp1, sq1);
+            __builtin_amdgcn_s_waitcnt(0);
+            __syncthreads();
+        }
+
+        // a lane's 16 columns of row m
+        const int n0 = wn * 64 + q * 16;
+#pragma unroll
+        for (int i = 0; i < IP; ++i) {
+            const int m = tm * BM + wm * (BM / WM) + i * 16 + r;
+            float v[2][8];
+#pragma unroll
+            for (int x = 0; x < 16; ++x)
+                v[x >> 3][x & 7] = acc[i][x >> 2][x & 3];
+            if (FORM == kWeightGrad) {
+                if (m >= a.N)
+                    continue;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int n = tn * BN + n0 + h * 8;
+                    if (n >= a.K)
+                        continue;
+                    const int64_t at = ((int64_t)e * a.N + m) * a.K + n;
+                    if (a.accumulate) {
+                        float old[8];
+                        if (a.out_f32) {
+#pragma unroll
+                            for (int x = 0; x < 8; ++x)
+                                old[x] = static_cast<const float *>(a.y)[at + x];
+                        } else {
+                            load_bf16<8>(static_cast<const __bf16 *>(a.y) + at, old);
+                        }
+#pragma unroll
+                        for (int x = 0; x < 8; ++x)
+                            v[h][x] += old[x];
+                    }
+                    store_out<8>(a, at, v[h]);
+                }
+            } else if (m < cnt) {
+                if (paired) {
+                    const int f = tn * (BN / 2) + n0 / 2;
+                    if (f < a.N / 2)
+                        emit_pair<8>(a, e, lo + m, f, v[0], v[1]);
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int n = tn * BN + n0 + h * 8;
+                        if (n < a.N)
+                            emit<8>(a, e, lo + m, n, v[h]);
+                    }
+                }
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------ few-rows kernel --
+//
+// For experts with a few rows the weights' bytes are the cost: each is read
+// once, straight into the registers of the matrix instruction. A workgroup
+// of 4 waves takes 32 columns of one expert; the waves share the contraction
+// (128 deep a turn each) and add their sums through LDS in wave order.
+
+constexpr int kFewThreads = 256;
+constexpr int kFewCols = 32;
+
+template <int MT>
+__device__ __forceinline__ void few_rows(const Args &a, int e, int64_t row0, int left, int nb,
+                                         float *red)
+{
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, q = lane >> 4;
+    const bool paired = a.act == EPL_ACT_SWIGLU;
+    const __bf16 *w = a.q + (int64_t)e * a.N * a.K;
+    const __bf16 *pw[2], *px[MT];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        // lane q holds 8 neighbouring columns, or 4 of the gate and the same 4 of the up half
+        int n = paired ? min(nb * 16 + r, a.N / 2 - 1) + j * (a.N / 2)
+                       : min(nb * 32 + (r >> 2) * 8 + j * 4 + (r & 3), a.N - 1);
+        pw[j] = w + (int64_t)n * a.K + q * 8;
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+        px[i] = a.p + (row0 + min(i * 16 + r, left - 1)) * a.K + q * 8;
+    f32x4 acc[MT][2];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+        acc[i][0] = acc[i][1] = f32x4{0, 0, 0, 0};
+
+    const bf16x8 zero = {};
+    for (int k0 = wave * 128; k0 < a.K; k0 += 512) {
+        bf16x8 fw[4][2], fx[4][MT];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int k = k0 + u * 32;
+            const bool in = k + q * 8 < a.K;
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                fw[u][j] = in ? *reinterpret_cast<const bf16x8 *>(pw[j] + k) : zero;
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+                fx[u][i] = in ? *reinterpret_cast<const bf16x8 *>(px[i] + k) : zero;
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fw[u][j], fx[u][i],
+                                                                        acc[i][j], 0, 0, 0);
+    }
+
+    __syncthreads();           // red may still be read for the rows before
+    f32x4 *mine = reinterpret_cast<f32x4 *>(red);
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            mine[((wave * MT + i) * 2 + j) * 64 + lane] = acc[i][j];
+    __syncthreads();
+    if (wave >= MT)
+        return;
+    f32x4 sum[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        sum[j] = mine[(wave * 2 + j) * 64 + lane];
+#pragma unroll
+        for (int v = 1; v < 4; ++v)
+            sum[j] += mine[((v * MT + wave) * 2 + j) * 64 + lane];
+    }
+    const int m = wave * 16 + r;
+    if (m >= left)
+        return;
+    if (paired) {
+        const int f = nb * 16 + q * 4;
+        float g[4], u[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            g[x] = sum[0][x], u[x] = sum[1][x];
+        if (f < a.N / 2)
+            emit_pair<4>(a, e, row0 + m, f, g, u);
+    } else {
+        const int n = nb * 32 + q * 8;
+        float v[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+            v[x] = sum[x >> 2][x & 3];
+        if (n < a.N)
+            emit<8>(a, e, row0 + m, n, v);
+    }
+}
+
+__global__ __launch_bounds__(kFewThreads) void few_rows_kernel(Args a)
+{
+    __shared__ __align__(16) float red[4 * 4 * 2 * 64 * 4];
+    const int e = blockIdx.y, nb = blockIdx.x;
+    int64_t lo;
+    const int cnt = block_of(a, e, lo);
+    for (int m = 0; m < cnt;) {
+        const int left = cnt - m;
+        if (left <= 16) {
+            few_rows<1>(a, e, lo + m, left, nb, red);
+            m += 16;
+        } else if (left <= 32) {
+            few_rows<2>(a, e, lo + m, left, nb, red);
+            m += 32;
+        } else {
+            few_rows<4>(a, e, lo + m, left, nb, red);
+            m += 64;
+        }
+    }
+}
+
+// --------------------------------------------------------- bias gradient --
+//
+// db[e, n] = sum over the expert's rows of d[p, n], in binary32. A workgroup
+// takes 64 columns (8 lanes of 8) of one expert; its 32 row lanes add rows
+// 32 apart and are added in order through LDS.
+
+constexpr int kBiasThreads = 256;
+
+__global__ __launch_bounds__(kBiasThreads) void bias_grad_kernel(Args a, float *db)
+{
+    __shared__ float red[32][65];
+    const int e = blockIdx.y, tid = threadIdx.x, c = tid & 7, y = tid >> 3;
+    const int n = blockIdx.x * 64 + c * 8;
+    int64_t lo;
+    const int cnt = block_of(a, e, lo);
+    float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (n < a.N) {
+        for (int m = y; m < cnt; m += 32) {
+            float v[8];
+            load_bf16<8>(a.p + (lo + m) * a.N + n, v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                s[i] += v[i];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        red[y][c * 8 + i] = s[i];
+    __syncthreads();
+    if (tid < 64 && (int)blockIdx.x * 64 + tid < a.N) {
+        float t = 0;
+        for (int i = 0; i < 32; ++i)
+            t += red[i][tid];
+        float *out = db + (int64_t)e * a.N + blockIdx.x * 64 + tid;
+        *out = a.accumulate ? *out + t : t;
+    }
+}
+
+}  // namespace epl_product

@@ -1,0 +1,636 @@
+// Device kernels of the router and its gradient for gfx950 (CDNA4): scores,
+// the choice of top-k experts (with a bias and groups), their weights; and
+// the gradient of the logits from the weights'.
+//
+// The choice needs an exact order, so every candidate is one binary64 key:
+// its choice score with the low 11 bits of the significand replaced by the
+// expert's index, such that of two equal scores the lower index has the
+// larger key. Keys are then all different, one v_max_f64 both compares and
+// carries the index, and the selection is a sorting network on registers.
+// Without a bias (and without sums of two) the score is the logit itself,
+// which orders the experts as any score does and leaves the low 29 bits of a
+// binary64 free: the order is exact. With them scores are computed in
+// binary64, to about 2^-44, and compared to 41 bits.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "epl.h"
+
+namespace epl_router_k {
+
+constexpr int kMaxExperts = 2048;
+constexpr int kMaxTopk = 64;
+constexpr int kMaxGroups = 64;
+constexpr int kThreads = 256;
+constexpr uint64_t kIndexMask = 2047;
+
+struct Args {
+    const void *logits;
+    const float *bias;             // [E] or null
+    const uint8_t *mask;           // [T] or null
+    int64_t *idx;                  // [T, K]
+    float *w;                      // [T, K]
+    int64_t T;
+    int K, E, G, topk_groups, group_top;
+    bool softmax, renorm, bf16, need_scores, vec;
+    float scale;
+};
+
+struct GradArgs {
+    const void *logits;
+    const int64_t *idx;
+    const float *g;                // [T, K] d weights
+    void *out;                     // [T, E] d logits
+    int64_t T;
+    int K, E;
+    bool softmax, renorm, bf16, vec;
+    float scale;
+};
+
+// exp(x) in binary64 to a few units of 2^-47: x = n ln 2 + r with |r| <=
+// ln 2 / 2 (ln 2 split in two words), the Taylor polynomial of degree 11 in
+// r (its remainder is below 2^-47), and an exponent shift.
+__device__ __forceinline__ double exp64(double x)
+{
+    x = fmin(fmax(x, -700.0), 700.0);
+    const double n = __builtin_rint(x * 1.4426950408889634074);
+    double r = fma(n, -6.93147180369123816490e-01, x);
+    r = fma(n, -1.90821492927058770002e-10, r);
+    double p = 1.0 / 39916800.0;
+    p = fma(p, r, 1.0 / 3628800.0);
+    p = fma(p, r, 1.0 / 362880.0);
+    p = fma(p, r, 1.0 / 40320.0);
+    p = fma(p, r, 1.0 / 5040.0);
+    p = fma(p, r, 1.0 / 720.0);
+    p = fma(p, r, 1.0 / 120.0);
+    p = fma(p, r, 1.0 / 24.0);
+    p = fma(p, r, 1.0 / 6.0);
+    p = fma(p, r, 0.5);
+    p = fma(p, r, 1.0);
+    p = fma(p, r, 1.0);
+    return __builtin_ldexp(p, (int)n);
+}
+
+// 1 / d for finite positive d: the hardware's estimate and two Newton steps.
+__device__ __forceinline__ double rcp64(double d)
+{
+    double y = __builtin_amdgcn_rcp(d);
+    y = fma(fma(-d, y, 1.0), y, y);
+    return fma(fma(-d, y, 1.0), y, y);
+}
+
+// 0 below -700, where exp64 stops growing.
+__device__ __forceinline__ double sigmoid64(double x)
+{
+    return x < -700.0 ? 0.0 : rcp64(1.0 + exp64(-x));
+}
+
+// +inf competes as the largest finite logit; a NaN stays one.
+__device__ __forceinline__ float no_inf(float v) { return v > 3.402823466e+38f ? 3.402823466e+38f : v; }
+
+__device__ __forceinline__ float load_logit(const void *p, bool bf16, int64_t at)
+{
+    return no_inf(bf16 ? (float)static_cast<const __bf16 *>(p)[at]
+                       : static_cast<const float *>(p)[at]);
+}
+
+// A key that may win: not -inf (no candidate).
+__device__ __forceinline__ double make_key(double score, int index)
+{
+    uint64_t u = __builtin_bit_cast(uint64_t, score + 0.0);      // -0 becomes +0
+    const uint64_t tail = (u >> 63) ? (uint64_t)index : kIndexMask - (uint64_t)index;
+    return __builtin_bit_cast(double, (u & ~kIndexMask) | tail);
+}
+
+__device__ __forceinline__ int key_index(double key)
+{
+    const uint64_t u = __builtin_bit_cast(uint64_t, key);
+    const int tail = (int)(u & kIndexMask);
+    return (u >> 63) ? tail : (int)kIndexMask - tail;
+}
+
+// Choice score of a logit, or -inf where the expert cannot be chosen. `m`
+// and `inv` are the row's largest logit and 1 / sum of exponentials.
+__device__ __forceinline__ double choice(const Args &a, float l, float bias, double m, double inv)
+{
+    const bool out = !(l > -INFINITY) || !(bias > -INFINITY);
+    if (!a.need_scores)
+        return out ? -INFINITY : (double)l;
+    const double s = a.softmax ? exp64((double)l - m) * inv : sigmoid64((double)l);
+    return out ? -INFINITY : s + (double)no_inf(bias);
+}
+
+// ---- register sorting ------------------------------------------------------
+
+__device__ __forceinline__ void desc(double &a, double &b)
+{
+    const double hi = fmax(a, b), lo = fmin(a, b);
+    a = hi;
+    b = lo;
+}
+
+// Batcher's odd-even merge sort of 8 keys, descending (19 exchanges).
+__device__ __forceinline__ void sort8(double (&k)[8])
+{
+    desc(k[0], k[1]); desc(k[2], k[3]); desc(k[4], k[5]); desc(k[6], k[7]);
+    desc(k[0], k[2]); desc(k[1], k[3]); desc(k[4], k[6]); desc(k[5], k[7]);
+    desc(k[1], k[2]); desc(k[5], k[6]);
+    desc(k[0], k[4]); desc(k[1], k[5]); desc(k[2], k[6]); desc(k[3], k[7]);
+    desc(k[2], k[4]); desc(k[3], k[5]);
+    desc(k[1], k[2]); desc(k[3], k[4]); desc(k[5], k[6]);
+}
+
+// The 8 largest of two descending lists, descending: the larger of a[i] and
+// b[7 - i] over i is a bitonic sequence of the 8 largest.
+__device__ __forceinline__ void merge8(double (&a)[8], const double (&b)[8])
+{
+    double c[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        c[i] = fmax(a[i], b[7 - i]);
+#pragma unroll
+    for (int d = 4; d > 0; d >>= 1)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (!(i & d))
+                desc(c[i], c[i + d]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        a[i] = c[i];
+}
+
+// The value of the lane `D` away (the lane number's bit D flipped, for lists
+// that are alike within blocks of D lanes): DPP moves within 16 lanes, a
+// permute above.
+template <int D>
+__device__ __forceinline__ int lane_swap(int v)
+{
+    if constexpr (D == 1)
+        return __builtin_amdgcn_mov_dpp(v, 0xB1, 0xF, 0xF, true);          // quad_perm 1 0 3 2
+    else if constexpr (D == 2)
+        return __builtin_amdgcn_mov_dpp(v, 0x4E, 0xF, 0xF, true);          // quad_perm 2 3 0 1
+    else if constexpr (D == 4)
+        return __builtin_amdgcn_mov_dpp(v, 0x141, 0xF, 0xF, true);         // row_half_mirror
+    else if constexpr (D == 8)
+        return __builtin_amdgcn_mov_dpp(v, 0x140, 0xF, 0xF, true);         // row_mirror
+    else
+        return __shfl_xor(v, D);
+}
+template <int D>
+__device__ __forceinline__ float lane_swap(float v)
+{
+    return __builtin_bit_cast(float, lane_swap<D>(__builtin_bit_cast(int, v)));
+}
+template <int D>
+__device__ __forceinline__ double lane_swap(double v)
+{
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)lane_swap<D>((int)(uint32_t)u);
+    const uint32_t hi = (uint32_t)lane_swap<D>((int)(uint32_t)(u >> 32));
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+
+// f(v, v of the other half) over blocks of L lanes: all lanes get the same.
+template <int L, int D = 1, typename V, typename F>
+__device__ __forceinline__ V all_lanes(V v, F f)
+{
+    if constexpr (D < L)
+        return all_lanes<L, D * 2>(f(v, lane_swap<D>(v)), f);
+    else
+        return v;
+}
+template <int L, typename V>
+__device__ __forceinline__ V lane_max(V v)
+{
+    return all_lanes<L>(v, [](V a, V b) { return a > b ? a : b; });
+}
+template <int L, typename V>
+__device__ __forceinline__ V lane_sum(V v)
+{
+    return all_lanes<L>(v, [](V a, V b) { return a + b; });
+}
+
+template <int L, int D = 1>
+__device__ __forceinline__ void merge_lanes(double (&k)[8])
+{
+    if constexpr (D < L) {
+        double o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            o[i] = lane_swap<D>(k[i]);
+        merge8(k, o);
+        merge_lanes<L, D * 2>(k);
+    }
+}
+
+__device__ __forceinline__ void two_best(double &a, double &b, double c, double d)
+{
+    const double lo = fmin(a, c);
+    a = fmax(a, c);
+    b = fmax(lo, fmax(b, d));
+}
+
+// Group score from its two best keys: a group of one candidate has that one.
+__device__ __forceinline__ double group_score(const Args &a, double best, double next)
+{
+    return a.group_top == 2 && next > -INFINITY ? best + next : best;
+}
+
+// Logits of 8 neighbouring experts; -inf past the row's end.
+__device__ __forceinline__ void load8(const void *p, bool bf16, bool vec, int64_t row, int E, int e0,
+                                      float (&v)[8])
+{
+    const int64_t at = row * E + e0;
+    if (vec && e0 + 8 <= E) {
+        if (bf16) {
+            typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+            const bf16x8 r = *reinterpret_cast<const bf16x8 *>(static_cast<const __bf16 *>(p) + at);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] = no_inf((float)r[i]);
+        } else {
+            const float4 x = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + at);
+            const float4 y = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + at + 4);
+            const float t[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] = no_inf(t[i]);
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        v[i] = e0 + i < E ? load_logit(p, bf16, at + i) : -INFINITY;
+}
+
+// A logit that takes part: NaN counts as -inf.
+__device__ __forceinline__ float usable(float l) { return l > -INFINITY ? l : -INFINITY; }
+
+// Weights of the chosen experts in lanes k = 0 .. K - 1 of a block of at
+// least K lanes: `l` is the chosen logit (-inf: no expert).
+template <int L>
+__device__ __forceinline__ float weight_of(const Args &a, float l, double m, double inv)
+{
+    double s;
+    if (a.softmax) {
+        // the row's sum drops out of renormalised weights: the chosen
+        // logits' own maximum keeps their ratios from underflowing
+        const double top = a.renorm ? (double)lane_max<L>(l) : m;
+        s = l > -INFINITY ? exp64((double)l - top) : 0.0;
+        if (!a.renorm)
+            s *= inv;
+    } else {
+        s = l > -INFINITY ? sigmoid64((double)l) : 0.0;
+    }
+    if (a.renorm) {
+        const double d = lane_sum<L>(s);
+        s = d > 0.0 ? s / d : 0.0;
+    }
+    return (float)(s * (double)a.scale);
+}
+
+// ---- top-k of at most 8, L lanes a token, CH pieces of 8 experts a lane ----
+//
+// Piece c of lane i holds experts (c L + i) 8 .. + 7. Each lane sorts its
+// pieces, merges them to its 8 best, and log2(L) merges across lanes leave
+// the token's 8 best, in order, in every lane. Bound by its vector
+// instructions: about 50 binary64 maxima and minima a token at L = 8.
+template <int L, int CH>
+__global__ __launch_bounds__(kThreads) void route_kernel(Args a)
+{
+    __shared__ double groups[kThreads / L][kMaxGroups + 1];
+    const int lane = threadIdx.x % L, slot = threadIdx.x / L;
+    const int64_t t = (int64_t)blockIdx.x * (kThreads / L) + slot;
+    const bool in = t < a.T;
+    const int64_t row = in ? t : a.T - 1;
+
+    float l[CH][8];
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+        load8(a.logits, a.bf16, a.vec, row, a.E, (c * L + lane) * 8, l[c]);
+
+    double m = 0.0, inv = 1.0;
+    if (a.softmax && (a.need_scores || !a.renorm)) {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                mx = fmaxf(mx, usable(l[c][i]));
+        mx = lane_max<L>(mx);
+        m = mx > -INFINITY ? (double)mx : 0.0;
+        if (a.need_scores) {
+            double s = 0.0;
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    s += l[c][i] > -INFINITY ? exp64((double)l[c][i] - m) : 0.0;
+            s = lane_sum<L>(s);
+            inv = s > 0.0 ? rcp64(s) : 0.0;
+        } else {
+            float s = 0.0f;
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    s += l[c][i] > -INFINITY ? __expf(l[c][i] - (float)m) : 0.0f;
+            s = lane_sum<L>(s);
+            inv = s > 0.0f ? 1.0 / (double)s : 0.0;
+        }
+    }
+
+    double best[8];
+    double key[CH][8];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int e = (c * L + lane) * 8 + i;
+            const double s = choice(a, l[c][i], a.bias && e < a.E ? a.bias[e] : 0.0f, m, inv);
+            key[c][i] = s > -INFINITY ? make_key(s, e) : -INFINITY;
+        }
+        sort8(key[c]);
+    }
+    if (a.G > 1) {
+        // pieces lie within groups of `per` pieces (a power of two): the two
+        // best keys of a group by exchanges, its score and those of the
+        // token's other groups from LDS
+        const int per = a.E / a.G / 8;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            double x = key[c][0], y = key[c][1];
+            if (per > 1) { two_best(x, y, lane_swap<1>(x), lane_swap<1>(y)); }
+            if (per > 2) { two_best(x, y, lane_swap<2>(x), lane_swap<2>(y)); }
+            if constexpr (L > 4)
+                if (per > 4) { two_best(x, y, lane_swap<4>(x), lane_swap<4>(y)); }
+            if constexpr (L > 8)
+                if (per > 8) { two_best(x, y, lane_swap<8>(x), lane_swap<8>(y)); }
+            if constexpr (L > 16)
+                if (per > 16) { two_best(x, y, lane_swap<16>(x), lane_swap<16>(y)); }
+            if constexpr (L > 32)
+                if (per > 32) { two_best(x, y, lane_swap<32>(x), lane_swap<32>(y)); }
+            const int piece = c * L + lane;
+            if (piece % per == 0 && piece / per < a.G)
+                groups[slot][piece / per] = group_score(a, x, y);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int g = min((c * L + lane) / per, a.G - 1);
+            const double own = groups[slot][g];
+            int before = 0;
+            for (int o = 0; o < a.G; ++o) {
+                const double s = groups[slot][o];
+                before += s > own || (s == own && o < g) ? 1 : 0;
+            }
+            if (before >= a.topk_groups)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    key[c][i] = -INFINITY;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        best[i] = key[0][i];
+#pragma unroll
+    for (int c = 1; c < CH; ++c)
+        merge8(best, key[c]);
+    merge_lanes<L>(best);
+
+    // lane k keeps the k-th best
+    double mine = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        mine = lane == i ? best[i] : mine;
+    const bool live = in && lane < a.K && (!a.mask || a.mask[row] != 0);
+    const bool found = live && mine > -INFINITY;
+    const int e = found ? key_index(mine) : -1;
+    const float chosen = found ? load_logit(a.logits, a.bf16, row * a.E + e) : -INFINITY;
+    const float w = weight_of<L>(a, chosen, m, inv);
+    if (in && lane < a.K) {
+        a.idx[t * a.K + lane] = e;
+        a.w[t * a.K + lane] = found ? w : 0.0f;
+    }
+}
+
+// ---- any top-k, any groups: a wave a token, its keys in LDS ----------------
+//
+// K rounds, each the largest key below the last round's. For sizes that the
+// kernel above does not cover (K above 8, groups that end inside a piece).
+__global__ __launch_bounds__(64) void route_any_kernel(Args a)
+{
+    __shared__ double key[kMaxExperts];
+    __shared__ double score[kMaxGroups];
+    __shared__ int kept[kMaxTopk];
+    const int lane = threadIdx.x;
+    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+        double m = 0.0, inv = 1.0;
+        if (a.softmax) {
+            float mx = -INFINITY;
+            for (int e = lane; e < a.E; e += 64)
+                mx = fmaxf(mx, usable(load_logit(a.logits, a.bf16, t * a.E + e)));
+            mx = lane_max<64>(mx);
+            m = mx > -INFINITY ? (double)mx : 0.0;
+            double s = 0.0;
+            for (int e = lane; e < a.E; e += 64) {
+                const float l = load_logit(a.logits, a.bf16, t * a.E + e);
+                s += l > -INFINITY ? exp64((double)l - m) : 0.0;
+            }
+            s = lane_sum<64>(s);
+            inv = s > 0.0 ? 1.0 / s : 0.0;
+        }
+        for (int e = lane; e < a.E; e += 64) {
+            const double s = choice(a, load_logit(a.logits, a.bf16, t * a.E + e),
+                                    a.bias ? a.bias[e] : 0.0f, m, inv);
+            key[e] = s > -INFINITY ? make_key(s, e) : -INFINITY;
+        }
+        __syncthreads();
+        if (a.G > 1) {
+            const int size = a.E / a.G;
+            if (lane < a.G) {
+                double x = -INFINITY, y = -INFINITY;
+                for (int i = 0; i < size; ++i)
+                    two_best(x, y, key[lane * size + i], -INFINITY);
+                score[lane] = group_score(a, x, y);
+            }
+            __syncthreads();
+            bool gone = false;
+            if (lane < a.G) {
+                int before = 0;
+                for (int o = 0; o < a.G; ++o)
+                    before += score[o] > score[lane] || (score[o] == score[lane] && o < lane) ? 1 : 0;
+                gone = before >= a.topk_groups;
+            }
+            if (gone)
+                for (int i = 0; i < size; ++i)
+                    key[lane * size + i] = -INFINITY;
+            __syncthreads();
+        }
+        const bool live = !a.mask || a.mask[t] != 0;
+        double last = INFINITY;
+        for (int k = 0; k < a.K; ++k) {
+            double x = -INFINITY;
+            for (int e = lane; e < a.E; e += 64) {
+                const double v = key[e];
+                x = v < last && v > x ? v : x;
+            }
+            last = lane_max<64>(x);
+            if (lane == k)
+                kept[k] = live && last > -INFINITY ? key_index(last) : -1;
+        }
+        __syncthreads();
+        const int e = lane < a.K ? kept[lane] : -1;
+        const float l = e >= 0 ? load_logit(a.logits, a.bf16, t * a.E + e) : -INFINITY;
+        const float w = weight_of<64>(a, l, m, inv);
+        if (lane < a.K) {
+            a.idx[t * a.K + lane] = e;
+            a.w[t * a.K + lane] = e >= 0 ? w : 0.0f;
+        }
+        __syncthreads();
+    }
+}
+
+// ---- gradient of the logits ------------------------------------------------
+//
+// With p the scores, chosen experts i_k, g_k = scale * d w_k:
+//   renormalised: h_k = g_k - sum_j (p_j / D) g_j over the chosen, D their sum
+//       softmax: d l_{i_k} = (p_k / D) h_k, zero elsewhere (the sum over all
+//                experts drops out of the ratios)
+//       sigmoid: d l_{i_k} = (p_k / D) (1 - p_k) h_k, zero elsewhere
+//   plain: sigmoid: d l_{i_k} = p_k (1 - p_k) g_k
+//          softmax: d l_i = p_i (d p_i - sum_j p_j d p_j) for every expert
+// Slots that name the same expert add up. L lanes a token: each lane makes a
+// share of the K slots' values, puts them in LDS, and writes its pieces of 8
+// experts by comparing their indices with the slots'.
+template <int L, int CH>
+__global__ __launch_bounds__(kThreads) void route_grad_kernel(GradArgs a)
+{
+    constexpr int TOK = kThreads / L;
+    __shared__ float val[TOK][kMaxTopk];
+    __shared__ int who[TOK][kMaxTopk];
+    const int lane = threadIdx.x % L, slot = threadIdx.x / L;
+    const int64_t t = (int64_t)blockIdx.x * TOK + slot;
+    const bool in = t < a.T;
+    const int64_t row = in ? t : a.T - 1;
+    const bool dense = a.softmax && !a.renorm;
+
+    float p[CH][8];
+    float m = 0.0f, inv = 0.0f;
+    if (dense) {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            load8(a.logits, a.bf16, a.vec, row, a.E, (c * L + lane) * 8, p[c]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                mx = fmaxf(mx, usable(p[c][i]));
+        }
+        mx = lane_max<L>(mx);
+        m = mx > -INFINITY ? mx : 0.0f;
+        float s = 0.0f;
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                p[c][i] = p[c][i] > -INFINITY ? __expf(p[c][i] - m) : 0.0f;
+                s += p[c][i];
+            }
+        s = lane_sum<L>(s);
+        inv = s > 0.0f ? 1.0f / s : 0.0f;
+    }
+
+    // the slots' logits, for the maximum of the chosen
+    float top = -INFINITY;
+    if (a.softmax && a.renorm) {
+        for (int k = lane; k < a.K; k += L) {
+            const int64_t e = a.idx[row * a.K + k];
+            if (e >= 0 && e < a.E)
+                top = fmaxf(top, usable(load_logit(a.logits, a.bf16, row * a.E + e)));
+        }
+        top = lane_max<L>(top);
+        top = top > -INFINITY ? top : 0.0f;
+    }
+    float sum = 0.0f, dot = 0.0f;
+    for (int k = lane; k < a.K; k += L) {
+        const int64_t e = a.idx[row * a.K + k];
+        const bool live = e >= 0 && e < a.E;
+        const float l = live ? load_logit(a.logits, a.bf16, row * a.E + e) : -INFINITY;
+        const float g = live ? a.g[row * a.K + k] * a.scale : 0.0f;
+        float s = 0.0f;
+        if (l > -INFINITY)
+            s = !a.softmax ? 1.0f / (1.0f + __expf(-l)) : dense ? __expf(l - m) * inv : __expf(l - top);
+        who[slot][k] = live ? (int)e : -1;
+        val[slot][k] = g;
+        sum += s;
+        dot += s * g;
+    }
+    sum = lane_sum<L>(sum);
+    dot = lane_sum<L>(dot);
+    const float over = a.renorm ? (sum > 0.0f ? 1.0f / sum : 0.0f) : 1.0f;
+    const float mean = a.renorm ? dot * over : 0.0f;
+    for (int k = lane; k < a.K; k += L) {
+        const int e = who[slot][k];
+        const float l = e >= 0 ? load_logit(a.logits, a.bf16, row * a.E + e) : -INFINITY;
+        float d = 0.0f;
+        if (l > -INFINITY) {
+            const float h = (val[slot][k] - mean) * over;
+            if (dense) {
+                d = h;
+            } else if (a.softmax) {
+                d = h * __expf(l - top);
+            } else {
+                const float s = 1.0f / (1.0f + __expf(-l));
+                d = h * s / (1.0f + __expf(l));             // 1 - s without cancellation
+            }
+        }
+        val[slot][k] = d;
+    }
+    __syncthreads();
+    if (!in)
+        return;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        const int e0 = (c * L + lane) * 8;
+        if (e0 >= a.E)
+            break;
+        float d[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        for (int k = 0; k < a.K; ++k) {
+            const int at = who[slot][k] - e0;
+            const float v = val[slot][k];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                d[i] += at == i ? v : 0.0f;
+        }
+        if (dense)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                d[i] = p[c][i] * inv * (d[i] - dot);
+        const int64_t at = t * a.E + e0;
+        if (a.vec && e0 + 8 <= a.E) {
+            if (a.bf16) {
+                typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+                bf16x8 r;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    r[i] = (__bf16)d[i];
+                *reinterpret_cast<bf16x8 *>(static_cast<__bf16 *>(a.out) + at) = r;
+            } else {
+                float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at);
+                o[0] = make_float4(d[0], d[1], d[2], d[3]);
+                o[1] = make_float4(d[4], d[5], d[6], d[7]);
+            }
+        } else {
+            for (int i = 0; i < 8 && e0 + i < a.E; ++i) {
+                if (a.bf16)
+                    static_cast<__bf16 *>(a.out)[at + i] = (__bf16)d[i];
+                else
+                    static_cast<float *>(a.out)[at + i] = d[i];
+            }
+        }
+    }
+}
+
+}  // namespace epl_router_k
