@@ -15,6 +15,9 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+#include <utility>
+
 #include "epl.h"
 
 namespace epl_product {
@@ -47,6 +50,19 @@ struct Args {
     int out_f32;
     int accumulate;           // weight gradient: add to y
 };
+
+// f(0), f(1), .. f(N - 1) with the index a constant from the start: an array
+// of 128 accumulators indexed by an unrolled loop stays in scratch memory.
+template <typename F, int... I>
+__device__ __forceinline__ void each_of(F &&f, std::integer_sequence<int, I...>)
+{
+    (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void each(F &&f)
+{
+    each_of(f, std::make_integer_sequence<int, N>{});
+}
 
 // An expert's block, cut to the buffer: [lo, lo + n).
 __device__ __forceinline__ int block_of(const Args &a, int e, int64_t &lo)
@@ -217,6 +233,26 @@ __device__ __forceinline__ void emit_pair(const Args &a, int e, int64_t row, int
     store_out<C>(a, row * F + f, v);
 }
 
+// C neighbouring elements of a weight gradient.
+template <int C>
+__device__ __forceinline__ void emit_weight(const Args &a, int64_t at, float (&v)[C])
+{
+    if (a.accumulate) {
+        float old[C];
+        if (a.out_f32) {
+#pragma unroll
+            for (int x = 0; x < C; ++x)
+                old[x] = static_cast<const float *>(a.y)[at + x];
+        } else {
+            load_bf16<C>(static_cast<const __bf16 *>(a.y) + at, old);
+        }
+#pragma unroll
+        for (int x = 0; x < C; ++x)
+            v[x] += old[x];
+    }
+    store_out<C>(a, at, v);
+}
+
 // ----------------------------------------------------------- tile kernel --
 //
 // A workgroup of 8 waves computes BM x BN outputs, 64 deep at a time, from
@@ -241,29 +277,36 @@ __device__ __forceinline__ int swz_q(int row) { return ((row >> 1) & 1) | (((row
 __device__ __forceinline__ int swz_pt(int k) { return ((k & 3) << 1) | (((k >> 3) & 1) << 3); }
 __device__ __forceinline__ int swz_qt(int k) { return (k & 1) | (((k >> 1) & 1) << 3); }
 
-// Where a lane's 16-byte pieces of one operand lie: the byte offset of its
-// piece of DMA number 0, and the step from one DMA (8 KB of LDS) to the next.
-struct Piece {
-    uint32_t off, step;
-    int k;            // contraction index of the piece within a stage
-};
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void *base, int64_t bytes)
+// A buffer descriptor of `bytes` bytes from `base`: a lane that reads beyond
+// them gets zeros.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const char *base, int64_t bytes)
 {
     const int n = bytes <= 0 ? 0 : bytes > 0x7fffffff ? 0x7fffffff : (int)bytes;
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, n, 0x00020000);
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(base), 0, n, 0x00020000);
 }
 
-// `ISSUES` DMAs of 16 bytes a lane into lds + wave * 1 KB. A lane whose
-// offset lies beyond the descriptor's bytes gets zeros.
+// One operand's stage: ISSUES DMAs of 16 bytes a lane, each filling 8 KB of
+// LDS (wave w the w-th KB), `step` bytes apart in memory. `off` is the lane's
+// offset in each; the descriptors move, so one register serves all of them.
 template <int ISSUES>
-__device__ __forceinline__ void dma(__amdgpu_buffer_rsrc_t r, uint16_t *lds, int wave,
-                                    const uint32_t (&off)[ISSUES], uint32_t outside)
+__device__ __forceinline__ void dma(const char *base, int64_t bytes, int64_t step, uint32_t off,
+                                    uint16_t *lds, int wave)
 {
 #pragma unroll
     for (int i = 0; i < ISSUES; ++i)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)(lds + i * 4096 + wave * 512), 16,
-                                                 (int)(off[i] | outside), 0, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc(base + i * step, bytes - i * step),
+                                                 (lds_void *)(lds + i * 4096 + wave * 512), 16,
+                                                 (int)off, 0, 0, 0);
+}
+
+// 8 consecutive k of one column from a strided operand's stage [64][COLS]:
+// two 4-row transposing reads.
+template <int COLS>
+__device__ __forceinline__ bf16x8 read_tr(const uint16_t *at)
+{
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)at);
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(at + 4 * COLS));
+    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
 enum Form { kForward, kDataGrad, kWeightGrad };
@@ -323,6 +366,21 @@ __global__ __launch_bounds__(kTileThreads) void tile_kernel(Args a)
     const int wm = wave / WN, wn = wave % WN, r = lane & 15, q = lane >> 4;
     const bool paired = a.act == EPL_ACT_SWIGLU;
 
+    // The lane's LDS offsets (elements) of its first pieces; the others lie at
+    // fixed distances, since the swizzles use none of the bits that j, i, and
+    // (for strided operands) the 32-deep half and u change. A strided Q has
+    // one offset for each piece of 8 columns, a strided P an exclusive or.
+    int aq[2], ap[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int n = wn * 64 + (r >> 2) * 16 + (r & 3), m = wm * (BM / WM) + r;
+        const int k = q * 8 + (r >> 2);
+        aq[h] = QT ? k * BN + ((wn * 8 + (r & 3) * 2 + h) ^ swz_qt(k)) * 8
+                   : n * kTileK + ((h * 4 + q) ^ swz_q(n)) * 8;
+        ap[h] = PT ? k * BM + ((wm * (BM / WM / 8) + ((r & 3) >> 1)) ^ swz_pt(k)) * 8 + (r & 1) * 4
+                   : m * kTileK + ((h * 4 + q) ^ swz_p(m)) * 8;
+    }
+
     // tiles along m and n, over all experts
     const int ntn = FORM == kWeightGrad ? (a.K + BN - 1) / BN : (a.N + BN - 1) / BN;
     int ntm = 0;
@@ -372,71 +430,55 @@ __global__ __launch_bounds__(kTileThreads) void tile_kernel(Args a)
         tm = band * 8 + rest % bh;
         const int tn = rest / bh;
 
-        // operands: base, bytes, and the lane's pieces
+        // operands: base, bytes to their end, bytes between DMAs and between
+        // stages, and the lane's offset
         const int depth = FORM == kWeightGrad ? cnt : a.K;
         const int steps = (depth + kTileK - 1) / kTileK;
-        uint32_t op[ISP], oq[ISQ];
-        int kp, kq;                          // contraction index of the lane's pieces
-        const __bf16 *bp, *bq;
-        int64_t np, nq;                      // bytes from the base to the operand's end
-        int64_t sp, sq;                      // base step a stage, in bytes
+        const char *bp, *bq;
+        int64_t np, nq, ip, iq, sp, sq;
+        uint32_t op, oq;
+        int kp = 0, kq = 0;                  // contraction index of the lane's piece
         if (PT) {
-            const int cols = a.N;
-            const int kk = (tid * 8) / BM, c = (tid * 8 % BM) / 8;
-#pragma unroll
-            for (int i = 0; i < ISP; ++i) {
-                const int k = kk + i * (4096 / BM);
-                op[i] = (uint32_t)k * cols * 2 + (tm * BM + (c ^ swz_pt(k)) * 8) * 2;
-            }
-            kp = 0;
-            bp = a.p + lo * cols;
-            np = (int64_t)cnt * cols * 2;
-            sp = (int64_t)kTileK * cols * 2;
+            const int k = (tid * 8) / BM, c = ((tid * 8 % BM) / 8) ^ swz_pt(k);
+            op = ((uint32_t)k * a.N + tm * BM + c * 8) * 2;
+            bp = reinterpret_cast<const char *>(a.p + lo * a.N);
+            np = (int64_t)cnt * a.N * 2;
+            ip = (int64_t)(4096 / BM) * a.N * 2;
+            sp = (int64_t)kTileK * a.N * 2;
         } else {
             const int row = tid >> 3, c = (tid & 7) ^ swz_p(row);
-#pragma unroll
-            for (int i = 0; i < ISP; ++i)
-                op[i] = (uint32_t)(row + i * 64) * a.K * 2 + c * 16;
+            op = ((uint32_t)row * a.K + c * 8) * 2;
             kp = c * 8;
-            bp = a.p + (lo + (int64_t)tm * BM) * a.K;
+            bp = reinterpret_cast<const char *>(a.p + (lo + (int64_t)tm * BM) * a.K);
             np = (int64_t)(cnt - tm * BM) * a.K * 2;
+            ip = (int64_t)64 * a.K * 2;
             sp = kTileK * 2;
         }
         if (QT) {
             const int cols = FORM == kWeightGrad ? a.K : a.N;
-            const int kk = (tid * 8) / BN, c = (tid * 8 % BN) / 8;
-#pragma unroll
-            for (int i = 0; i < ISQ; ++i) {
-                const int k = kk + i * (4096 / BN), cc = c ^ swz_qt(k);
-                const int col = paired ? tn * (BN / 2) + (cc >> 1) * 8 + (cc & 1) * (a.N / 2)
-                                       : tn * BN + cc * 8;
-                oq[i] = ((uint32_t)k * cols + col) * 2;
-            }
-            kq = 0;
-            bq = FORM == kWeightGrad ? a.q + lo * cols : a.q + (int64_t)e * a.K * a.N;
+            const int k = (tid * 8) / BN, c = ((tid * 8 % BN) / 8) ^ swz_qt(k);
+            const int col = paired ? tn * (BN / 2) + (c >> 1) * 8 + (c & 1) * (a.N / 2)
+                                   : tn * BN + c * 8;
+            oq = ((uint32_t)k * cols + col) * 2;
+            bq = reinterpret_cast<const char *>(
+                FORM == kWeightGrad ? a.q + lo * cols : a.q + (int64_t)e * a.K * a.N);
             nq = (int64_t)depth * cols * 2;
+            iq = (int64_t)(4096 / BN) * cols * 2;
             sq = (int64_t)kTileK * cols * 2;
         } else {
             const int row = tid >> 3, c = (tid & 7) ^ swz_q(row);
-#pragma unroll
-            for (int i = 0; i < ISQ; ++i) {
-                const int n = row + i * 64;
-                const int g = paired ? tn * (BN / 2) + (n >> 4) * 8 + (n & 7) + (n & 8 ? a.N / 2 : 0)
-                                     : tn * BN + n;
-                oq[i] = ((uint32_t)g * a.K + c * 8) * 2;
-            }
+            const int n = paired ? tn * (BN / 2) + (row >> 4) * 8 + (row & 7) + (row & 8 ? a.N / 2 : 0)
+                                 : tn * BN + row;
+            oq = ((uint32_t)n * a.K + c * 8) * 2;
             kq = c * 8;
-            bq = a.q + (int64_t)e * a.K * a.N;
+            bq = reinterpret_cast<const char *>(a.q + (int64_t)e * a.K * a.N);
             nq = (int64_t)a.N * a.K * 2;
+            iq = (int64_t)(paired ? 32 : 64) * a.K * 2;
             sq = kTileK * 2;
         }
 
-        f32x4 acc[IP][4];
-#pragma unroll
-        for (int i = 0; i < IP; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                acc[i][j] = f32x4{0, 0, 0, 0};
+        f32x4 acc[IP * 4];
+        each<IP * 4>([&](auto i) { acc[i] = f32x4{0, 0, 0, 0}; });
 
         auto fetch = [&](int s, uint16_t *lp, uint16_t *lq) {
             // pieces past the contraction's end must read as zero: whole rows
@@ -445,128 +487,116 @@ __global__ __launch_bounds__(kTileThreads) void tile_kernel(Args a)
             const int k0 = s * kTileK;
             const uint32_t zp = !PT && k0 + kp >= depth ? 0x80000000u : 0u;
             const uint32_t zq = !QT && k0 + kq >= depth ? 0x80000000u : 0u;
-            const char *gp = reinterpret_cast<const char *>(bp) + s * sp;
-            const char *gq = reinterpret_cast<const char *>(bq) + s * sq;
-            dma<ISP>(rsrc(gp, np - s * sp), lp, wave, op, zp);
-            dma<ISQ>(rsrc(gq, nq - s * sq), lq, wave, oq, zq);
+            const char *gp = bp + s * sp, *gq = bq + s * sq;
+            dma<ISP>(gp, np - s * sp, ip, op | zp, lp, wave);
+            dma<ISQ>(gq, nq - s * sq, iq, oq | zq, lq, wave);
         };
         auto multiply = [&](const uint16_t *lp, const uint16_t *lq) {
 #pragma unroll
             for (int kb = 0; kb < kTileK / 32; ++kb) {
                 bf16x8 fq[4], fp[IP];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (QT) {
-                        s16x4 h[2];
-#pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            const int k = kb * 32 + q * 8 + u * 4 + (r >> 2);
-                            const int c = (wn * 8 + (r & 3) * 2 + (j >> 1)) ^ swz_qt(k);
-                            h[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                (lds_s16x4 *)(lq + k * BN + c * 8 + (j & 1) * 4));
-                        }
-                        fq[j] = __builtin_bit_cast(
-                            bf16x8, __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
-                    } else {
-                        const int n = wn * 64 + (r >> 2) * 16 + j * 4 + (r & 3);
-                        const int c = (kb * 4 + q) ^ swz_q(n);
-                        fq[j] = *reinterpret_cast<const bf16x8 *>(lq + n * kTileK + c * 8);
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < IP; ++i) {
-                    if (PT) {
-                        s16x4 h[2];
-#pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            const int k = kb * 32 + q * 8 + u * 4 + (r >> 2);
-                            const int c = (wm * (BM / WM / 8) + i * 2 + ((r & 3) >> 1)) ^ swz_pt(k);
-                            h[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                (lds_s16x4 *)(lp + k * BM + c * 8 + (r & 1) * 4));
-                        }
-                        fp[i] = __builtin_bit_cast(
-                            bf16x8, __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
-                    } else {
-                        const int m = wm * (BM / WM) + i * 16 + r;
-                        const int c = (kb * 4 + q) ^ swz_p(m);
-                        fp[i] = *reinterpret_cast<const bf16x8 *>(lp + m * kTileK + c * 8);
-                    }
-                }
+                for (int j = 0; j < 4; ++j)
+                    fq[j] = QT ? read_tr<BN>(lq + aq[j >> 1] + kb * 32 * BN + (j & 1) * 4)
+                               : *reinterpret_cast<const bf16x8 *>(lq + aq[kb] + j * 4 * kTileK);
 #pragma unroll
                 for (int i = 0; i < IP; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fq[j], fp[i], acc[i][j],
-                                                                            0, 0, 0);
+                    fp[i] = PT ? read_tr<BM>(lp + (ap[0] ^ (i * 16)) + kb * 32 * BM)
+                               : *reinterpret_cast<const bf16x8 *>(lp + ap[kb] + i * 16 * kTileK);
+                each<IP * 4>([&](auto x) {
+                    acc[x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fq[x % 4], fp[x / 4], acc[x],
+                                                                     0, 0, 0);
+                });
             }
         };
 
-        if (steps > 0)
+        // one step first where their number is odd, then pairs
+        auto turn = [&](int next, uint16_t *np_, uint16_t *nq_, const uint16_t *lp,
+                        const uint16_t *lq) {
+            if (next < steps)
+                fetch(next, np_, nq_);
+            multiply(lp, lq);
+            __builtin_amdgcn_s_waitcnt(0);
+            __syncthreads();
+        };
+        const int odd = steps & 1;
+        if (odd)
+            fetch(0, sp1, sq1);
+        else if (steps > 0)
             fetch(0, sp0, sq0);
         __builtin_amdgcn_s_waitcnt(0);
         __syncthreads();
-        for (int s = 0; s < steps; s += 2) {
-            if (s + 1 < steps)
-                fetch(s + 1, sp1, sq1);
-            multiply(sp0, sq0);
-            __builtin_amdgcn_s_waitcnt(0);
-            __syncthreads();
-            if (s + 1 >= steps)
-                break;
-            if (s + 2 < steps)
-                fetch(s + 2, sp0, sq0);
-            multiply(sp1, sq1);
-            __builtin_amdgcn_s_waitcnt(0);
-            __syncthreads();
+        if (odd)
+            turn(1, sp0, sq0, sp1, sq1);
+        for (int s = odd; s < steps; s += 2) {
+            turn(s + 1, sp1, sq1, sp0, sq0);
+            turn(s + 2, sp0, sq0, sp1, sq1);
         }
 
-        // a lane's 16 columns of row m
-        const int n0 = wn * 64 + q * 16;
-#pragma unroll
-        for (int i = 0; i < IP; ++i) {
-            const int m = tm * BM + wm * (BM / WM) + i * 16 + r;
-            float v[2][8];
-#pragma unroll
-            for (int x = 0; x < 16; ++x)
-                v[x >> 3][x & 7] = acc[i][x >> 2][x & 3];
-            if (FORM == kWeightGrad) {
+        if (FORM == kWeightGrad) {
+            // a lane's 16 columns of row m
+            each<IP>([&](auto i) {
+                const int m = tm * BM + wm * (BM / WM) + i * 16 + r;
                 if (m >= a.N)
-                    continue;
+                    return;
+                float v[2][8];
+                each<16>([&](auto x) { v[x / 8][x % 8] = acc[i * 4 + x / 4][x % 4]; });
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const int n = tn * BN + n0 + h * 8;
-                    if (n >= a.K)
-                        continue;
-                    const int64_t at = ((int64_t)e * a.N + m) * a.K + n;
-                    if (a.accumulate) {
-                        float old[8];
-                        if (a.out_f32) {
-#pragma unroll
-                            for (int x = 0; x < 8; ++x)
-                                old[x] = static_cast<const float *>(a.y)[at + x];
-                        } else {
-                            load_bf16<8>(static_cast<const __bf16 *>(a.y) + at, old);
-                        }
-#pragma unroll
-                        for (int x = 0; x < 8; ++x)
-                            v[h][x] += old[x];
-                    }
-                    store_out<8>(a, at, v[h]);
+                    const int n = tn * BN + wn * 64 + q * 16 + h * 8;
+                    if (n < a.K)
+                        emit_weight<8>(a, ((int64_t)e * a.N + m) * a.K + n, v[h]);
                 }
-            } else if (m < cnt) {
-                if (paired) {
-                    const int f = tn * (BN / 2) + n0 / 2;
-                    if (f < a.N / 2)
-                        emit_pair<8>(a, e, lo + m, f, v[0], v[1]);
-                } else {
+            });
+        } else {
+            // Two passes of half the wave's rows through its own part of the
+            // stages (16-byte pieces swizzled by row): a lane then has 8
+            // neighbouring columns and the epilogue's code is there once a
+            // pass, not once an accumulator (43 000 instructions otherwise).
+            constexpr int half = IP / 2 * 16;
+            uint16_t *const part = wave < 2 ? sp0 : wave < 4 ? sp1 : wave < 6 ? sq0 : sq1;
+            float *const mine = reinterpret_cast<float *>(part) + (wave & 1) * half * 64;
+            each<2>([&](auto h) {
+                each<IP / 2>([&](auto i) {
+                    each<4>([&](auto j) {
+                        const int row = i * 16 + r, c = (q * 4 + j) ^ r;
+                        *reinterpret_cast<f32x4 *>(mine + row * 64 + c * 4) =
+                            acc[(h * (IP / 2) + i) * 4 + j];
+                    });
+                });
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+                const int m0 = tm * BM + wm * (BM / WM) + h * half;
+                const int lanes = paired ? 4 : 8;             // a row
+#pragma unroll 1
+                for (int row = lane / lanes; row < half; row += 64 / lanes) {
+                    const int m = m0 + row, c = (lane % lanes) * (64 / lanes);
+                    if (m >= cnt)
+                        break;
+                    auto take = [&](int col, float (&v)[8]) {
+                        const float *at = mine + row * 64;
+                        const f32x4 x = *reinterpret_cast<const f32x4 *>(at + ((col / 4) ^ (row & 15)) * 4);
+                        const f32x4 y =
+                            *reinterpret_cast<const f32x4 *>(at + ((col / 4 + 1) ^ (row & 15)) * 4);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int n = tn * BN + n0 + h * 8;
+                        for (int i = 0; i < 4; ++i)
+                            v[i] = x[i], v[4 + i] = y[i];
+                    };
+                    float v[8], u[8];
+                    take(c, v);
+                    if (paired) {
+                        take(c + 8, u);
+                        const int f = tn * (BN / 2) + wn * 32 + c / 2;
+                        if (f < a.N / 2)
+                            emit_pair<8>(a, e, lo + m, f, v, u);
+                    } else {
+                        const int n = tn * BN + wn * 64 + c;
                         if (n < a.N)
-                            emit<8>(a, e, lo + m, n, v[h]);
+                            emit<8>(a, e, lo + m, n, v);
                     }
                 }
-            }
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+            });
+            __syncthreads();       // the next tile's stages overwrite the other waves' parts
         }
     }
 }
