@@ -279,24 +279,21 @@ __device__ __forceinline__ int swz_qt(int k) { return (k & 1) | (((k >> 1) & 1) 
 
 // A buffer descriptor of `bytes` bytes from `base`: a lane that reads beyond
 // them gets zeros.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const char *base, int64_t bytes)
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const char *base, int bytes)
 {
-    const int n = bytes <= 0 ? 0 : bytes > 0x7fffffff ? 0x7fffffff : (int)bytes;
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(base), 0, n, 0x00020000);
+    // scalar registers, whatever the compiler can prove: a descriptor in
+    // vector registers costs a loop at every use
+    const uint64_t at = reinterpret_cast<uint64_t>(base);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)at);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(at >> 32));
+    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>(((uint64_t)hi << 32) | lo), 0,
+                                             __builtin_amdgcn_readfirstlane(max(bytes, 0)), 0x00020000);
 }
 
-// One operand's stage: ISSUES DMAs of 16 bytes a lane, each filling 8 KB of
-// LDS (wave w the w-th KB), `step` bytes apart in memory. `off` is the lane's
-// offset in each; the descriptors move, so one register serves all of them.
-template <int ISSUES>
-__device__ __forceinline__ void dma(const char *base, int64_t bytes, int64_t step, uint32_t off,
-                                    uint16_t *lds, int wave)
+// 16 bytes a lane into 1 KB of LDS.
+__device__ __forceinline__ void dma(__amdgpu_buffer_rsrc_t r, uint32_t off, uint16_t *lds)
 {
-#pragma unroll
-    for (int i = 0; i < ISSUES; ++i)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc(base + i * step, bytes - i * step),
-                                                 (lds_void *)(lds + i * 4096 + wave * 512), 16,
-                                                 (int)off, 0, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)lds, 16, (int)off, 0, 0, 0);
 }
 
 // 8 consecutive k of one column from a strided operand's stage [64][COLS]:
@@ -361,7 +358,8 @@ __global__ __launch_bounds__(kTileThreads) void tile_kernel(Args a)
     __shared__ int32_t pre[FORM == kWeightGrad ? 1 : kMaxExperts + 1];
     __shared__ int32_t sums[8];
 
-    const int tid = threadIdx.x, lane = tid & 63;
+    const int tid = threadIdx.x;
+    const int lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WN, wn = wave % WN, r = lane & 15, q = lane >> 4;
     const bool paired = a.act == EPL_ACT_SWIGLU;
@@ -430,41 +428,37 @@ __global__ __launch_bounds__(kTileThreads) void tile_kernel(Args a)
         tm = band * 8 + rest % bh;
         const int tn = rest / bh;
 
-        // operands: base, bytes to their end, bytes between DMAs and between
-        // stages, and the lane's offset
+        // Operands: base, the lane's offset, and the bytes between the DMAs of
+        // a stage. Their ends: a strided operand ends with its rows of the
+        // contraction; a contiguous one with its last row, and pieces beyond
+        // the contraction are sent past it by the offset's top bit.
         const int depth = FORM == kWeightGrad ? cnt : a.K;
         const int steps = (depth + kTileK - 1) / kTileK;
+        const int qcols = FORM == kWeightGrad ? a.K : a.N;
         const char *bp, *bq;
-        int64_t np, nq, ip, iq, sp, sq;
         uint32_t op, oq;
+        int np = 0, nq = 0;                  // bytes of a contiguous operand
         int kp = 0, kq = 0;                  // contraction index of the lane's piece
+        const int ip = PT ? 4096 / BM * a.N * 2 : 64 * a.K * 2;
+        const int iq = QT ? 4096 / BN * qcols * 2 : (paired ? 32 : 64) * a.K * 2;
         if (PT) {
             const int k = (tid * 8) / BM, c = ((tid * 8 % BM) / 8) ^ swz_pt(k);
             op = ((uint32_t)k * a.N + tm * BM + c * 8) * 2;
             bp = reinterpret_cast<const char *>(a.p + lo * a.N);
-            np = (int64_t)cnt * a.N * 2;
-            ip = (int64_t)(4096 / BM) * a.N * 2;
-            sp = (int64_t)kTileK * a.N * 2;
         } else {
             const int row = tid >> 3, c = (tid & 7) ^ swz_p(row);
             op = ((uint32_t)row * a.K + c * 8) * 2;
             kp = c * 8;
             bp = reinterpret_cast<const char *>(a.p + (lo + (int64_t)tm * BM) * a.K);
-            np = (int64_t)(cnt - tm * BM) * a.K * 2;
-            ip = (int64_t)64 * a.K * 2;
-            sp = kTileK * 2;
+            np = min(cnt - tm * BM, BM) * a.K * 2;
         }
         if (QT) {
-            const int cols = FORM == kWeightGrad ? a.K : a.N;
             const int k = (tid * 8) / BN, c = ((tid * 8 % BN) / 8) ^ swz_qt(k);
             const int col = paired ? tn * (BN / 2) + (c >> 1) * 8 + (c & 1) * (a.N / 2)
                                    : tn * BN + c * 8;
-            oq = ((uint32_t)k * cols + col) * 2;
+            oq = ((uint32_t)k * qcols + col) * 2;
             bq = reinterpret_cast<const char *>(
-                FORM == kWeightGrad ? a.q + lo * cols : a.q + (int64_t)e * a.K * a.N);
-            nq = (int64_t)depth * cols * 2;
-            iq = (int64_t)(4096 / BN) * cols * 2;
-            sq = (int64_t)kTileK * cols * 2;
+                FORM == kWeightGrad ? a.q + lo * qcols : a.q + (int64_t)e * a.K * a.N);
         } else {
             const int row = tid >> 3, c = (tid & 7) ^ swz_q(row);
             const int n = paired ? tn * (BN / 2) + (row >> 4) * 8 + (row & 7) + (row & 8 ? a.N / 2 : 0)
@@ -472,66 +466,105 @@ __global__ __launch_bounds__(kTileThreads) void tile_kernel(Args a)
             oq = ((uint32_t)n * a.K + c * 8) * 2;
             kq = c * 8;
             bq = reinterpret_cast<const char *>(a.q + (int64_t)e * a.K * a.N);
-            nq = (int64_t)a.N * a.K * 2;
-            iq = (int64_t)(paired ? 32 : 64) * a.K * 2;
-            sq = kTileK * 2;
+            nq = a.N * a.K * 2;
         }
 
         f32x4 acc[IP * 4];
         each<IP * 4>([&](auto i) { acc[i] = f32x4{0, 0, 0, 0}; });
 
+        struct Stage {
+            __amdgpu_buffer_rsrc_t rp, rq;
+            uint32_t op, oq;
+        };
+        auto stage = [&](int s) {
+            const int k0 = s * kTileK, left = max(min(depth - k0, kTileK), 0);
+            Stage f;
+            f.rp = PT ? rsrc(bp + (int64_t)k0 * a.N * 2, left * a.N * 2) : rsrc(bp + k0 * 2, np - k0 * 2);
+            f.rq = QT ? rsrc(bq + (int64_t)k0 * qcols * 2, left * qcols * 2)
+                      : rsrc(bq + k0 * 2, nq - k0 * 2);
+            f.op = !PT && kp >= left ? op | 0x80000000u : op;
+            f.oq = !QT && kq >= left ? oq | 0x80000000u : oq;
+            return f;
+        };
+        // DMA number x of a stage: those of P, then those of Q
+        auto fetch_one = [&](const Stage &f, uint16_t *lp, uint16_t *lq, auto x) {
+            if constexpr (x < ISP)
+                dma(f.rp, f.op + x * ip, lp + x * 4096 + wave * 512);
+            else
+                dma(f.rq, f.oq + (x - ISP) * iq, lq + (x - ISP) * 4096 + wave * 512);
+        };
         auto fetch = [&](int s, uint16_t *lp, uint16_t *lq) {
-            // pieces past the contraction's end must read as zero: whole rows
-            // of a strided operand lie beyond its bytes, pieces of a
-            // contiguous one are pointed there
-            const int k0 = s * kTileK;
-            const uint32_t zp = !PT && k0 + kp >= depth ? 0x80000000u : 0u;
-            const uint32_t zq = !QT && k0 + kq >= depth ? 0x80000000u : 0u;
-            const char *gp = bp + s * sp, *gq = bq + s * sq;
-            dma<ISP>(gp, np - s * sp, ip, op | zp, lp, wave);
-            dma<ISQ>(gq, nq - s * sq, iq, oq | zq, lq, wave);
+            const Stage f = stage(s);
+            each<ISP + ISQ>([&](auto x) { fetch_one(f, lp, lq, x); });
         };
-        auto multiply = [&](const uint16_t *lp, const uint16_t *lq) {
-#pragma unroll
-            for (int kb = 0; kb < kTileK / 32; ++kb) {
-                bf16x8 fq[4], fp[IP];
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    fq[j] = QT ? read_tr<BN>(lq + aq[j >> 1] + kb * 32 * BN + (j & 1) * 4)
-                               : *reinterpret_cast<const bf16x8 *>(lq + aq[kb] + j * 4 * kTileK);
-#pragma unroll
-                for (int i = 0; i < IP; ++i)
-                    fp[i] = PT ? read_tr<BM>(lp + (ap[0] ^ (i * 16)) + kb * 32 * BM)
-                               : *reinterpret_cast<const bf16x8 *>(lp + ap[kb] + i * 16 * kTileK);
-                each<IP * 4>([&](auto x) {
-                    acc[x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fq[x % 4], fp[x / 4], acc[x],
-                                                                     0, 0, 0);
-                });
-            }
+        auto read_q = [&](bf16x8 (&f)[4], const uint16_t *lq, auto kb) {
+            each<4>([&](auto j) {
+                f[j] = QT ? read_tr<BN>(lq + aq[j / 2] + kb * 32 * BN + (j & 1) * 4)
+                          : *reinterpret_cast<const bf16x8 *>(lq + aq[kb] + j * 4 * kTileK);
+            });
         };
-
-        // one step first where their number is odd, then pairs
-        auto turn = [&](int next, uint16_t *np_, uint16_t *nq_, const uint16_t *lp,
-                        const uint16_t *lq) {
-            if (next < steps)
-                fetch(next, np_, nq_);
-            multiply(lp, lq);
+        bf16x8 fp[IP], qa[4], qb[4];
+        auto read_p = [&](const uint16_t *lp, auto i, auto kb) {
+            fp[i] = PT ? read_tr<BM>(lp + (ap[0] ^ (i * 16)) + kb * 32 * BM)
+                       : *reinterpret_cast<const bf16x8 *>(lp + ap[kb] + i * 16 * kTileK);
+        };
+        auto multiply = [&](const bf16x8 (&fq)[4], auto i) {
+            each<4>([&](auto j) {
+                acc[i * 4 + j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fq[j], fp[i], acc[i * 4 + j],
+                                                                         0, 0, 0);
+            });
+        };
+        // One stage, in two halves of 32. A piece of P is read again, for the
+        // next half, as soon as its products are issued, so reads run under
+        // the products all the time and take no second set of registers; Q
+        // has two sets. The one barrier a stage, behind the first products of
+        // its second half, says both that every wave has read the rest of
+        // this stage, which the DMA of the stage after the next may now
+        // overwrite, and that the next stage has landed.
+        using Zero = std::integral_constant<int, 0>;
+        using One = std::integral_constant<int, 1>;
+        constexpr int ahead = IP / 4;        // pieces multiplied ahead of the barrier
+        auto turn = [&](int s, uint16_t *cp, uint16_t *cq, uint16_t *xp, uint16_t *xq) {
+            read_q(qb, cq, One{});
+            each<IP>([&](auto i) {
+                multiply(qa, i);
+                read_p(cp, i, One{});
+                __builtin_amdgcn_sched_barrier(0);
+            });
+            each<ahead>([&](auto i) { multiply(qb, i); });
+            __builtin_amdgcn_sched_barrier(0);
             __builtin_amdgcn_s_waitcnt(0);
-            __syncthreads();
+            __builtin_amdgcn_s_barrier();
+            const Stage f = stage(s + 2);
+            read_q(qa, xq, Zero{});          // after the last stage: not used
+            each<ahead>([&](auto i) { read_p(xp, i, Zero{}); });
+            __builtin_amdgcn_sched_barrier(0);
+            constexpr int groups = IP - ahead, per = (ISP + ISQ + groups - 1) / groups;
+            each<groups>([&](auto o) {
+                constexpr std::integral_constant<int, ahead + decltype(o)::value> i{};
+                multiply(qb, i);
+                read_p(xp, i, Zero{});
+                each<per>([&](auto u) {
+                    constexpr std::integral_constant<int, decltype(o)::value * per + decltype(u)::value> x{};
+                    if constexpr (x < ISP + ISQ)
+                        fetch_one(f, cp, cq, x);
+                });
+                __builtin_amdgcn_sched_barrier(0);
+            });
         };
-        const int odd = steps & 1;
-        if (odd)
-            fetch(0, sp1, sq1);
-        else if (steps > 0)
-            fetch(0, sp0, sq0);
+        // Pairs of stages, without a branch inside: a stage past the last is
+        // filled with zeros, by descriptors that hold no bytes.
+        fetch(0, sp0, sq0);
         __builtin_amdgcn_s_waitcnt(0);
-        __syncthreads();
-        if (odd)
-            turn(1, sp0, sq0, sp1, sq1);
-        for (int s = odd; s < steps; s += 2) {
+        __builtin_amdgcn_s_barrier();
+        fetch(1, sp1, sq1);
+        read_q(qa, sq0, Zero{});
+        each<IP>([&](auto i) { read_p(sp0, i, Zero{}); });
+        for (int s = 0; s < steps; s += 2) {
+            turn(s, sp0, sq0, sp1, sq1);
             turn(s + 1, sp1, sq1, sp0, sq0);
-            turn(s + 2, sp0, sq0, sp1, sq1);
         }
+        __syncthreads();
 
         if (FORM == kWeightGrad) {
             // a lane's 16 columns of row m
@@ -554,12 +587,15 @@ __global__ __launch_bounds__(kTileThreads) void tile_kernel(Args a)
             // neighbouring columns and the epilogue's code is there once a
             // pass, not once an accumulator (43 000 instructions otherwise).
             constexpr int half = IP / 2 * 16;
+            int own = lane;                  // opaque: no address of it is kept from tile to tile
+            asm volatile("" : "+v"(own));
+            const int er = own & 15, eq = own >> 4;
             uint16_t *const part = wave < 2 ? sp0 : wave < 4 ? sp1 : wave < 6 ? sq0 : sq1;
             float *const mine = reinterpret_cast<float *>(part) + (wave & 1) * half * 64;
             each<2>([&](auto h) {
                 each<IP / 2>([&](auto i) {
                     each<4>([&](auto j) {
-                        const int row = i * 16 + r, c = (q * 4 + j) ^ r;
+                        const int row = i * 16 + er, c = (eq * 4 + j) ^ er;
                         *reinterpret_cast<f32x4 *>(mine + row * 64 + c * 4) =
                             acc[(h * (IP / 2) + i) * 4 + j];
                     });
@@ -568,8 +604,8 @@ __global__ __launch_bounds__(kTileThreads) void tile_kernel(Args a)
                 const int m0 = tm * BM + wm * (BM / WM) + h * half;
                 const int lanes = paired ? 4 : 8;             // a row
 #pragma unroll 1
-                for (int row = lane / lanes; row < half; row += 64 / lanes) {
-                    const int m = m0 + row, c = (lane % lanes) * (64 / lanes);
+                for (int row = own / lanes; row < half; row += 64 / lanes) {
+                    const int m = m0 + row, c = (own % lanes) * (64 / lanes);
                     if (m >= cnt)
                         break;
                     auto take = [&](int col, float (&v)[8]) {
