@@ -336,9 +336,8 @@ int epl_expert_scale(const epl_problem *p, const uint16_t *rows_in,
  *   epl_route_backward.
  * The conventions above hold: device pointers to dense row-major arrays, the
  * caller owns every buffer, calls only enqueue on `stream`, arguments are
- * checked on the host first. These calls need no workspace, so captured
- * graphs and concurrent streams share nothing. No output may overlap an
- * input unless it says so. Results are deterministic, bit for bit.
+ * checked on the host first. No output may overlap an input unless it says
+ * so. Results are deterministic, bit for bit.
  * ======================================================================= */
 
 /* ---- router ------------------------------------------------------------- */
@@ -425,6 +424,15 @@ typedef struct epl_product_desc {
 /* Host-only check of a product description. Needs no GPU. */
 int epl_product_validate(const epl_product_desc *p);
 
+/* Bytes of device workspace for the two calls below, 0 if they need none (or
+ * `p` is invalid). Where there are fewer tiles of the output than the GPU has
+ * CUs to work on them, or a last few, their sums over K (over the rows) are
+ * split and joined through it; without one (NULL) the results hold as well,
+ * more slowly (the two differ by the order of fp32 sums). It needs no
+ * initialisation; calls that may overlap need one each. Host-only. */
+size_t epl_product_workspace_bytes(const epl_product_desc *p);
+size_t epl_weight_grad_workspace_bytes(const epl_product_desc *p);
+
 /* Product of every expert's rows with its weight. For expert e and its rows
  * p in [expert_start_loc[e], expert_start_loc[e] + num_tokens_per_expert[e])
  * (both int32 [E] on the GPU, as the dispatch writes them):
@@ -438,11 +446,12 @@ int epl_product_validate(const epl_product_desc *p);
  * gradient with respect to the activation's output. Rows that belong to no
  * expert (padding, capacity beyond the total) are left as they were in y and
  * pre; a block is cut to the buffer's rows. Blocks of different experts must
- * not share rows. All pointers 16-byte aligned but the int32 ones. */
+ * not share rows. All pointers 16-byte aligned but the int32 ones (4) and the
+ * workspace (256). */
 int epl_expert_product(const epl_product_desc *p, const uint16_t *x, const uint16_t *weight,
                        const float *bias, const uint16_t *residual,
                        const int32_t *expert_start_loc, const int32_t *num_tokens_per_expert,
-                       uint16_t *pre, void *y, void *stream);
+                       uint16_t *pre, void *y, void *workspace, void *stream);
 
 /* Gradient of the weights and the bias of a product (weight_layout OUT_IN,
  * activation NONE): for every expert
@@ -454,7 +463,8 @@ int epl_expert_product(const epl_product_desc *p, const uint16_t *x, const uint1
  * (in fp32, one rounding). */
 int epl_expert_weight_grad(const epl_product_desc *p, const uint16_t *grad, const uint16_t *x,
                            const int32_t *expert_start_loc, const int32_t *num_tokens_per_expert,
-                           int accumulate, void *grad_weight, float *grad_bias, void *stream);
+                           int accumulate, void *grad_weight, float *grad_bias, void *workspace,
+                           void *stream);
 
 /* ---- gradient of the combine ---------------------------------------------- */
 /* For y = epl_combine(expert_out, output_index, topk_weights):

@@ -27,7 +27,8 @@ __all__ = [
     "EPL_OUT_BF16", "prepare", "epl_scatter_fp8", "epl_dispatch_fp8", "EPL_SCALE_NONE",
     "EPL_SCALE_F32", "EPL_SCALE_UE8M0", "epl_dispatch_static", "StaticWorkspace",
     "EPL_STATIC_WORKSPACE_BYTES", "Router", "Product", "epl_router_validate", "epl_route",
-    "epl_route_backward", "epl_product_validate", "epl_expert_product", "epl_expert_weight_grad",
+    "epl_route_backward", "epl_product_validate", "epl_product_workspace_bytes",
+    "epl_weight_grad_workspace_bytes", "epl_expert_product", "epl_expert_weight_grad",
     "epl_combine_backward", "route", "route_backward", "expert_product", "expert_weight_grad",
     "combine_backward", "dispatch_backward", "EPL_SCORE_SOFTMAX", "EPL_SCORE_SIGMOID",
     "EPL_ACT_NONE", "EPL_ACT_SILU", "EPL_ACT_GELU", "EPL_ACT_SWIGLU", "EPL_ACT_SILU_GRAD",
@@ -65,6 +66,7 @@ C_ENTRY_POINTS = (
     "epl_ll_workspace_bytes", "epl_ll_dispatch", "epl_dispatch_static",
     "epl_router_validate", "epl_route", "epl_route_backward", "epl_product_validate",
     "epl_expert_product", "epl_expert_weight_grad", "epl_combine_backward",
+    "epl_product_workspace_bytes", "epl_weight_grad_workspace_bytes",
 )
 
 
@@ -222,10 +224,13 @@ def load() -> ctypes.CDLL:
     lib.epl_route_backward.restype = i32
     lib.epl_product_validate.argtypes = [pp]
     lib.epl_product_validate.restype = i32
-    lib.epl_expert_product.argtypes = [pp, _P, _P, _P, _P, _P, _P, _P, _P, _P]
+    lib.epl_expert_product.argtypes = [pp, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]
     lib.epl_expert_product.restype = i32
-    lib.epl_expert_weight_grad.argtypes = [pp, _P, _P, _P, _P, i32, _P, _P, _P]
+    lib.epl_expert_weight_grad.argtypes = [pp, _P, _P, _P, _P, i32, _P, _P, _P, _P]
     lib.epl_expert_weight_grad.restype = i32
+    for name in ("epl_product_workspace_bytes", "epl_weight_grad_workspace_bytes"):
+        getattr(lib, name).argtypes = [pp]
+        getattr(lib, name).restype = ctypes.c_size_t
     lib.epl_combine_backward.argtypes = [_PP, i32, _P, _P, i64, _P, _P, _P, _P, _P, _P]
     lib.epl_combine_backward.restype = i32
     lib.epl_status.argtypes = [_P, _P]
@@ -692,8 +697,24 @@ def _blocks(p: Product, expert_start_loc, num_tokens_per_expert, dev):
     _need(num_tokens_per_expert, "num_tokens_per_expert", torch.int32, (p.num_experts,), dev)
 
 
+def epl_product_workspace_bytes(p: Product) -> int:
+    return int(load().epl_product_workspace_bytes(ctypes.byref(p)))
+
+
+def epl_weight_grad_workspace_bytes(p: Product) -> int:
+    return int(load().epl_weight_grad_workspace_bytes(ctypes.byref(p)))
+
+
+def _need_split_ws(workspace, dev, need, where):
+    """The optional workspace of the products: None, or all of it."""
+    _need(workspace, "workspace", _torch().uint8, None, dev, allow_none=True)
+    if workspace is not None and workspace.numel() < need:
+        raise ValueError(f"{where}: workspace holds {workspace.numel()} bytes, the product needs "
+                         f"{need}")
+
+
 def epl_expert_product(p: Product, x, weight, bias, residual, expert_start_loc,
-                       num_tokens_per_expert, pre, y, stream=None):
+                       num_tokens_per_expert, pre, y, workspace=None, stream=None):
     torch = _torch()
     rows, E, K, N = p.num_rows, p.num_experts, p.in_cols, p.out_cols
     bf16 = torch.bfloat16
@@ -709,13 +730,15 @@ def epl_expert_product(p: Product, x, weight, bias, residual, expert_start_loc,
     _need(pre, "pre", bf16, (rows, cols if grad else N), dev, allow_none=not grad)
     _need(y, "y", bf16 if p.out_type == EPL_OUT_BF16 else torch.float32, (rows, cols), dev)
     _blocks(p, expert_start_loc, num_tokens_per_expert, dev)
+    if workspace is not None:
+        _need_split_ws(workspace, dev, epl_product_workspace_bytes(p), "epl_expert_product")
     _launch("epl_expert_product", dev, stream, ctypes.byref(p), _ptr(x), _ptr(weight), _ptr(bias),
             _ptr(residual), _ptr(expert_start_loc), _ptr(num_tokens_per_expert), _ptr(pre),
-            _ptr(y))
+            _ptr(y), _ptr(workspace))
 
 
 def epl_expert_weight_grad(p: Product, grad, x, expert_start_loc, num_tokens_per_expert,
-                           accumulate, grad_weight, grad_bias=None, stream=None):
+                           accumulate, grad_weight, grad_bias=None, workspace=None, stream=None):
     torch = _torch()
     rows, E, K, N = p.num_rows, p.num_experts, p.in_cols, p.out_cols
     _need(grad, "grad", torch.bfloat16, (rows, N))
@@ -725,9 +748,12 @@ def epl_expert_weight_grad(p: Product, grad, x, expert_start_loc, num_tokens_per
           torch.bfloat16 if p.out_type == EPL_OUT_BF16 else torch.float32, (E, N, K), dev)
     _need(grad_bias, "grad_bias", torch.float32, (E, N), dev, allow_none=True)
     _blocks(p, expert_start_loc, num_tokens_per_expert, dev)
+    if workspace is not None:
+        _need_split_ws(workspace, dev, epl_weight_grad_workspace_bytes(p),
+                       "epl_expert_weight_grad")
     _launch("epl_expert_weight_grad", dev, stream, ctypes.byref(p), _ptr(grad), _ptr(x),
             _ptr(expert_start_loc), _ptr(num_tokens_per_expert), int(bool(accumulate)),
-            _ptr(grad_weight), _ptr(grad_bias))
+            _ptr(grad_weight), _ptr(grad_bias), _ptr(workspace))
 
 
 def epl_combine_backward(p: Problem, grad_y, expert_out, expert_rows, output_index, topk_weights,
@@ -894,6 +920,20 @@ def expert_scale(res: DispatchResult, rows_in=None, stream=None):
     return out
 
 
+def _split_ws(nbytes, device, stream):
+    """A product's workspace, from torch's allocator (kept for `stream` when
+    that is not torch's current one)."""
+    if nbytes == 0:
+        return None
+    torch = _torch()
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if stream is not None:
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=device)
+        ws.record_stream(stream)
+    return ws
+
+
 _SCORES = {"softmax": EPL_SCORE_SOFTMAX, "sigmoid": EPL_SCORE_SIGMOID}
 _ACTIVATIONS = {"none": EPL_ACT_NONE, "silu": EPL_ACT_SILU, "gelu": EPL_ACT_GELU,
                 "swiglu": EPL_ACT_SWIGLU, "silu_grad": EPL_ACT_SILU_GRAD,
@@ -952,14 +992,15 @@ def route_backward(logits, topk_idx, grad_weights, score: str = "softmax",
 
 def expert_product(x, weight, expert_start_loc, num_tokens_per_expert, bias=None,
                    activation: str = "none", residual=None, pre=None, out=None, out_dtype=None,
-                   transposed: bool = False, expected_rows: int = 0, stream=None):
+                   transposed: bool = False, expected_rows: int = 0, workspace=None, stream=None):
     """act(x @ weight[e]^T + bias[e]) + residual for the rows of each expert
     (x [rows, K] bf16, e.g. DispatchResult.out; weight [E, N, K] bf16), as
     epl_expert_product in include/epl.h. transposed=True takes weight as
     [E, K, N] and multiplies by it as it is: with the forward pass's array
     that is the data gradient. `pre` (bf16 [rows, N]) receives the product
     before the activation, or feeds a "..._grad" activation. Rows outside the
-    experts' blocks are not written: pass `out` to choose what they hold."""
+    experts' blocks are not written: pass `out` to choose what they hold.
+    A workspace is taken from torch's allocator where none is passed."""
     torch = _torch()
     _matrix(x, "x", 2)
     _matrix(weight, "weight", 3)
@@ -979,13 +1020,15 @@ def expert_product(x, weight, expert_start_loc, num_tokens_per_expert, bias=None
     if out is None:
         cols = N // 2 if act == EPL_ACT_SWIGLU else 2 * N if act == EPL_ACT_SWIGLU_GRAD else N
         out = torch.empty((x.shape[0], cols), dtype=out_dtype, device=x.device)
+    if workspace is None and x.is_cuda:
+        workspace = _split_ws(epl_product_workspace_bytes(p), x.device, stream)
     epl_expert_product(p, x, weight, bias, residual, expert_start_loc, num_tokens_per_expert, pre,
-                       out, stream)
+                       out, workspace, stream)
     return out
 
 
 def expert_weight_grad(grad, x, expert_start_loc, num_tokens_per_expert, out=None, out_dtype=None,
-                       bias_grad=None, accumulate: bool = False, stream=None):
+                       bias_grad=None, accumulate: bool = False, workspace=None, stream=None):
     """Gradient of expert_product's weight, [E, N, K], from that of its
     product `grad` (bf16 [rows, N]) and its input x (bf16 [rows, K]).
     `bias_grad` (fp32 [E, N]) receives the bias's. accumulate=True adds to
@@ -1005,8 +1048,10 @@ def expert_weight_grad(grad, x, expert_start_loc, num_tokens_per_expert, out=Non
     p = Product(grad.shape[0], 0, E, K, N, EPL_WEIGHT_OUT_IN, EPL_ACT_NONE,
                 _type_code(out.dtype, "out"), 0)
     _check(epl_product_validate(p), "epl_product_validate")
+    if workspace is None and x.is_cuda:
+        workspace = _split_ws(epl_weight_grad_workspace_bytes(p), x.device, stream)
     epl_expert_weight_grad(p, grad, x, expert_start_loc, num_tokens_per_expert, accumulate, out,
-                           bias_grad, stream)
+                           bias_grad, workspace, stream)
     return out
 
 

@@ -58,14 +58,93 @@ int num_cus()
     return n;
 }
 
+// The kernel that a product takes. The counts are on the GPU: the choice goes
+// by the rows that the caller expects an expert to have on average.
+enum Kind { kFew, kSquare, kWide, kTall };       // tiles 256 x 256, 128 x 256, 256 x 128
+
+Kind kind_of(const epl_product_desc &p)
+{
+    const int64_t rows = p.expected_rows > 0 ? std::min(p.expected_rows, p.num_rows) : p.num_rows;
+    const int64_t avg = (rows + p.num_experts - 1) / p.num_experts;
+    if (p.weight_layout == EPL_WEIGHT_OUT_IN && avg <= 64)
+        return kFew;
+    // half of the last 256 columns empty, or of the rows
+    if (p.out_cols % 256 != 0 && p.out_cols % 256 <= 128 && p.out_cols < 1024)
+        return kTall;
+    return avg <= 128 ? kWide : kSquare;
+}
+
+Kind grad_kind_of(const epl_product_desc &p)
+{
+    return p.out_cols <= 128 ? kWide : p.in_cols <= 128 ? kTall : kSquare;
+}
+
+int rows_of(Kind k) { return k == kWide ? 128 : 256; }
+int cols_of(Kind k) { return k == kTall ? 128 : 256; }
+
+// Parts that a contraction of `depth` is worth being split into: at least
+// four stages each.
+int max_parts(int64_t depth)
+{
+    return (int)std::min<int64_t>(P::kMaxParts, depth / (4 * P::kTileK));
+}
+
+// The depth of a weight gradient's contraction is the expert's rows.
+int64_t grad_depth(const epl_product_desc &p) { return p.num_rows / p.num_experts; }
+
+size_t tile_workspace(Kind k, int64_t tiles, int parts)
+{
+    if (k == kFew || parts < 2)
+        return 0;
+    const int64_t slots = std::min<int64_t>(P::kSlots, tiles * parts);
+    return (size_t)slots * rows_of(k) * cols_of(k) * sizeof(float);
+}
+
+int64_t product_tiles(const epl_product_desc &p, Kind k)
+{
+    return (p.num_rows / rows_of(k) + p.num_experts) * ((p.out_cols + cols_of(k) - 1) / cols_of(k));
+}
+
+int64_t grad_tiles(const epl_product_desc &p, Kind k)
+{
+    return (int64_t)p.num_experts * ((p.out_cols + rows_of(k) - 1) / rows_of(k)) *
+           ((p.in_cols + cols_of(k) - 1) / cols_of(k));
+}
+
+// `tiles`: how many there are, or at most are.
 template <int BM, int BN, P::Form FORM>
 int launch_tiles(const P::Args &a, int64_t tiles, hipStream_t s)
 {
-    // one workgroup a CU, striding over the tiles
-    const int64_t grid = std::min<int64_t>(tiles, num_cus());
+    // one workgroup a CU, striding over the tiles; also with fewer tiles
+    // where their contraction can be split
+    const bool split = a.ws && a.max_parts > 1;
+    const int cus = std::min(num_cus(), P::kSlots);
+    const int grid = (int)(split ? std::min<int64_t>(tiles * a.max_parts, cus)
+                                 : std::min<int64_t>(tiles, cus));
     hipLaunchKernelGGL((P::tile_kernel<BM, BN, FORM>), dim3((unsigned)grid), dim3(P::kTileThreads), 0,
                        s, a);
-    return launch_status();
+    int rc = launch_status();
+    if (rc == EPL_OK && split) {
+        constexpr int pieces = BM / (8 / (BN / 64)) / 16;
+        hipLaunchKernelGGL((P::join_kernel<BM, BN, FORM>),
+                           dim3(pieces, (unsigned)std::max<int64_t>(1, std::min<int64_t>(tiles, grid / 2))),
+                           dim3(P::kTileThreads), 0, s, a, grid);
+        rc = launch_status();
+    }
+    return rc;
+}
+
+template <P::Form FORM>
+int launch_kind(Kind k, const P::Args &a, int64_t tiles, hipStream_t s)
+{
+    switch (k) {
+    case kWide:
+        return launch_tiles<128, 256, FORM>(a, tiles, s);
+    case kTall:
+        return launch_tiles<256, 128, FORM>(a, tiles, s);
+    default:
+        return launch_tiles<256, 256, FORM>(a, tiles, s);
+    }
 }
 
 }  // namespace
@@ -74,10 +153,26 @@ extern "C" {
 
 int epl_product_validate(const epl_product_desc *p) { return desc_ok(p) ? EPL_OK : EPL_EINVAL; }
 
+size_t epl_product_workspace_bytes(const epl_product_desc *p)
+{
+    if (!desc_ok(p))
+        return 0;
+    const Kind k = kind_of(*p);
+    return tile_workspace(k, product_tiles(*p, k), max_parts(p->in_cols));
+}
+
+size_t epl_weight_grad_workspace_bytes(const epl_product_desc *p)
+{
+    if (!desc_ok(p))
+        return 0;
+    const Kind k = grad_kind_of(*p);
+    return tile_workspace(k, grad_tiles(*p, k), max_parts(grad_depth(*p)));
+}
+
 int epl_expert_product(const epl_product_desc *p, const uint16_t *x, const uint16_t *weight,
                        const float *bias, const uint16_t *residual,
                        const int32_t *expert_start_loc, const int32_t *num_tokens_per_expert,
-                       uint16_t *pre, void *y, void *stream)
+                       uint16_t *pre, void *y, void *workspace, void *stream)
 {
     if (!desc_ok(p))
         return EPL_EINVAL;
@@ -86,7 +181,7 @@ int epl_expert_product(const epl_product_desc *p, const uint16_t *x, const uint1
         return EPL_EINVAL;
     if (!weight || !aligned(weight, 16) || !expert_start_loc || !aligned(expert_start_loc, 4) ||
         !num_tokens_per_expert || !aligned(num_tokens_per_expert, 4) || !aligned(bias, 16) ||
-        !aligned(residual, 16) || !aligned(pre, 16))
+        !aligned(residual, 16) || !aligned(pre, 16) || !aligned(workspace, 256))
         return EPL_EINVAL;
     if (p->num_rows == 0)
         return EPL_OK;
@@ -108,44 +203,31 @@ int epl_expert_product(const epl_product_desc *p, const uint16_t *x, const uint1
     a.act = p->activation;
     a.out_f32 = p->out_type == EPL_OUT_F32;
     hipStream_t s = static_cast<hipStream_t>(stream);
-
-    // The counts are on the GPU: the kernel is chosen by the rows that the
-    // caller expects an expert to have on average.
-    const int64_t rows = p->expected_rows > 0 ? std::min(p->expected_rows, p->num_rows) : p->num_rows;
-    const int64_t avg = (rows + a.E - 1) / a.E;
-    const bool swiglu = a.act == EPL_ACT_SWIGLU;
-    if (p->weight_layout == EPL_WEIGHT_OUT_IN && avg <= 64) {
-        const int nb = swiglu ? (a.N / 2 + 15) / 16 : (a.N + 31) / 32;
+    const Kind k = kind_of(*p);
+    if (k == kFew) {
+        const int nb = a.act == EPL_ACT_SWIGLU ? (a.N / 2 + 15) / 16 : (a.N + 31) / 32;
         hipLaunchKernelGGL(P::few_rows_kernel, dim3((unsigned)nb, (unsigned)a.E),
                            dim3(P::kFewThreads), 0, s, a);
         return launch_status();
     }
-    // Tile rows: 256 reuse the weights most; 128 make more tiles. Rounds of
-    // one tile a CU are compared, a tile of 128 rows at 0.65 of the time of
-    // one of 256 (measured: 64 experts of 192 rows, 4096 -> 2048, 297 us in 2
-    // rounds of 256 against 381 us in 4 of 128; 8 experts of 192 rows, 7168
-    // -> 4096, 198 us against 166 us in one round each).
-    const int64_t cus = num_cus(), ntn = (a.N + 255) / 256;
-    auto rounds = [&](int64_t bm) { return ((avg + bm - 1) / bm * a.E * ntn + cus - 1) / cus; };
-    const bool tall = rounds(256) * 100 <= rounds(128) * 65;
-    auto tiles = [&](int bm) { return (p->num_rows / bm + a.E) * ntn; };
-    if (p->weight_layout == EPL_WEIGHT_OUT_IN)
-        return tall ? launch_tiles<256, 256, P::kForward>(a, tiles(256), s)
-                    : launch_tiles<128, 256, P::kForward>(a, tiles(128), s);
-    return tall ? launch_tiles<256, 256, P::kDataGrad>(a, tiles(256), s)
-                : launch_tiles<128, 256, P::kDataGrad>(a, tiles(128), s);
+    a.max_parts = max_parts(a.K);
+    a.ws = a.max_parts > 1 ? static_cast<P::f32x4 *>(workspace) : nullptr;
+    const int64_t tiles = product_tiles(*p, k);
+    return p->weight_layout == EPL_WEIGHT_OUT_IN ? launch_kind<P::kForward>(k, a, tiles, s)
+                                                 : launch_kind<P::kDataGrad>(k, a, tiles, s);
 }
 
 int epl_expert_weight_grad(const epl_product_desc *p, const uint16_t *grad, const uint16_t *x,
                            const int32_t *expert_start_loc, const int32_t *num_tokens_per_expert,
-                           int accumulate, void *grad_weight, float *grad_bias, void *stream)
+                           int accumulate, void *grad_weight, float *grad_bias, void *workspace,
+                           void *stream)
 {
     if (!desc_ok(p) || p->activation != EPL_ACT_NONE || p->weight_layout != EPL_WEIGHT_OUT_IN ||
         (accumulate != 0 && accumulate != 1))
         return EPL_EINVAL;
     if (!expert_start_loc || !aligned(expert_start_loc, 4) || !num_tokens_per_expert ||
         !aligned(num_tokens_per_expert, 4) || !grad_weight || !aligned(grad_weight, 16) ||
-        !aligned(grad_bias, 4))
+        !aligned(grad_bias, 4) || !aligned(workspace, 256))
         return EPL_EINVAL;
     if (p->num_rows > 0 && (!x || !aligned(x, 16) || !grad || !aligned(grad, 16)))
         return EPL_EINVAL;
@@ -163,8 +245,14 @@ int epl_expert_weight_grad(const epl_product_desc *p, const uint16_t *grad, cons
     a.out_f32 = p->out_type == EPL_OUT_F32;
     a.accumulate = accumulate;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const int64_t tiles = (int64_t)a.E * ((a.N + 255) / 256) * ((a.K + 255) / 256);
-    int rc = launch_tiles<256, 256, P::kWeightGrad>(a, tiles, s);
+    const Kind k = grad_kind_of(*p);
+    const int64_t tiles = grad_tiles(*p, k);
+    const int cus = std::min(num_cus(), P::kSlots);
+    // no tile is left over, or too many to share out: nothing to join
+    const bool even = tiles >= cus && (tiles % cus == 0 || tiles % cus > cus / 2);
+    a.max_parts = max_parts(grad_depth(*p));
+    a.ws = a.max_parts > 1 && !even ? static_cast<P::f32x4 *>(workspace) : nullptr;
+    int rc = launch_kind<P::kWeightGrad>(k, a, tiles, s);
     if (rc == EPL_OK && grad_bias) {
         hipLaunchKernelGGL(P::bias_grad_kernel, dim3((unsigned)((a.N + 63) / 64), (unsigned)a.E),
                            dim3(P::kBiasThreads), 0, s, a, grad_bias);

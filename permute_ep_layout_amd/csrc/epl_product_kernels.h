@@ -33,6 +33,8 @@ constexpr int kMaxExperts = 2048;
 constexpr int kTileThreads = 512;      // 8 waves: one workgroup fills a CU's four SIMDs twice
 constexpr int kTileK = 64;             // contraction depth of one LDS stage
 constexpr int kNumXcd = 8;
+constexpr int kMaxParts = 16;          // parts that a tile's contraction is split into, at most
+constexpr int kSlots = 256;            // partial tiles of a workspace, at most
 
 struct Args {
     const __bf16 *p;          // rows (forward, data gradient) or d rows (weight gradient)
@@ -49,6 +51,8 @@ struct Args {
     int act;                  // EPL_ACT_*
     int out_f32;
     int accumulate;           // weight gradient: add to y
+    f32x4 *ws;                // partial tiles, or null
+    int max_parts;            // parts worth splitting a tile's contraction into
 };
 
 // f(0), f(1), .. f(N - 1) with the index a constant from the start: an array
@@ -290,6 +294,16 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const char *base, int byt
                                              __builtin_amdgcn_readfirstlane(max(bytes, 0)), 0x00020000);
 }
 
+// All of this wave's loads into LDS and reads of it are done, and the other
+// waves' too.
+__device__ __forceinline__ void landed()
+{
+    __builtin_amdgcn_s_waitcnt(0);
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
 // 16 bytes a lane into 1 KB of LDS.
 __device__ __forceinline__ void dma(__amdgpu_buffer_rsrc_t r, uint32_t off, uint16_t *lds)
 {
@@ -345,6 +359,122 @@ __device__ __forceinline__ void tile_prefix(const Args &a, int32_t *pre, int32_t
     __syncthreads();
 }
 
+// Which tiles are computed whole, and into how many parts the contraction of
+// the rest is split. A round is one tile for every workgroup; a last round
+// that would leave half of them or more without one is shared out instead:
+// each of its `left` tiles among `parts` workgroups, whose sums
+// join_kernel adds in order.
+struct Plan {
+    int64_t whole;
+    int left, parts;
+};
+
+__device__ __forceinline__ Plan plan_of(const Args &a, int64_t tiles, int grid)
+{
+    Plan p{tiles, 0, 1};
+    const int left = (int)(tiles % grid);
+    const int parts = a.ws && left > 0 ? min(min(grid, kSlots) / left, a.max_parts) : 1;
+    if (parts > 1)
+        p = Plan{tiles - left, left, parts};
+    return p;
+}
+
+struct Tile {
+    int64_t lo;               // first row of the expert's block
+    int e, cnt, tm, tn;
+};
+
+template <Form FORM>
+__device__ __forceinline__ Tile locate(const Args &a, const int32_t *pre, int64_t t, int ntm, int ntn)
+{
+    Tile x;
+    int64_t in_e;
+    int ntm_e = ntm;
+    if (FORM == kWeightGrad) {
+        x.e = (int)(t / ((int64_t)ntm * ntn));
+        in_e = t - (int64_t)x.e * ntm * ntn;
+    } else {
+        int l = 0, h = a.E;                 // last expert with pre[e] * ntn <= t
+        while (h - l > 1) {
+            const int mid = (l + h) >> 1;
+            if ((int64_t)pre[mid] * ntn <= t)
+                l = mid;
+            else
+                h = mid;
+        }
+        x.e = __builtin_amdgcn_readfirstlane(l);
+        const int first = __builtin_amdgcn_readfirstlane(pre[x.e]);
+        in_e = t - (int64_t)first * ntn;
+        ntm_e = __builtin_amdgcn_readfirstlane(pre[x.e + 1]) - first;
+    }
+    x.cnt = block_of(a, x.e, x.lo);
+    // within an expert: bands of up to 8 m tiles, m fastest, so that the
+    // tiles in flight on an XCD share both operands in its L2
+    const int band = (int)(in_e / (8 * (int64_t)ntn));
+    const int bh = min(8, ntm_e - band * 8);
+    const int rest = (int)(in_e - (int64_t)band * 8 * ntn);
+    x.tm = band * 8 + rest % bh;
+    x.tn = rest / bh;
+    return x;
+}
+
+// The epilogue of `rows` rows of 64 columns that a wave holds in its part of
+// LDS (16-byte pieces swizzled by row): a lane takes 8 neighbouring columns,
+// or 8 of the gate and 8 of the up half. m0: the first of them in the
+// expert's block; n0: the first column in the tile's columns.
+template <int BN>
+__device__ __forceinline__ void emit_rows(const Args &a, const Tile &x, const float *mine, int rows,
+                                          int m0, int n0, int lane)
+{
+    const bool paired = a.act == EPL_ACT_SWIGLU;
+    const int lanes = paired ? 4 : 8;             // a row
+#pragma unroll 1
+    for (int row = lane / lanes; row < rows; row += 64 / lanes) {
+        const int m = m0 + row, c = (lane % lanes) * (64 / lanes);
+        if (m >= x.cnt)
+            break;
+        auto take = [&](int col, float (&v)[8]) {
+            const float *at = mine + row * 64;
+            const f32x4 y = *reinterpret_cast<const f32x4 *>(at + ((col / 4) ^ (row & 15)) * 4);
+            const f32x4 z = *reinterpret_cast<const f32x4 *>(at + ((col / 4 + 1) ^ (row & 15)) * 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[i] = y[i], v[4 + i] = z[i];
+        };
+        float v[8], u[8];
+        take(c, v);
+        if (paired) {
+            take(c + 8, u);
+            const int f = (x.tn * BN + n0 + c) / 2;
+            if (f < a.N / 2)
+                emit_pair<8>(a, x.e, x.lo + m, f, v, u);
+        } else {
+            const int n = x.tn * BN + n0 + c;
+            if (n < a.N)
+                emit<8>(a, x.e, x.lo + m, n, v);
+        }
+    }
+}
+
+// A lane's 16 columns of one row of a weight gradient.
+template <int BN>
+__device__ __forceinline__ void emit_weight_row(const Args &a, const Tile &x, int m, int n0,
+                                                const f32x4 (&acc)[4])
+{
+    if (m >= a.N)
+        return;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int n = x.tn * BN + n0 + h * 8;
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = acc[h * 2 + i / 4][i % 4];
+        if (n < a.K)
+            emit_weight<8>(a, ((int64_t)x.e * a.N + m) * a.K + n, v);
+    }
+}
+
 template <int BM, int BN, Form FORM>
 __global__ __launch_bounds__(kTileThreads) void tile_kernel(Args a)
 {
@@ -392,48 +522,31 @@ __global__ __launch_bounds__(kTileThreads) void tile_kernel(Args a)
     }
 
     // workgroups of one XCD (every eighth) take neighbouring tiles
-    const int64_t grid = gridDim.x;
+    const int grid = gridDim.x;
     int64_t first = blockIdx.x;
     if (grid % kNumXcd == 0)
         first = (first % kNumXcd) * (grid / kNumXcd) + first / kNumXcd;
+    const Plan plan = plan_of(a, total, grid);
+    const int64_t items = plan.whole + plan.left * plan.parts;
 
-    for (int64_t t = first; t < total; t += grid) {
-        int e;
-        int64_t lo;
-        int cnt, tm, ntm_e;
-        int64_t in_e;
-        if (FORM == kWeightGrad) {
-            e = (int)(t / ((int64_t)ntm * ntn));
-            in_e = t - (int64_t)e * ntm * ntn;
-            ntm_e = ntm;
-        } else {
-            int l = 0, h = a.E;                 // last expert with pre[e] * ntn <= t
-            while (h - l > 1) {
-                const int mid = (l + h) >> 1;
-                if ((int64_t)pre[mid] * ntn <= t)
-                    l = mid;
-                else
-                    h = mid;
-            }
-            e = __builtin_amdgcn_readfirstlane(l);
-            in_e = t - (int64_t)__builtin_amdgcn_readfirstlane(pre[e]) * ntn;
-            ntm_e = __builtin_amdgcn_readfirstlane(pre[e + 1]) - __builtin_amdgcn_readfirstlane(pre[e]);
-        }
-        cnt = block_of(a, e, lo);
-        // within an expert: bands of up to 8 m tiles, m fastest, so that the
-        // tiles in flight on an XCD share both operands in its L2
-        const int band = (int)(in_e / (8 * (int64_t)ntn));
-        const int bh = min(8, ntm_e - band * 8);
-        const int rest = (int)(in_e - (int64_t)band * 8 * ntn);
-        tm = band * 8 + rest % bh;
-        const int tn = rest / bh;
+    for (int64_t item = first; item < items; item += grid) {
+        const bool split = item >= plan.whole;
+        // parts of the same place in the contraction are neighbours
+        const int o = split ? (int)(item - plan.whole) : 0;
+        const int part = split ? o / plan.left : 0, rest = split ? o % plan.left : 0;
+        const Tile x = locate<FORM>(a, pre, split ? plan.whole + rest : item, ntm, ntn);
+        const int e = x.e, cnt = x.cnt, tm = x.tm, tn = x.tn;
+        const int64_t lo = x.lo;
 
         // Operands: base, the lane's offset, and the bytes between the DMAs of
         // a stage. Their ends: a strided operand ends with its rows of the
         // contraction; a contiguous one with its last row, and pieces beyond
         // the contraction are sent past it by the offset's top bit.
-        const int depth = FORM == kWeightGrad ? cnt : a.K;
-        const int steps = (depth + kTileK - 1) / kTileK;
+        const int whole = FORM == kWeightGrad ? cnt : a.K;
+        const int steps = (whole + kTileK - 1) / kTileK;
+        const int s0 = split ? steps * part / plan.parts : 0;
+        const int s1 = split ? steps * (part + 1) / plan.parts : steps;
+        const int depth = min(s1 * kTileK, whole);
         const int qcols = FORM == kWeightGrad ? a.K : a.N;
         const char *bp, *bq;
         uint32_t op, oq;
@@ -503,136 +616,153 @@ __global__ __launch_bounds__(kTileThreads) void tile_kernel(Args a)
                           : *reinterpret_cast<const bf16x8 *>(lq + aq[kb] + j * 4 * kTileK);
             });
         };
-        bf16x8 fp[IP], qa[4], qb[4];
-        auto read_p = [&](const uint16_t *lp, auto i, auto kb) {
-            fp[i] = PT ? read_tr<BM>(lp + (ap[0] ^ (i * 16)) + kb * 32 * BM)
-                       : *reinterpret_cast<const bf16x8 *>(lp + ap[kb] + i * 16 * kTileK);
+        bf16x8 fp[4], qa[4], qb[4];
+        auto read_p = [&](const uint16_t *lp, auto g) {      // piece g of a stage's 2 IP
+            constexpr int i = g % IP, kb = g / IP;
+            fp[g % 4] = PT ? read_tr<BM>(lp + (ap[0] ^ (i * 16)) + kb * 32 * BM)
+                           : *reinterpret_cast<const bf16x8 *>(lp + ap[kb] + i * 16 * kTileK);
         };
-        auto multiply = [&](const bf16x8 (&fq)[4], auto i) {
+        auto multiply = [&](const bf16x8 (&fq)[4], auto g) {
+            constexpr int i = g % IP;
             each<4>([&](auto j) {
-                acc[i * 4 + j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fq[j], fp[i], acc[i * 4 + j],
-                                                                         0, 0, 0);
+                acc[i * 4 + j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fq[j], fp[g % 4],
+                                                                         acc[i * 4 + j], 0, 0, 0);
             });
         };
-        // One stage, in two halves of 32. A piece of P is read again, for the
-        // next half, as soon as its products are issued, so reads run under
-        // the products all the time and take no second set of registers; Q
-        // has two sets. The one barrier a stage, behind the first products of
-        // its second half, says both that every wave has read the rest of
-        // this stage, which the DMA of the stage after the next may now
-        // overwrite, and that the next stage has landed.
+        // One stage: 2 IP groups of 4 products, one piece of P each, the
+        // second half of them with the second half's Q. After a group the
+        // piece 4 further on is read into its registers, so reads run under
+        // the products all the time. One barrier a stage, a group behind the
+        // last read of it: it says both that every wave has read all of this
+        // stage, which the DMA of the stage after the next may now overwrite,
+        // and that the next stage, whose first pieces are read from then on,
+        // has landed.
         using Zero = std::integral_constant<int, 0>;
         using One = std::integral_constant<int, 1>;
-        constexpr int ahead = IP / 4;        // pieces multiplied ahead of the barrier
         auto turn = [&](int s, uint16_t *cp, uint16_t *cq, uint16_t *xp, uint16_t *xq) {
-            read_q(qb, cq, One{});
-            each<IP>([&](auto i) {
-                multiply(qa, i);
-                read_p(cp, i, One{});
+            constexpr int all = 2 * IP, meet = all - 4, dmas = ISP + ISQ;
+            Stage f;
+            each<all>([&](auto g) {
+                if constexpr (g < IP)
+                    multiply(qa, g);
+                else
+                    multiply(qb, g);
+                if constexpr (g == 0)
+                    read_q(qb, cq, One{});
+                if constexpr (g < meet)
+                    read_p(cp, std::integral_constant<int, g + 4>{});
                 __builtin_amdgcn_sched_barrier(0);
-            });
-            each<ahead>([&](auto i) { multiply(qb, i); });
-            __builtin_amdgcn_sched_barrier(0);
-            __builtin_amdgcn_s_waitcnt(0);
-            __builtin_amdgcn_s_barrier();
-            const Stage f = stage(s + 2);
-            read_q(qa, xq, Zero{});          // after the last stage: not used
-            each<ahead>([&](auto i) { read_p(xp, i, Zero{}); });
-            __builtin_amdgcn_sched_barrier(0);
-            constexpr int groups = IP - ahead, per = (ISP + ISQ + groups - 1) / groups;
-            each<groups>([&](auto o) {
-                constexpr std::integral_constant<int, ahead + decltype(o)::value> i{};
-                multiply(qb, i);
-                read_p(xp, i, Zero{});
-                each<per>([&](auto u) {
-                    constexpr std::integral_constant<int, decltype(o)::value * per + decltype(u)::value> x{};
-                    if constexpr (x < ISP + ISQ)
-                        fetch_one(f, cp, cq, x);
-                });
-                __builtin_amdgcn_sched_barrier(0);
+                if constexpr (g == meet) {
+                    landed();
+                    f = stage(s + 2);
+                    read_q(qa, xq, Zero{});      // after the last stage: not used
+                }
+                if constexpr (g >= meet)
+                    read_p(xp, std::integral_constant<int, g - meet>{});
+                if constexpr (g >= meet) {       // the DMAs, over the groups that are left
+                    constexpr int part = g - meet, per = (dmas + 3) / 4;
+                    each<per>([&](auto u) {
+                        constexpr std::integral_constant<int, part * per + decltype(u)::value> x{};
+                        if constexpr (x < dmas)
+                            fetch_one(f, cp, cq, x);
+                    });
+                    __builtin_amdgcn_sched_barrier(0);
+                }
             });
         };
         // Pairs of stages, without a branch inside: a stage past the last is
         // filled with zeros, by descriptors that hold no bytes.
-        fetch(0, sp0, sq0);
-        __builtin_amdgcn_s_waitcnt(0);
-        __builtin_amdgcn_s_barrier();
-        fetch(1, sp1, sq1);
+        fetch(s0, sp0, sq0);
+        landed();
+        fetch(s0 + 1, sp1, sq1);
         read_q(qa, sq0, Zero{});
-        each<IP>([&](auto i) { read_p(sp0, i, Zero{}); });
-        for (int s = 0; s < steps; s += 2) {
+        each<4>([&](auto g) { read_p(sp0, g); });
+        for (int s = s0; s < s1; s += 2) {
             turn(s, sp0, sq0, sp1, sq1);
             turn(s + 1, sp1, sq1, sp0, sq0);
         }
         __syncthreads();
 
-        if (FORM == kWeightGrad) {
-            // a lane's 16 columns of row m
+        const int m0 = tm * BM + wm * (BM / WM), n0 = wn * 64;
+        int own = lane;                      // opaque: no address of it is kept from tile to tile
+        asm volatile("" : "+v"(own));
+        const int er = own & 15, eq = own >> 4;
+        if (split) {
+            // registers as they are; join_kernel reads them alike
+            f32x4 *slot = a.ws + (int64_t)(rest * plan.parts + part) * (BM * BN / 4);
+            each<IP * 4>([&](auto y) { slot[((y / 4 * 8 + wave) * 4 + y % 4) * 64 + own] = acc[y]; });
+        } else if (FORM == kWeightGrad) {
             each<IP>([&](auto i) {
-                const int m = tm * BM + wm * (BM / WM) + i * 16 + r;
-                if (m >= a.N)
-                    return;
-                float v[2][8];
-                each<16>([&](auto x) { v[x / 8][x % 8] = acc[i * 4 + x / 4][x % 4]; });
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int n = tn * BN + wn * 64 + q * 16 + h * 8;
-                    if (n < a.K)
-                        emit_weight<8>(a, ((int64_t)e * a.N + m) * a.K + n, v[h]);
-                }
+                const f32x4 v[4] = {acc[i * 4], acc[i * 4 + 1], acc[i * 4 + 2], acc[i * 4 + 3]};
+                emit_weight_row<BN>(a, x, m0 + i * 16 + er, n0 + eq * 16, v);
             });
         } else {
             // Two passes of half the wave's rows through its own part of the
-            // stages (16-byte pieces swizzled by row): a lane then has 8
-            // neighbouring columns and the epilogue's code is there once a
-            // pass, not once an accumulator (43 000 instructions otherwise).
+            // stages: the epilogue's code is there once a pass, not once an
+            // accumulator (43 000 instructions otherwise).
             constexpr int half = IP / 2 * 16;
-            int own = lane;                  // opaque: no address of it is kept from tile to tile
-            asm volatile("" : "+v"(own));
-            const int er = own & 15, eq = own >> 4;
-            uint16_t *const part = wave < 2 ? sp0 : wave < 4 ? sp1 : wave < 6 ? sq0 : sq1;
-            float *const mine = reinterpret_cast<float *>(part) + (wave & 1) * half * 64;
+            uint16_t *const stages = wave < 2 ? sp0 : wave < 4 ? sp1 : wave < 6 ? sq0 : sq1;
+            float *const mine = reinterpret_cast<float *>(stages) + (wave & 1) * half * 64;
             each<2>([&](auto h) {
                 each<IP / 2>([&](auto i) {
                     each<4>([&](auto j) {
-                        const int row = i * 16 + er, c = (eq * 4 + j) ^ er;
-                        *reinterpret_cast<f32x4 *>(mine + row * 64 + c * 4) =
+                        *reinterpret_cast<f32x4 *>(mine + (i * 16 + er) * 64 + ((eq * 4 + j) ^ er) * 4) =
                             acc[(h * (IP / 2) + i) * 4 + j];
                     });
                 });
                 __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
-                const int m0 = tm * BM + wm * (BM / WM) + h * half;
-                const int lanes = paired ? 4 : 8;             // a row
-#pragma unroll 1
-                for (int row = own / lanes; row < half; row += 64 / lanes) {
-                    const int m = m0 + row, c = (own % lanes) * (64 / lanes);
-                    if (m >= cnt)
-                        break;
-                    auto take = [&](int col, float (&v)[8]) {
-                        const float *at = mine + row * 64;
-                        const f32x4 x = *reinterpret_cast<const f32x4 *>(at + ((col / 4) ^ (row & 15)) * 4);
-                        const f32x4 y =
-                            *reinterpret_cast<const f32x4 *>(at + ((col / 4 + 1) ^ (row & 15)) * 4);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            v[i] = x[i], v[4 + i] = y[i];
-                    };
-                    float v[8], u[8];
-                    take(c, v);
-                    if (paired) {
-                        take(c + 8, u);
-                        const int f = tn * (BN / 2) + wn * 32 + c / 2;
-                        if (f < a.N / 2)
-                            emit_pair<8>(a, e, lo + m, f, v, u);
-                    } else {
-                        const int n = tn * BN + wn * 64 + c;
-                        if (n < a.N)
-                            emit<8>(a, e, lo + m, n, v);
-                    }
-                }
+                emit_rows<BN>(a, x, mine, half, m0 + h * half, n0, own);
                 __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
             });
             __syncthreads();       // the next tile's stages overwrite the other waves' parts
+        }
+    }
+}
+
+// Adds the parts of the tiles that tile_kernel<BM, BN, FORM> split, in order,
+// and runs their epilogue. A workgroup takes one 16-row piece of each wave
+// (blockIdx.x) of tiles blockIdx.y, + gridDim.y, ..; `grid` is the tile
+// kernel's.
+template <int BM, int BN, Form FORM>
+__global__ __launch_bounds__(kTileThreads) void join_kernel(Args a, int grid)
+{
+    constexpr int WN = BN / 64, WM = 8 / WN;
+    __shared__ __align__(16) float rows[FORM == kWeightGrad ? 4 : 8 * 16 * 64];
+    __shared__ int32_t pre[FORM == kWeightGrad ? 1 : kMaxExperts + 1];
+    __shared__ int32_t sums[8];
+    const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, q = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave / WN, wn = wave % WN;
+    const int i = blockIdx.x;
+    const int ntn = FORM == kWeightGrad ? (a.K + BN - 1) / BN : (a.N + BN - 1) / BN;
+    const int ntm = FORM == kWeightGrad ? (a.N + BM - 1) / BM : 0;
+    if (FORM != kWeightGrad)
+        tile_prefix<BM>(a, pre, sums);
+    const Plan plan = plan_of(a, FORM == kWeightGrad ? (int64_t)a.E * ntm * ntn : (int64_t)pre[a.E] * ntn,
+                              grid);
+    for (int l = blockIdx.y; l < plan.left; l += gridDim.y) {
+        const Tile x = locate<FORM>(a, pre, plan.whole + l, ntm, ntn);
+        const f32x4 *slot = a.ws + (int64_t)l * plan.parts * (BM * BN / 4) + ((i * 8 + wave) * 4) * 64 + lane;
+        f32x4 acc[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            acc[j] = slot[j * 64];
+        for (int p = 1; p < plan.parts; ++p) {
+            slot += BM * BN / 4;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                acc[j] += slot[j * 64];
+        }
+        const int m0 = x.tm * BM + wm * (BM / WM) + i * 16, n0 = wn * 64;
+        if (FORM == kWeightGrad) {
+            emit_weight_row<BN>(a, x, m0 + r, n0 + q * 16, acc);
+        } else {
+            float *mine = rows + wave * 16 * 64;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<f32x4 *>(mine + r * 64 + ((q * 4 + j) ^ r) * 4) = acc[j];
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+            emit_rows<BN>(a, x, mine, 16, m0, n0, lane);
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
         }
     }
 }

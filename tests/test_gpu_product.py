@@ -89,9 +89,13 @@ def filled(shape, dtype, seed):
     return t
 
 
+def workspace(nbytes):
+    return redzones.poisoned(nbytes, torch.uint8, 0x5A, DEV) if nbytes else None
+
+
 def check_product(counts, K, N, act="none", bias=False, residual=False, pre=False,
                   transposed=False, out=torch.bfloat16, gap=0, expected=0, seed=0, rows=None,
-                  starts=None, in_place=False):
+                  starts=None, in_place=False, split=True):
     E = len(counts)
     made, total = blocks(counts, gap)
     starts = made if starts is None else starts
@@ -122,7 +126,7 @@ def check_product(counts, K, N, act="none", bias=False, residual=False, pre=Fals
                     1 if out == torch.bfloat16 else 0, 0)
     d = lambda t: None if t is None else t.to(DEV)  # noqa: E731
     epl.epl_expert_product(p, d(x), d(w), d(b), y if in_place else d(res), i32(starts),
-                           i32(counts), z_out, y)
+                           i32(counts), z_out, y, workspace(epl.epl_product_workspace_bytes(p)) if split else None)
     got = y.cpu()
     assert torch.equal(got[~owned].view(torch.int16 if out == torch.bfloat16 else torch.int32),
                        before[~owned].view(torch.int16 if out == torch.bfloat16 else torch.int32))
@@ -193,6 +197,28 @@ def test_forward_sizes(K, N, expected):
 def test_transposed_sizes(K, N, expected):
     counts = FEW if expected else MANY + [700] * 3
     check_product(counts, K, N, transposed=True, expected=expected, seed=K + 1)
+
+
+# Sums split over workgroups and joined: one tile to several rounds and a few
+# tiles left, odd numbers of stages, parts of different length, tiles without
+# rows; and the same without a workspace.
+@pytest.mark.parametrize("split", [True, False])
+@pytest.mark.parametrize("transposed", [False, True])
+@pytest.mark.parametrize("counts,K,N,act", [
+    ([300], 4096, 256, "none"), ([129], 2056, 128, "swiglu"), ([70, 0, 300, 200], 1288, 520, "gelu"),
+    ([256] * 3, 520, 1024, "silu"), ([140] * 40, 1032, 1808, "none"),
+    ([5000], 1160, 3600, "swiglu_grad"), ([100, 90], 8200, 64, "silu_grad")])
+def test_split_contraction(counts, K, N, act, transposed, split):
+    grad = act.endswith("_grad")
+    check_product(counts, K, N, act, transposed=transposed, bias=not grad, residual=not grad,
+                  pre=True, seed=11, split=split)
+
+
+@pytest.mark.parametrize("counts,N,K,accumulate", [
+    ([4000], 64, 72, False), ([3000, 0, 1500], 272, 520, True), ([700, 900], 1040, 264, False),
+    ([20000], 512, 128, True), ([513] * 12, 528, 1032, False)])
+def test_split_rows(counts, N, K, accumulate):
+    check_weight_grad(counts, N, K, accumulate=accumulate, seed=5)
 
 
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
@@ -321,7 +347,7 @@ def check_weight_grad(counts, N, K, out=torch.float32, bias=True, accumulate=Fal
     w0, b0 = dw.cpu().double(), None if db is None else db.cpu().double()
     p = epl.Product(total, 0, E, K, N, 0, 0, 1 if out == torch.bfloat16 else 0, 0)
     epl.epl_expert_weight_grad(p, d.to(DEV), x.to(DEV), i32(starts), i32(counts), accumulate, dw,
-                               db)
+                               db, workspace(epl.epl_weight_grad_workspace_bytes(p)))
     for e in range(E):
         lo, hi = max(starts[e], 0), max(min(starts[e] + counts[e], total), 0)
         hi = max(hi, lo)

@@ -101,31 +101,32 @@ def test_product_accepts(lib, kw):
 def test_product_refuses(lib, kw):
     p = product(**kw)
     assert epl.epl_product_validate(p) == epl.EPL_EINVAL
-    assert lib.epl_expert_product(ctypes.byref(p), *[PTR] * 8, NUL) == epl.EPL_EINVAL
+    assert lib.epl_expert_product(ctypes.byref(p), *[PTR] * 9, NUL) == epl.EPL_EINVAL
     assert lib.epl_expert_weight_grad(ctypes.byref(p), PTR, PTR, PTR, PTR, 0, PTR, NUL,
-                                      NUL) == epl.EPL_EINVAL
+                                      NUL, NUL) == epl.EPL_EINVAL
 
 
 def test_product_pointers(lib):
     p = ctypes.byref(product())
-    # x, weight, bias, residual, start, count, pre, y
-    good = [PTR, PTR, NUL, NUL, PTR, PTR, NUL, PTR]
-    bads = [(i, NUL) for i in (0, 1, 4, 5, 7)] + [(i, ODD) for i in range(8)]
+    # x, weight, bias, residual, start, count, pre, y, workspace
+    good = [PTR, PTR, NUL, NUL, PTR, PTR, NUL, PTR, NUL]
+    bads = [(i, NUL) for i in (0, 1, 4, 5, 7)] + [(i, ODD) for i in range(9)]
     for i, bad in bads:
         args = list(good)
         args[i] = bad
         assert lib.epl_expert_product(p, *args, NUL) == epl.EPL_EINVAL, (i, bad)
     for act in (epl.EPL_ACT_SILU_GRAD, epl.EPL_ACT_GELU_GRAD, epl.EPL_ACT_SWIGLU_GRAD):
         g = ctypes.byref(product(activation=act))
-        for args in ([PTR, PTR, NUL, NUL, PTR, PTR, NUL, PTR],      # no pre
-                     [PTR, PTR, PTR, NUL, PTR, PTR, PTR, PTR],      # a bias
-                     [PTR, PTR, NUL, PTR, PTR, PTR, PTR, PTR]):     # a residual
+        for args in ([PTR, PTR, NUL, NUL, PTR, PTR, NUL, PTR, NUL],      # no pre
+                     [PTR, PTR, PTR, NUL, PTR, PTR, PTR, PTR, NUL],      # a bias
+                     [PTR, PTR, NUL, PTR, PTR, PTR, PTR, PTR, NUL]):     # a residual
             assert lib.epl_expert_product(g, *args, NUL) == epl.EPL_EINVAL
     empty = ctypes.byref(product(num_rows=0))
-    assert lib.epl_expert_product(empty, NUL, PTR, NUL, NUL, PTR, PTR, NUL, NUL, NUL) == epl.EPL_OK
-    # grad, x, start, count, accumulate, grad_weight, grad_bias
-    good = [PTR, PTR, PTR, PTR, 0, PTR, NUL]
-    for i, bad in [(i, NUL) for i in (0, 1, 2, 3, 5)] + [(i, ODD) for i in (0, 1, 2, 3, 5, 6)] + \
+    assert lib.epl_expert_product(empty, NUL, PTR, NUL, NUL, PTR, PTR, NUL, NUL, NUL,
+                                  NUL) == epl.EPL_OK
+    # grad, x, start, count, accumulate, grad_weight, grad_bias, workspace
+    good = [PTR, PTR, PTR, PTR, 0, PTR, NUL, NUL]
+    for i, bad in [(i, NUL) for i in (0, 1, 2, 3, 5)] + [(i, ODD) for i in (0, 1, 2, 3, 5, 6, 7)] + \
             [(4, 2), (4, -1)]:
         args = list(good)
         args[i] = bad
@@ -133,6 +134,21 @@ def test_product_pointers(lib):
     for kw in (dict(activation=1), dict(weight_layout=1)):
         assert lib.epl_expert_weight_grad(ctypes.byref(product(**kw)), *good,
                                           NUL) == epl.EPL_EINVAL
+
+
+def test_product_workspace_sizes(lib):
+    """Partial tiles: none for few rows or a short contraction, else at most
+    256 of 256 KB."""
+    size = epl.epl_product_workspace_bytes
+    assert size(product()) == 0 and size(product(in_cols=12)) == 0
+    big = dict(num_rows=32768, in_cols=7168, out_cols=4096)
+    assert size(product(**big)) == 256 * 256 * 256 * 4
+    assert size(product(expected_rows=8, **big)) == 0
+    assert size(product(num_rows=800, in_cols=512, out_cols=256)) == (800 // 128 + 8) * 2 * 128 * 1024
+    grad = epl.epl_weight_grad_workspace_bytes
+    assert grad(product(**big)) == 256 * 256 * 256 * 4
+    assert grad(product(num_rows=800, in_cols=512, out_cols=256)) == 0
+    assert grad(product(num_rows=8 * 512, in_cols=64, out_cols=512)) == 8 * 2 * 2 * 128 * 1024
 
 
 def test_combine_backward_arguments(lib):
