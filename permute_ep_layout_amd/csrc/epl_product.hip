@@ -16,6 +16,10 @@ bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 
 int launch_status() { return hipGetLastError() == hipSuccess ? EPL_OK : EPL_EHIP; }
 
+// Rows an expert, on average, up to which the weights are read straight from
+// memory.
+constexpr int64_t kFewRows = 12;
+
 // Offsets within one expert's weight and within a tile are 32-bit.
 constexpr int32_t kMaxCols = 1 << 20;
 constexpr int64_t kMaxWeight = int64_t(1) << 29;
@@ -47,40 +51,56 @@ bool desc_ok(const epl_product_desc *p)
     return p->weight_layout == EPL_WEIGHT_OUT_IN || p->weight_layout == EPL_WEIGHT_IN_OUT;
 }
 
+// CUs that a launch counts on, at most (and those of an MI355X).
+constexpr int kCus = 256;
+
 int num_cus()
 {
     int dev = 0, n = 0;
     if (hipGetDevice(&dev) != hipSuccess ||
         hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n < 1) {
         (void)hipGetLastError();
-        return 256;
+        return kCus;
     }
-    return n;
+    return std::min(n, kCus);
 }
 
-// The kernel that a product takes. The counts are on the GPU: the choice goes
-// by the rows that the caller expects an expert to have on average.
-enum Kind { kFew, kSquare, kWide, kTall };       // tiles 256 x 256, 128 x 256, 256 x 128
+// The kernel that a product takes: straight from memory for a few rows, or
+// tiles of 256 x 256 or 128 x 128. The counts are on the GPU, so the choice
+// goes by the rows that the caller expects an expert to have on average.
+enum Kind { kFew, kLarge, kSmall };
+
+// Large tiles read the operands half as often as small ones, which come in
+// four times the number and share a CU in pairs. Measured (large, small), us:
+// 8 experts of 4096 rows, 7168 -> 4096: 1474, 1811; 64 of 192, 4096 -> 2048:
+// 277, 320; 8 of 256, 7168 -> 4096 (128 tiles): 149, 158; but 64 of 128:
+// 256, 218; 1 of 1000, 4096 -> 1024 (16 tiles): 37, 26; 16 of 500, 512 ->
+// 640 (96 tiles): 38, 21.
+Kind tiles_for(int64_t m, int64_t n, int64_t experts)
+{
+    const int64_t large = experts * ((m + 255) / 256) * ((n + 255) / 256);
+    // (and not where the last 256 columns of a few hold 128 at most)
+    const bool empty = n < 1024 && n % 256 >= 1 && n % 256 <= 128;
+    return m > 128 && large >= kCus / 2 && !empty ? kLarge : kSmall;
+}
+
+int64_t average_rows(const epl_product_desc &p)
+{
+    const int64_t rows = p.expected_rows > 0 ? std::min(p.expected_rows, p.num_rows) : p.num_rows;
+    return (rows + p.num_experts - 1) / p.num_experts;
+}
 
 Kind kind_of(const epl_product_desc &p)
 {
-    const int64_t rows = p.expected_rows > 0 ? std::min(p.expected_rows, p.num_rows) : p.num_rows;
-    const int64_t avg = (rows + p.num_experts - 1) / p.num_experts;
-    if (p.weight_layout == EPL_WEIGHT_OUT_IN && avg <= 64)
+    const int64_t avg = average_rows(p);
+    if (p.weight_layout == EPL_WEIGHT_OUT_IN && avg <= kFewRows)
         return kFew;
-    // half of the last 256 columns empty, or of the rows
-    if (p.out_cols % 256 != 0 && p.out_cols % 256 <= 128 && p.out_cols < 1024)
-        return kTall;
-    return avg <= 128 ? kWide : kSquare;
+    return tiles_for(avg, p.out_cols, p.num_experts);
 }
 
-Kind grad_kind_of(const epl_product_desc &p)
-{
-    return p.out_cols <= 128 ? kWide : p.in_cols <= 128 ? kTall : kSquare;
-}
+Kind grad_kind_of(const epl_product_desc &p) { return tiles_for(p.out_cols, p.in_cols, p.num_experts); }
 
-int rows_of(Kind k) { return k == kWide ? 128 : 256; }
-int cols_of(Kind k) { return k == kTall ? 128 : 256; }
+int side_of(Kind k) { return k == kSmall ? 128 : 256; }
 
 // Parts that a contraction of `depth` is worth being split into: at least
 // four stages each.
@@ -96,39 +116,39 @@ size_t tile_workspace(Kind k, int64_t tiles, int parts)
 {
     if (k == kFew || parts < 2)
         return 0;
-    const int64_t slots = std::min<int64_t>(P::kSlots, tiles * parts);
-    return (size_t)slots * rows_of(k) * cols_of(k) * sizeof(float);
+    const int64_t slots = std::min<int64_t>(kCus * P::tile_groups(side_of(k)), tiles * parts);
+    return (size_t)slots * side_of(k) * side_of(k) * sizeof(float);
 }
 
 int64_t product_tiles(const epl_product_desc &p, Kind k)
 {
-    return (p.num_rows / rows_of(k) + p.num_experts) * ((p.out_cols + cols_of(k) - 1) / cols_of(k));
+    return (p.num_rows / side_of(k) + p.num_experts) * ((p.out_cols + side_of(k) - 1) / side_of(k));
 }
 
 int64_t grad_tiles(const epl_product_desc &p, Kind k)
 {
-    return (int64_t)p.num_experts * ((p.out_cols + rows_of(k) - 1) / rows_of(k)) *
-           ((p.in_cols + cols_of(k) - 1) / cols_of(k));
+    return (int64_t)p.num_experts * ((p.out_cols + side_of(k) - 1) / side_of(k)) *
+           ((p.in_cols + side_of(k) - 1) / side_of(k));
 }
 
 // `tiles`: how many there are, or at most are.
-template <int BM, int BN, P::Form FORM>
+template <int SIDE, P::Form FORM>
 int launch_tiles(const P::Args &a, int64_t tiles, hipStream_t s)
 {
-    // one workgroup a CU, striding over the tiles; also with fewer tiles
-    // where their contraction can be split
+    // every workgroup that the CUs hold at once, striding over the tiles;
+    // also with fewer tiles where their contraction can be split
     const bool split = a.ws && a.max_parts > 1;
-    const int cus = std::min(num_cus(), P::kSlots);
-    const int grid = (int)(split ? std::min<int64_t>(tiles * a.max_parts, cus)
-                                 : std::min<int64_t>(tiles, cus));
-    hipLaunchKernelGGL((P::tile_kernel<BM, BN, FORM>), dim3((unsigned)grid), dim3(P::kTileThreads), 0,
-                       s, a);
+    constexpr int threads = P::tile_threads(SIDE);
+    const int most = num_cus() * P::tile_groups(SIDE);
+    const int grid = (int)std::min<int64_t>(split ? tiles * a.max_parts : tiles, most);
+    hipLaunchKernelGGL((P::tile_kernel<SIDE, SIDE, FORM>), dim3((unsigned)grid), dim3(threads), 0, s, a);
     int rc = launch_status();
     if (rc == EPL_OK && split) {
-        constexpr int pieces = BM / (8 / (BN / 64)) / 16;
-        hipLaunchKernelGGL((P::join_kernel<BM, BN, FORM>),
-                           dim3(pieces, (unsigned)std::max<int64_t>(1, std::min<int64_t>(tiles, grid / 2))),
-                           dim3(P::kTileThreads), 0, s, a, grid);
+        constexpr int pieces = SIDE / P::kWavesM / 16;
+        const int64_t most_left = std::min<int64_t>(tiles, grid / 2);
+        hipLaunchKernelGGL((P::join_kernel<SIDE, SIDE, FORM>),
+                           dim3(pieces, (unsigned)std::max<int64_t>(1, most_left)), dim3(threads), 0, s,
+                           a, grid);
         rc = launch_status();
     }
     return rc;
@@ -137,14 +157,7 @@ int launch_tiles(const P::Args &a, int64_t tiles, hipStream_t s)
 template <P::Form FORM>
 int launch_kind(Kind k, const P::Args &a, int64_t tiles, hipStream_t s)
 {
-    switch (k) {
-    case kWide:
-        return launch_tiles<128, 256, FORM>(a, tiles, s);
-    case kTall:
-        return launch_tiles<256, 128, FORM>(a, tiles, s);
-    default:
-        return launch_tiles<256, 256, FORM>(a, tiles, s);
-    }
+    return k == kSmall ? launch_tiles<128, FORM>(a, tiles, s) : launch_tiles<256, FORM>(a, tiles, s);
 }
 
 }  // namespace
@@ -205,9 +218,13 @@ int epl_expert_product(const epl_product_desc *p, const uint16_t *x, const uint1
     hipStream_t s = static_cast<hipStream_t>(stream);
     const Kind k = kind_of(*p);
     if (k == kFew) {
+        // 16 waves a workgroup where 4 would leave the GPU mostly empty
         const int nb = a.act == EPL_ACT_SWIGLU ? (a.N / 2 + 15) / 16 : (a.N + 31) / 32;
-        hipLaunchKernelGGL(P::few_rows_kernel, dim3((unsigned)nb, (unsigned)a.E),
-                           dim3(P::kFewThreads), 0, s, a);
+        const dim3 grid((unsigned)nb, (unsigned)a.E);
+        if ((int64_t)nb * a.E <= kCus)
+            hipLaunchKernelGGL((P::few_rows_kernel<16>), grid, dim3(1024), 0, s, a);
+        else
+            hipLaunchKernelGGL((P::few_rows_kernel<4>), grid, dim3(256), 0, s, a);
         return launch_status();
     }
     a.max_parts = max_parts(a.K);
@@ -247,9 +264,9 @@ int epl_expert_weight_grad(const epl_product_desc *p, const uint16_t *grad, cons
     hipStream_t s = static_cast<hipStream_t>(stream);
     const Kind k = grad_kind_of(*p);
     const int64_t tiles = grad_tiles(*p, k);
-    const int cus = std::min(num_cus(), P::kSlots);
     // no tile is left over, or too many to share out: nothing to join
-    const bool even = tiles >= cus && (tiles % cus == 0 || tiles % cus > cus / 2);
+    const int64_t round = num_cus() * P::tile_groups(side_of(k));
+    const bool even = tiles >= round && (tiles % round == 0 || tiles % round > round / 2);
     a.max_parts = max_parts(grad_depth(*p));
     a.ws = a.max_parts > 1 && !even ? static_cast<P::f32x4 *>(workspace) : nullptr;
     int rc = launch_kind<P::kWeightGrad>(k, a, tiles, s);

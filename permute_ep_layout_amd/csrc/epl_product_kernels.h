@@ -30,11 +30,17 @@ typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 constexpr int kMaxExperts = 2048;
-constexpr int kTileThreads = 512;      // 8 waves: one workgroup fills a CU's four SIMDs twice
 constexpr int kTileK = 64;             // contraction depth of one LDS stage
 constexpr int kNumXcd = 8;
 constexpr int kMaxParts = 16;          // parts that a tile's contraction is split into, at most
-constexpr int kSlots = 256;            // partial tiles of a workspace, at most
+
+// Waves along m and n of a tile's workgroup: a wave has half of its rows and
+// 64 of its columns. Tiles of 256 x 256 take 8 waves, those of 128 x 128 four
+// and two of their workgroups fit a CU.
+constexpr int kWavesM = 2;
+constexpr int waves_n(int bn) { return bn / 64; }
+constexpr int tile_threads(int bn) { return kWavesM * waves_n(bn) * 64; }
+constexpr int tile_groups(int bn) { return 512 / tile_threads(bn); }    // a CU
 
 struct Args {
     const __bf16 *p;          // rows (forward, data gradient) or d rows (weight gradient)
@@ -277,27 +283,23 @@ __device__ __forceinline__ void emit_weight(const Args &a, int64_t at, float (&v
 
 // ----------------------------------------------------------- tile kernel --
 //
-// A workgroup of 8 waves computes BM x BN outputs, 64 deep at a time, from
-// two LDS stages that buffer loads fill directly (16 bytes a lane) while the
-// other stage is multiplied. Q is the matrix instruction's A operand and P
-// its B operand, so a lane's accumulator registers run along n, the
-// contiguous index of the output: with the rows of Q taken in the order
-//     n(r, j) = (r / 4) * 16 + j * 4 + r % 4      (r: lane % 16, j: 0 .. 3)
-// the 16 values of a lane are 16 neighbouring columns, and a row leaves as
-// 128 contiguous bytes of bf16 without a pass through LDS.
+// A workgroup of 8 (or 4) waves computes BM x BN outputs, 64 deep at a time,
+// from two LDS stages that buffer loads fill directly (16 bytes a lane) while
+// the other stage is multiplied. Q is the matrix instruction's A operand and
+// P its B operand, so a lane's accumulator registers run along n, the
+// contiguous index of the output: register quad (i, j) of lane 16 q + r holds
+// row 16 i + r, columns 16 j + 4 q .. + 3 of the wave's part.
 //
 // LDS layouts (XOR swizzles on 16-byte pieces so that the 16 lanes of a read
 // fall on different banks; a DMA writes LDS in lane order, so the swizzle is
 // applied to the global address that the lane reads):
-//   contiguous operand: [rows][64], piece c of row r at c ^ f(r)
-//   strided operand:    [64][cols], piece c of row k at c ^ g(k), read with
-//                       ds_read_b64_tr_b16, which hands lane r column r of a
-//                       4-row block, 4 consecutive k
+//   contiguous operand: [rows][64], piece c of row r at c ^ swz(r)
+//   strided operand:    [64][cols], piece c of row k at c ^ swz_t(k), read
+//                       with ds_read_b64_tr_b16, which hands lane r column r
+//                       of a 4-row block, 4 consecutive k
 
-__device__ __forceinline__ int swz_p(int row) { return (row >> 1) & 7; }
-__device__ __forceinline__ int swz_q(int row) { return ((row >> 1) & 1) | (((row >> 4) & 3) << 1); }
-__device__ __forceinline__ int swz_pt(int k) { return ((k & 3) << 1) | (((k >> 3) & 1) << 3); }
-__device__ __forceinline__ int swz_qt(int k) { return (k & 1) | (((k >> 1) & 1) << 3); }
+__device__ __forceinline__ int swz(int row) { return (row >> 1) & 7; }
+__device__ __forceinline__ int swz_t(int k) { return ((k & 3) << 1) | (((k >> 3) & 1) << 3); }
 
 // A buffer descriptor of `bytes` bytes from `base`: a lane that reads beyond
 // them gets zeros.
@@ -338,42 +340,52 @@ __device__ __forceinline__ bf16x8 read_tr(const uint16_t *at)
     return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
+// `elements` behind the lane's byte offset into a stage.
+__device__ __forceinline__ const uint16_t *at(const uint16_t *stage, int bytes, int elements)
+{
+    return reinterpret_cast<const uint16_t *>(reinterpret_cast<const char *>(stage) + bytes) + elements;
+}
+
+// offset ^= by, in place: the compiler must not keep a register for every value
+// (with those the weight gradient's loop spills: 1.86 ms against 1.35 for
+// 29765 rows of 7168 x 4096).
+__device__ __forceinline__ void walk(int &offset, int by)
+{
+    offset ^= by;
+    asm("" : "+v"(offset));
+}
+
 enum Form { kForward, kDataGrad, kWeightGrad };
 
-// The m tiles of the experts before each expert, for experts in LDS order.
-template <int BM>
+// The m tiles of the experts before each expert, and of all of them.
+template <int BM, int THREADS>
 __device__ __forceinline__ void tile_prefix(const Args &a, int32_t *pre, int32_t *sums)
 {
-    constexpr int per = kMaxExperts / kTileThreads;
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-    int n[per], own = 0;
-#pragma unroll
-    for (int i = 0; i < per; ++i) {
-        const int e = t * per + i;
+    int base = 0;
+    for (int e0 = 0; e0 < a.E; e0 += THREADS) {
+        const int e = e0 + t;
         int64_t lo;
-        n[i] = e < a.E ? (block_of(a, e, lo) + BM - 1) / BM : 0;
-        own += n[i];
+        const int own = e < a.E ? (block_of(a, e, lo) + BM - 1) / BM : 0;
+        int up = own;
+        for (int d = 1; d < 64; d <<= 1) {
+            const int v = __shfl_up(up, d);
+            up += lane >= d ? v : 0;
+        }
+        if (lane == 63)
+            sums[wave] = up;
+        __syncthreads();
+        int before = base;
+        for (int w = 0; w < THREADS / 64; ++w) {
+            before += w < wave ? sums[w] : 0;
+            base += sums[w];
+        }
+        if (e < a.E)
+            pre[e] = before + up - own;
+        __syncthreads();
     }
-    int up = own;
-    for (int d = 1; d < 64; d <<= 1) {
-        const int v = __shfl_up(up, d);
-        up += lane >= d ? v : 0;
-    }
-    if (lane == 63)
-        sums[wave] = up;
-    __syncthreads();
-    int before = up - own;
-    for (int w = 0; w < wave; ++w)
-        before += sums[w];
-#pragma unroll
-    for (int i = 0; i < per; ++i) {
-        const int e = t * per + i;
-        if (e <= a.E)
-            pre[e] = before;
-        before += n[i];
-    }
-    if (t == kTileThreads - 1 && a.E == kMaxExperts)
-        pre[a.E] = before;
+    if (t == 0)
+        pre[a.E] = base;
     __syncthreads();
 }
 
@@ -391,7 +403,7 @@ __device__ __forceinline__ Plan plan_of(const Args &a, int64_t tiles, int grid)
 {
     Plan p{tiles, 0, 1};
     const int left = (int)(tiles % grid);
-    const int parts = a.ws && left > 0 ? min(min(grid, kSlots) / left, a.max_parts) : 1;
+    const int parts = a.ws && left > 0 ? min(grid / left, a.max_parts) : 1;
     if (parts > 1)
         p = Plan{tiles - left, left, parts};
     return p;
@@ -436,71 +448,81 @@ __device__ __forceinline__ Tile locate(const Args &a, const int32_t *pre, int64_
     return x;
 }
 
+// A register quad of a wave's rows into its part of LDS, [rows][64] with
+// 16-byte pieces swizzled by row.
+__device__ __forceinline__ void put(float *mine, int row, int piece, f32x4 v)
+{
+    *reinterpret_cast<f32x4 *>(mine + row * 64 + (piece ^ (row & 15)) * 4) = v;
+}
+
+template <int C>
+__device__ __forceinline__ void take(const float *mine, int row, int col, float (&v)[C])
+{
+#pragma unroll
+    for (int i = 0; i < C; i += 4) {
+        const f32x4 x =
+            *reinterpret_cast<const f32x4 *>(mine + row * 64 + (((col + i) / 4) ^ (row & 15)) * 4);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            v[i + j] = x[j];
+    }
+}
+
 // The epilogue of `rows` rows of 64 columns that a wave holds in its part of
-// LDS (16-byte pieces swizzled by row): a lane takes 8 neighbouring columns,
-// or 8 of the gate and 8 of the up half. m0: the first of them in the
-// expert's block; n0: the first column in the tile's columns.
-template <int BN>
+// LDS: a lane takes 8 neighbouring columns, or 8 of the gate and 8 of the up
+// half, or 4 of a weight gradient in binary32, so that rows leave in whole
+// lines. m0: the first of them in the tile's block; n0: the first column in
+// the tile's columns.
+template <int BN, Form FORM>
 __device__ __forceinline__ void emit_rows(const Args &a, const Tile &x, const float *mine, int rows,
                                           int m0, int n0, int lane)
 {
     const bool paired = a.act == EPL_ACT_SWIGLU;
-    const int lanes = paired ? 4 : 8;             // a row
+    const bool four = FORM == kWeightGrad && a.out_f32;
+    const int lanes = four ? 16 : paired ? 4 : 8;             // a row
+    const int last = FORM == kWeightGrad ? a.N : x.cnt;
 #pragma unroll 1
     for (int row = lane / lanes; row < rows; row += 64 / lanes) {
-        const int m = m0 + row, c = (lane % lanes) * (64 / lanes);
-        if (m >= x.cnt)
+        const int m = m0 + row, c = (lane % lanes) * (64 / lanes), n = x.tn * BN + n0 + c;
+        if (m >= last)
             break;
-        auto take = [&](int col, float (&v)[8]) {
-            const float *at = mine + row * 64;
-            const f32x4 y = *reinterpret_cast<const f32x4 *>(at + ((col / 4) ^ (row & 15)) * 4);
-            const f32x4 z = *reinterpret_cast<const f32x4 *>(at + ((col / 4 + 1) ^ (row & 15)) * 4);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                v[i] = y[i], v[4 + i] = z[i];
-        };
+        if (FORM == kWeightGrad) {
+            if (n >= a.K)
+                continue;
+            const int64_t at = ((int64_t)x.e * a.N + m) * a.K + n;
+            if (four) {
+                float v[4];
+                take<4>(mine, row, c, v);
+                emit_weight<4>(a, at, v);
+            } else {
+                float v[8];
+                take<8>(mine, row, c, v);
+                emit_weight<8>(a, at, v);
+            }
+            continue;
+        }
         float v[8], u[8];
-        take(c, v);
+        take<8>(mine, row, c, v);
         if (paired) {
-            take(c + 8, u);
-            const int f = (x.tn * BN + n0 + c) / 2;
-            if (f < a.N / 2)
-                emit_pair<8>(a, x.e, x.lo + m, f, v, u);
-        } else {
-            const int n = x.tn * BN + n0 + c;
-            if (n < a.N)
-                emit<8>(a, x.e, x.lo + m, n, v);
+            take<8>(mine, row, c + 8, u);
+            if (n / 2 < a.N / 2)
+                emit_pair<8>(a, x.e, x.lo + m, n / 2, v, u);
+        } else if (n < a.N) {
+            emit<8>(a, x.e, x.lo + m, n, v);
         }
     }
 }
 
-// A lane's 16 columns of one row of a weight gradient.
-template <int BN>
-__device__ __forceinline__ void emit_weight_row(const Args &a, const Tile &x, int m, int n0,
-                                                const f32x4 (&acc)[4])
-{
-    if (m >= a.N)
-        return;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int n = x.tn * BN + n0 + h * 8;
-        float v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] = acc[h * 2 + i / 4][i % 4];
-        if (n < a.K)
-            emit_weight<8>(a, ((int64_t)x.e * a.N + m) * a.K + n, v);
-    }
-}
-
 template <int BM, int BN, Form FORM>
-__global__ __launch_bounds__(kTileThreads) void tile_kernel(Args a)
+__global__ __launch_bounds__(tile_threads(BN), 2) void tile_kernel(Args a)
 {
     constexpr bool PT = FORM == kWeightGrad;             // P strided
     constexpr bool QT = FORM != kForward;                // Q strided
-    constexpr int WN = BN / 64, WM = 8 / WN;             // waves along n and m
+    constexpr int WN = waves_n(BN), WM = kWavesM, WAVES = WM * WN;
     constexpr int IP = BM / WM / 16;                     // 16-row pieces of P a wave
-    constexpr int ISP = BM / 64, ISQ = BN / 64;          // DMAs a stage
+    constexpr int ROWS = WAVES * 8;                      // rows of a contiguous operand a DMA
+    constexpr int ISP = BM / ROWS, ISQ = BN / ROWS;      // DMAs a stage
+    constexpr int KP = WAVES * 512 / BM, KQ = WAVES * 512 / BN;    // rows of a strided one
     __shared__ __align__(1024) uint16_t sp0[BM * kTileK], sp1[BM * kTileK];
     __shared__ __align__(1024) uint16_t sq0[BN * kTileK], sq1[BN * kTileK];
     __shared__ int32_t pre[FORM == kWeightGrad ? 1 : kMaxExperts + 1];
@@ -512,19 +534,20 @@ __global__ __launch_bounds__(kTileThreads) void tile_kernel(Args a)
     const int wm = wave / WN, wn = wave % WN, r = lane & 15, q = lane >> 4;
     const bool paired = a.act == EPL_ACT_SWIGLU;
 
-    // The lane's LDS offsets (elements) of its first pieces; the others lie at
-    // fixed distances, since the swizzles use none of the bits that j, i, and
-    // (for strided operands) the 32-deep half and u change. A strided Q has
-    // one offset for each piece of 8 columns, a strided P an exclusive or.
+    // The lane's LDS offsets (bytes) of its first pieces; the others lie at
+    // fixed distances, since the swizzles use none of the bits that the piece
+    // and (for strided operands) the 32-deep half change; those of a strided
+    // operand by an exclusive or, for which the offset walks from piece to
+    // piece and comes back to the first.
     int aq[2], ap[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const int n = wn * 64 + (r >> 2) * 16 + (r & 3), m = wm * (BM / WM) + r;
-        const int k = q * 8 + (r >> 2);
-        aq[h] = QT ? k * BN + ((wn * 8 + (r & 3) * 2 + h) ^ swz_qt(k)) * 8
-                   : n * kTileK + ((h * 4 + q) ^ swz_q(n)) * 8;
-        ap[h] = PT ? k * BM + ((wm * (BM / WM / 8) + ((r & 3) >> 1)) ^ swz_pt(k)) * 8 + (r & 1) * 4
-                   : m * kTileK + ((h * 4 + q) ^ swz_p(m)) * 8;
+        const int n = wn * 64 + r, m = wm * (BM / WM) + r;
+        const int k = q * 8 + (r >> 2), c = (r & 3) >> 1;
+        aq[h] = 2 * (QT ? k * BN + ((wn * 8 + c) ^ swz_t(k)) * 8 + (r & 1) * 4
+                        : n * kTileK + ((h * 4 + q) ^ swz(n)) * 8);
+        ap[h] = 2 * (PT ? k * BM + ((wm * (BM / WM / 8) + c) ^ swz_t(k)) * 8 + (r & 1) * 4
+                        : m * kTileK + ((h * 4 + q) ^ swz(m)) * 8);
     }
 
     // tiles along m and n, over all experts
@@ -535,7 +558,7 @@ __global__ __launch_bounds__(kTileThreads) void tile_kernel(Args a)
         ntm = (a.N + BM - 1) / BM;
         total = (int64_t)a.E * ntm * ntn;
     } else {
-        tile_prefix<BM>(a, pre, sums);
+        tile_prefix<BM, WAVES * 64>(a, pre, sums);
         total = (int64_t)pre[a.E] * ntn;
     }
 
@@ -556,6 +579,9 @@ __global__ __launch_bounds__(kTileThreads) void tile_kernel(Args a)
         const int e = x.e, cnt = x.cnt, tm = x.tm, tn = x.tn;
         const int64_t lo = x.lo;
 
+        // opaque: what is derived from the lane for one tile is not kept for the next
+        int own = tid;
+        asm volatile("" : "+v"(own));
         // Operands: base, the lane's offset, and the bytes between the DMAs of
         // a stage. Their ends: a strided operand ends with its rows of the
         // contraction; a contiguous one with its last row, and pieces beyond
@@ -576,28 +602,28 @@ __global__ __launch_bounds__(kTileThreads) void tile_kernel(Args a)
         uint32_t op, oq;
         int np = 0, nq = 0;                  // bytes of a contiguous operand
         int kp = 0, kq = 0;                  // contraction index of the lane's piece
-        const int ip = PT ? 4096 / BM * a.N * 2 : 64 * a.K * 2;
-        const int iq = QT ? 4096 / BN * qcols * 2 : (paired ? 32 : 64) * a.K * 2;
+        const int ip = PT ? KP * a.N * 2 : ROWS * a.K * 2;
+        const int iq = QT ? KQ * qcols * 2 : (paired ? ROWS / 2 : ROWS) * a.K * 2;
         if (PT) {
-            const int k = (tid * 8) / BM, c = ((tid * 8 % BM) / 8) ^ swz_pt(k);
+            const int k = (own * 8) / BM, c = ((own * 8 % BM) / 8) ^ swz_t(k);
             op = ((uint32_t)k * a.N + tm * BM + c * 8) * 2;
             bp = reinterpret_cast<const char *>(a.p + lo * a.N);
         } else {
-            const int row = tid >> 3, c = (tid & 7) ^ swz_p(row);
+            const int row = own >> 3, c = (own & 7) ^ swz(row);
             op = ((uint32_t)row * a.K + c * 8) * 2;
             kp = c * 8;
             bp = reinterpret_cast<const char *>(a.p + (lo + (int64_t)tm * BM) * a.K);
             np = min(cnt - tm * BM, BM) * a.K * 2;
         }
         if (QT) {
-            const int k = (tid * 8) / BN, c = ((tid * 8 % BN) / 8) ^ swz_qt(k);
+            const int k = (own * 8) / BN, c = ((own * 8 % BN) / 8) ^ swz_t(k);
             const int col = paired ? tn * (BN / 2) + (c >> 1) * 8 + (c & 1) * (a.N / 2)
                                    : tn * BN + c * 8;
             oq = ((uint32_t)k * qcols + col) * 2;
             bq = reinterpret_cast<const char *>(
                 FORM == kWeightGrad ? a.q + lo * qcols : a.q + (int64_t)e * a.K * a.N);
         } else {
-            const int row = tid >> 3, c = (tid & 7) ^ swz_q(row);
+            const int row = own >> 3, c = (own & 7) ^ swz(row);
             const int n = paired ? tn * (BN / 2) + (row >> 4) * 8 + (row & 7) + (row & 8 ? a.N / 2 : 0)
                                  : tn * BN + row;
             oq = ((uint32_t)n * a.K + c * 8) * 2;
@@ -627,9 +653,9 @@ __global__ __launch_bounds__(kTileThreads) void tile_kernel(Args a)
         // DMA number x of a stage: those of P, then those of Q
         auto fetch_one = [&](const Stage &f, uint16_t *lp, uint16_t *lq, auto x) {
             if constexpr (x < ISP)
-                dma(f.rp, f.op + x * ip, lp + x * 4096 + wave * 512);
+                dma(f.rp, f.op + x * ip, lp + x * WAVES * 512 + wave * 512);
             else
-                dma(f.rq, f.oq + (x - ISP) * iq, lq + (x - ISP) * 4096 + wave * 512);
+                dma(f.rq, f.oq + (x - ISP) * iq, lq + (x - ISP) * WAVES * 512 + wave * 512);
         };
         auto fetch = [&](int s, uint16_t *lp, uint16_t *lq) {
             const Stage f = stage(s);
@@ -637,15 +663,19 @@ __global__ __launch_bounds__(kTileThreads) void tile_kernel(Args a)
         };
         auto read_q = [&](bf16x8 (&f)[4], const uint16_t *lq, auto kb) {
             each<4>([&](auto j) {
-                f[j] = QT ? read_tr<BN>(lq + aq[j / 2] + kb * 32 * BN + (j & 1) * 4)
-                          : *reinterpret_cast<const bf16x8 *>(lq + aq[kb] + j * 4 * kTileK);
+                f[j] = QT ? read_tr<BN>(at(lq, aq[0] ^ (j * 32), kb * 32 * BN))
+                          : *reinterpret_cast<const bf16x8 *>(at(lq, aq[kb], j * 16 * kTileK));
             });
         };
         bf16x8 fp[4], qa[4], qb[4];
         auto read_p = [&](const uint16_t *lp, auto g) {      // piece g of a stage's 2 IP
             constexpr int i = g % IP, kb = g / IP;
-            fp[g % 4] = PT ? read_tr<BM>(lp + (ap[0] ^ (i * 16)) + kb * 32 * BM)
-                           : *reinterpret_cast<const bf16x8 *>(lp + ap[kb] + i * 16 * kTileK);
+            if constexpr (PT) {
+                fp[g % 4] = read_tr<BM>(at(lp, ap[0], kb * 32 * BM));
+                walk(ap[0], (i ^ ((i + 1) % IP)) * 32);
+            } else {
+                fp[g % 4] = *reinterpret_cast<const bf16x8 *>(at(lp, ap[kb], i * 16 * kTileK));
+            }
         };
         auto multiply = [&](const bf16x8 (&fq)[4], auto g) {
             constexpr int i = g % IP;
@@ -709,34 +739,32 @@ __global__ __launch_bounds__(kTileThreads) void tile_kernel(Args a)
         __syncthreads();
 
         const int m0 = tm * BM + wm * (BM / WM), n0 = wn * 64;
-        int own = lane;                      // opaque: no address of it is kept from tile to tile
+        own = tid & 63;
         asm volatile("" : "+v"(own));
         const int er = own & 15, eq = own >> 4;
         if (split) {
             // registers as they are; join_kernel reads them alike
             f32x4 *slot = a.ws + (int64_t)(rest * plan.parts + part) * (BM * BN / 4);
-            each<IP * 4>([&](auto y) { slot[((y / 4 * 8 + wave) * 4 + y % 4) * 64 + own] = acc[y]; });
-        } else if (FORM == kWeightGrad) {
-            each<IP>([&](auto i) {
-                const f32x4 v[4] = {acc[i * 4], acc[i * 4 + 1], acc[i * 4 + 2], acc[i * 4 + 3]};
-                emit_weight_row<BN>(a, x, m0 + i * 16 + er, n0 + eq * 16, v);
-            });
+            each<IP * 4>([&](auto y) { slot[((y / 4 * WAVES + wave) * 4 + y % 4) * 64 + own] = acc[y]; });
         } else {
             // Two passes of half the wave's rows through its own part of the
             // stages: the epilogue's code is there once a pass, not once an
             // accumulator (43 000 instructions otherwise).
             constexpr int half = IP / 2 * 16;
-            uint16_t *const stages = wave < 2 ? sp0 : wave < 4 ? sp1 : wave < 6 ? sq0 : sq1;
-            float *const mine = reinterpret_cast<float *>(stages) + (wave & 1) * half * 64;
+            constexpr int share = WAVES / 4;       // waves to a stage array
+            uint16_t *const stages = wave < share       ? sp0
+                                     : wave < 2 * share ? sp1
+                                     : wave < 3 * share ? sq0
+                                                        : sq1;
+            float *const mine = reinterpret_cast<float *>(stages) + wave % share * half * 64;
             each<2>([&](auto h) {
                 each<IP / 2>([&](auto i) {
                     each<4>([&](auto j) {
-                        *reinterpret_cast<f32x4 *>(mine + (i * 16 + er) * 64 + ((eq * 4 + j) ^ er) * 4) =
-                            acc[(h * (IP / 2) + i) * 4 + j];
+                        put(mine, i * 16 + er, j * 4 + eq, acc[(h * (IP / 2) + i) * 4 + j]);
                     });
                 });
                 __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
-                emit_rows<BN>(a, x, mine, half, m0 + h * half, n0, own);
+                emit_rows<BN, FORM>(a, x, mine, half, m0 + h * half, n0, own);
                 __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
             });
             __syncthreads();       // the next tile's stages overwrite the other waves' parts
@@ -749,10 +777,10 @@ __global__ __launch_bounds__(kTileThreads) void tile_kernel(Args a)
 // (blockIdx.x) of tiles blockIdx.y, + gridDim.y, ..; `grid` is the tile
 // kernel's.
 template <int BM, int BN, Form FORM>
-__global__ __launch_bounds__(kTileThreads) void join_kernel(Args a, int grid)
+__global__ __launch_bounds__(tile_threads(BN)) void join_kernel(Args a, int grid)
 {
-    constexpr int WN = BN / 64, WM = 8 / WN;
-    __shared__ __align__(16) float rows[FORM == kWeightGrad ? 4 : 8 * 16 * 64];
+    constexpr int WN = waves_n(BN), WM = kWavesM, WAVES = WM * WN;
+    __shared__ __align__(16) float rows[WAVES * 16 * 64];
     __shared__ int32_t pre[FORM == kWeightGrad ? 1 : kMaxExperts + 1];
     __shared__ int32_t sums[8];
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, q = lane >> 4;
@@ -761,12 +789,12 @@ __global__ __launch_bounds__(kTileThreads) void join_kernel(Args a, int grid)
     const int ntn = FORM == kWeightGrad ? (a.K + BN - 1) / BN : (a.N + BN - 1) / BN;
     const int ntm = FORM == kWeightGrad ? (a.N + BM - 1) / BM : 0;
     if (FORM != kWeightGrad)
-        tile_prefix<BM>(a, pre, sums);
+        tile_prefix<BM, WAVES * 64>(a, pre, sums);
     const Plan plan = plan_of(a, FORM == kWeightGrad ? (int64_t)a.E * ntm * ntn : (int64_t)pre[a.E] * ntn,
                               grid);
     for (int l = blockIdx.y; l < plan.left; l += gridDim.y) {
         const Tile x = locate<FORM>(a, pre, plan.whole + l, ntm, ntn);
-        const f32x4 *slot = a.ws + (int64_t)l * plan.parts * (BM * BN / 4) + ((i * 8 + wave) * 4) * 64 + lane;
+        const f32x4 *slot = a.ws + (int64_t)l * plan.parts * (BM * BN / 4) + ((i * WAVES + wave) * 4) * 64 + lane;
         f32x4 acc[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -778,17 +806,13 @@ __global__ __launch_bounds__(kTileThreads) void join_kernel(Args a, int grid)
                 acc[j] += slot[j * 64];
         }
         const int m0 = x.tm * BM + wm * (BM / WM) + i * 16, n0 = wn * 64;
-        if (FORM == kWeightGrad) {
-            emit_weight_row<BN>(a, x, m0 + r, n0 + q * 16, acc);
-        } else {
-            float *mine = rows + wave * 16 * 64;
+        float *mine = rows + wave * 16 * 64;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                *reinterpret_cast<f32x4 *>(mine + r * 64 + ((q * 4 + j) ^ r) * 4) = acc[j];
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
-            emit_rows<BN>(a, x, mine, 16, m0, n0, lane);
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
-        }
+        for (int j = 0; j < 4; ++j)
+            put(mine, r, j * 4 + q, acc[j]);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+        emit_rows<BN, FORM>(a, x, mine, 16, m0, n0, lane);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
     }
 }
 
@@ -796,15 +820,17 @@ __global__ __launch_bounds__(kTileThreads) void join_kernel(Args a, int grid)
 //
 // For experts with a few rows the weights' bytes are the cost: each is read
 // once, straight into the registers of the matrix instruction. A workgroup
-// of 4 waves takes 32 columns of one expert; the waves share the contraction
-// (128 deep a turn each) and add their sums through LDS in wave order.
+// of WAVES waves takes 32 columns of one expert; the waves share the
+// contraction (128 deep a turn each) and add their sums through LDS in wave
+// order. Workgroups start at different places of the contraction and come
+// round, so that those under way at one time read different columns of their
+// rows, which lie on different memory channels.
 
-constexpr int kFewThreads = 256;
 constexpr int kFewCols = 32;
 
-template <int MT>
+template <int WAVES, int MT>
 __device__ __forceinline__ void few_rows(const Args &a, int e, int64_t row0, int left, int nb,
-                                         float *red)
+                                         f32x4 *red)
 {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, q = lane >> 4;
     const bool paired = a.act == EPL_ACT_SWIGLU;
@@ -826,11 +852,13 @@ __device__ __forceinline__ void few_rows(const Args &a, int e, int64_t row0, int
         acc[i][0] = acc[i][1] = f32x4{0, 0, 0, 0};
 
     const bf16x8 zero = {};
-    for (int k0 = wave * 128; k0 < a.K; k0 += 512) {
+    const int turns = (a.K + 127) / 128;
+    int at = (int)((uint32_t)(e * 13 + nb * 3 + wave) % (uint32_t)turns);
+    for (int t = wave; t < turns; t += WAVES) {
         bf16x8 fw[4][2], fx[4][MT];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            const int k = k0 + u * 32;
+            const int k = at * 128 + u * 32;
             const bool in = k + q * 8 < a.K;
 #pragma unroll
             for (int j = 0; j < 2; ++j)
@@ -847,25 +875,27 @@ __device__ __forceinline__ void few_rows(const Args &a, int e, int64_t row0, int
                 for (int j = 0; j < 2; ++j)
                     acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fw[u][j], fx[u][i],
                                                                         acc[i][j], 0, 0, 0);
+        at += WAVES;
+        while (at >= turns)
+            at -= turns;
     }
 
     __syncthreads();           // red may still be read for the rows before
-    f32x4 *mine = reinterpret_cast<f32x4 *>(red);
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-            mine[((wave * MT + i) * 2 + j) * 64 + lane] = acc[i][j];
+            red[((wave * MT + i) * 2 + j) * 64 + lane] = acc[i][j];
     __syncthreads();
     if (wave >= MT)
         return;
     f32x4 sum[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        sum[j] = mine[(wave * 2 + j) * 64 + lane];
+        sum[j] = red[(wave * 2 + j) * 64 + lane];
 #pragma unroll
-        for (int v = 1; v < 4; ++v)
-            sum[j] += mine[((v * MT + wave) * 2 + j) * 64 + lane];
+        for (int v = 1; v < WAVES; ++v)
+            sum[j] += red[((v * MT + wave) * 2 + j) * 64 + lane];
     }
     const int m = wave * 16 + r;
     if (m >= left)
@@ -889,24 +919,18 @@ __device__ __forceinline__ void few_rows(const Args &a, int e, int64_t row0, int
     }
 }
 
-__global__ __launch_bounds__(kFewThreads) void few_rows_kernel(Args a)
+template <int WAVES>
+__global__ __launch_bounds__(WAVES * 64, 4) void few_rows_kernel(Args a)
 {
-    __shared__ __align__(16) float red[4 * 4 * 2 * 64 * 4];
+    __shared__ f32x4 red[WAVES * 2 * 2 * 64];
     const int e = blockIdx.y, nb = blockIdx.x;
     int64_t lo;
     const int cnt = block_of(a, e, lo);
-    for (int m = 0; m < cnt;) {
-        const int left = cnt - m;
-        if (left <= 16) {
-            few_rows<1>(a, e, lo + m, left, nb, red);
-            m += 16;
-        } else if (left <= 32) {
-            few_rows<2>(a, e, lo + m, left, nb, red);
-            m += 32;
-        } else {
-            few_rows<4>(a, e, lo + m, left, nb, red);
-            m += 64;
-        }
+    for (int m = 0; m < cnt; m += 32) {
+        if (cnt - m <= 16)
+            few_rows<WAVES, 1>(a, e, lo + m, cnt - m, nb, red);
+        else
+            few_rows<WAVES, 2>(a, e, lo + m, cnt - m, nb, red);
     }
 }
 
