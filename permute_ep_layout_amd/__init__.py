@@ -13,6 +13,7 @@ they allocate outputs with ``torch.empty`` and call the same entry points.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import NamedTuple, Optional
 
@@ -629,19 +630,41 @@ def epl_expert_scale(p: Problem, rows_in, m_indices, capacity_rows, rows_out, wo
            "epl_expert_scale")
 
 
+def _raw_stream(index: int) -> int:
+    """torch's current stream on GPU `index`, without the Stream object
+    around it (1.9 us) where torch offers that."""
+    torch = _torch()
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return get(index) if get is not None else torch.cuda.current_stream(index).cuda_stream
+
+
 def _launch(name: str, dev, stream, *args):
     """Call C entry point `name` with `dev` as the current device (kernels are
     launched on the current device, which need not be the tensors') and the
     stream last."""
     torch = _torch()
     fn = getattr(load(), name)
-    if dev.index is None or torch.cuda.current_device() == dev.index:
-        rc = fn(*args, _stream(stream, dev))
+    current = torch.cuda.current_device()
+    index = current if dev.index is None else dev.index
+    raw = _raw_stream(index) if stream is None else _stream(stream)
+    if index == current:
+        rc = fn(*args, raw)
     else:
-        with torch.cuda.device(dev):
-            rc = fn(*args, _stream(stream, dev))
+        with torch.cuda.device(index):
+            rc = fn(*args, raw)
     if rc != EPL_OK:
         raise EplError(rc, name)
+
+
+def _need_same(t, name, dtype, shape, dev):
+    """_need with every condition given; the common case in one expression."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous() \
+                and t.is_cuda:
+            return
+    except AttributeError:
+        pass
+    _need(t, name, dtype, shape, dev)
 
 
 def _type_code(dtype, name) -> int:
@@ -664,12 +687,14 @@ def _router_dtype(p: Router):
 def epl_route(p: Router, logits, bias, token_mask, topk_idx, topk_weights, stream=None):
     torch = _torch()
     T, K, E = p.num_tokens, p.num_topk, p.num_experts
-    _need(logits, "logits", _router_dtype(p), (T, E))
-    dev = logits.device
-    _need(bias, "bias", torch.float32, (E,), dev, allow_none=True)
-    _need(token_mask, "token_mask", torch.uint8, (T,), dev, allow_none=True)
-    _need(topk_idx, "topk_idx", torch.int64, (T, K), dev)
-    _need(topk_weights, "topk_weights", torch.float32, (T, K), dev)
+    dev = getattr(logits, "device", None)
+    _need_same(logits, "logits", _router_dtype(p), (T, E), dev)
+    if bias is not None:
+        _need_same(bias, "bias", torch.float32, (E,), dev)
+    if token_mask is not None:
+        _need_same(token_mask, "token_mask", torch.uint8, (T,), dev)
+    _need_same(topk_idx, "topk_idx", torch.int64, (T, K), dev)
+    _need_same(topk_weights, "topk_weights", torch.float32, (T, K), dev)
     _launch("epl_route", dev, stream, ctypes.byref(p), _ptr(logits), _ptr(bias), _ptr(token_mask),
             _ptr(topk_idx), _ptr(topk_weights))
 
@@ -678,11 +703,11 @@ def epl_route_backward(p: Router, logits, topk_idx, grad_weights, grad_logits, s
     torch = _torch()
     T, K, E = p.num_tokens, p.num_topk, p.num_experts
     dt = _router_dtype(p)
-    _need(logits, "logits", dt, (T, E))
-    dev = logits.device
-    _need(topk_idx, "topk_idx", torch.int64, (T, K), dev)
-    _need(grad_weights, "grad_weights", torch.float32, (T, K), dev)
-    _need(grad_logits, "grad_logits", dt, (T, E), dev)
+    dev = getattr(logits, "device", None)
+    _need_same(logits, "logits", dt, (T, E), dev)
+    _need_same(topk_idx, "topk_idx", torch.int64, (T, K), dev)
+    _need_same(grad_weights, "grad_weights", torch.float32, (T, K), dev)
+    _need_same(grad_logits, "grad_logits", dt, (T, E), dev)
     _launch("epl_route_backward", dev, stream, ctypes.byref(p), _ptr(logits), _ptr(topk_idx),
             _ptr(grad_weights), _ptr(grad_logits))
 
@@ -693,8 +718,8 @@ def epl_product_validate(p: Product) -> int:
 
 def _blocks(p: Product, expert_start_loc, num_tokens_per_expert, dev):
     torch = _torch()
-    _need(expert_start_loc, "expert_start_loc", torch.int32, (p.num_experts,), dev)
-    _need(num_tokens_per_expert, "num_tokens_per_expert", torch.int32, (p.num_experts,), dev)
+    _need_same(expert_start_loc, "expert_start_loc", torch.int32, (p.num_experts,), dev)
+    _need_same(num_tokens_per_expert, "num_tokens_per_expert", torch.int32, (p.num_experts,), dev)
 
 
 def epl_product_workspace_bytes(p: Product) -> int:
@@ -718,17 +743,20 @@ def epl_expert_product(p: Product, x, weight, bias, residual, expert_start_loc,
     torch = _torch()
     rows, E, K, N = p.num_rows, p.num_experts, p.in_cols, p.out_cols
     bf16 = torch.bfloat16
-    _need(x, "x", bf16, (rows, K))
-    dev = x.device
-    _need(weight, "weight", bf16, (E, K, N) if p.weight_layout == EPL_WEIGHT_IN_OUT else (E, N, K),
-          dev)
-    _need(bias, "bias", torch.float32, (E, N), dev, allow_none=True)
+    dev = getattr(x, "device", None)
+    _need_same(x, "x", bf16, (rows, K), dev)
+    _need_same(weight, "weight", bf16,
+               (E, K, N) if p.weight_layout == EPL_WEIGHT_IN_OUT else (E, N, K), dev)
+    if bias is not None:
+        _need_same(bias, "bias", torch.float32, (E, N), dev)
     grad = p.activation >= EPL_ACT_SILU_GRAD
     cols = N // 2 if p.activation == EPL_ACT_SWIGLU else \
         2 * N if p.activation == EPL_ACT_SWIGLU_GRAD else N
-    _need(residual, "residual", bf16, (rows, cols), dev, allow_none=True)
-    _need(pre, "pre", bf16, (rows, cols if grad else N), dev, allow_none=not grad)
-    _need(y, "y", bf16 if p.out_type == EPL_OUT_BF16 else torch.float32, (rows, cols), dev)
+    if residual is not None:
+        _need_same(residual, "residual", bf16, (rows, cols), dev)
+    if pre is not None or grad:
+        _need_same(pre, "pre", bf16, (rows, cols if grad else N), dev)
+    _need_same(y, "y", bf16 if p.out_type == EPL_OUT_BF16 else torch.float32, (rows, cols), dev)
     _blocks(p, expert_start_loc, num_tokens_per_expert, dev)
     if workspace is not None:
         _need_split_ws(workspace, dev, epl_product_workspace_bytes(p), "epl_expert_product")
@@ -741,12 +769,13 @@ def epl_expert_weight_grad(p: Product, grad, x, expert_start_loc, num_tokens_per
                            accumulate, grad_weight, grad_bias=None, workspace=None, stream=None):
     torch = _torch()
     rows, E, K, N = p.num_rows, p.num_experts, p.in_cols, p.out_cols
-    _need(grad, "grad", torch.bfloat16, (rows, N))
-    dev = grad.device
-    _need(x, "x", torch.bfloat16, (rows, K), dev)
-    _need(grad_weight, "grad_weight",
-          torch.bfloat16 if p.out_type == EPL_OUT_BF16 else torch.float32, (E, N, K), dev)
-    _need(grad_bias, "grad_bias", torch.float32, (E, N), dev, allow_none=True)
+    dev = getattr(grad, "device", None)
+    _need_same(grad, "grad", torch.bfloat16, (rows, N), dev)
+    _need_same(x, "x", torch.bfloat16, (rows, K), dev)
+    _need_same(grad_weight, "grad_weight",
+               torch.bfloat16 if p.out_type == EPL_OUT_BF16 else torch.float32, (E, N, K), dev)
+    if grad_bias is not None:
+        _need_same(grad_bias, "grad_bias", torch.float32, (E, N), dev)
     _blocks(p, expert_start_loc, num_tokens_per_expert, dev)
     if workspace is not None:
         _need_split_ws(workspace, dev, epl_weight_grad_workspace_bytes(p),
@@ -760,14 +789,14 @@ def epl_combine_backward(p: Problem, grad_y, expert_out, expert_rows, output_ind
                          grad_rows, grad_weights, workspace=None, stream=None):
     torch = _torch()
     T, K, H = p.num_tokens, p.num_topk, p.hidden
-    _need(output_index, "output_index", torch.int32, (T, K))
-    dev = output_index.device
+    dev = getattr(output_index, "device", None)
+    _need_same(output_index, "output_index", torch.int32, (T, K), dev)
     code = _type_code(getattr(grad_y, "dtype", None), "grad_y")
-    _need(grad_y, "grad_y", grad_y.dtype, (T, H), dev)
-    _need(expert_out, "expert_out", torch.bfloat16, (expert_rows, H), dev)
-    _need(topk_weights, "topk_weights", torch.float32, (T, K), dev)
-    _need(grad_rows, "grad_rows", torch.bfloat16, (expert_rows, H), dev)
-    _need(grad_weights, "grad_weights", torch.float32, (T, K), dev)
+    _need_same(grad_y, "grad_y", grad_y.dtype, (T, H), dev)
+    _need_same(expert_out, "expert_out", torch.bfloat16, (expert_rows, H), dev)
+    _need_same(topk_weights, "topk_weights", torch.float32, (T, K), dev)
+    _need_same(grad_rows, "grad_rows", torch.bfloat16, (expert_rows, H), dev)
+    _need_same(grad_weights, "grad_weights", torch.float32, (T, K), dev)
     _need_ws_arg(workspace, dev, allow_none=True)
     if workspace is not None:
         _need_workspace(workspace, WS_HEADER_BYTES, "epl_combine_backward")
@@ -920,6 +949,22 @@ def expert_scale(res: DispatchResult, rows_in=None, stream=None):
     return out
 
 
+@functools.lru_cache(maxsize=256)
+def _router_for(*fields) -> Router:
+    """A checked description; the same sizes come again and again."""
+    p = Router(*fields, 0)
+    _check(epl_router_validate(p), "epl_router_validate")
+    return p
+
+
+@functools.lru_cache(maxsize=256)
+def _product_for(*fields):
+    """A checked description and its workspace's bytes."""
+    p = Product(*fields, 0)
+    _check(epl_product_validate(p), "epl_product_validate")
+    return p, epl_product_workspace_bytes(p)
+
+
 def _split_ws(nbytes, device, stream):
     """A product's workspace, from torch's allocator (kept for `stream` when
     that is not torch's current one)."""
@@ -964,12 +1009,12 @@ def route(logits, num_topk: int, score: str = "softmax", bias=None, num_groups: 
     torch = _torch()
     _matrix(logits, "logits", 2)
     T, E = logits.shape
-    p = Router(T, int(num_topk), E, _named(_SCORES, score, "score"), int(num_groups),
-               int(topk_groups), int(group_top), int(bool(renormalize)),
-               _type_code(logits.dtype, "logits"), float(scale), 0)
-    _check(epl_router_validate(p), "epl_router_validate")
-    idx = torch.empty((T, p.num_topk), dtype=torch.int64, device=logits.device)
-    w = torch.empty((T, p.num_topk), dtype=torch.float32, device=logits.device)
+    K = int(num_topk)
+    p = _router_for(T, K, E, _named(_SCORES, score, "score"), int(num_groups), int(topk_groups),
+                    int(group_top), int(bool(renormalize)), _type_code(logits.dtype, "logits"),
+                    float(scale))
+    idx = torch.empty((T, K), dtype=torch.int64, device=logits.device)
+    w = torch.empty((T, K), dtype=torch.float32, device=logits.device)
     epl_route(p, logits, bias, token_mask, idx, w, stream)
     return idx, w
 
@@ -982,9 +1027,8 @@ def route_backward(logits, topk_idx, grad_weights, score: str = "softmax",
     _matrix(logits, "logits", 2)
     _matrix(topk_idx, "topk_idx", 2)
     T, E = logits.shape
-    p = Router(T, topk_idx.shape[1], E, _named(_SCORES, score, "score"), 1, 1, 1,
-               int(bool(renormalize)), _type_code(logits.dtype, "logits"), float(scale), 0)
-    _check(epl_router_validate(p), "epl_router_validate")
+    p = _router_for(T, topk_idx.shape[1], E, _named(_SCORES, score, "score"), 1, 1, 1,
+                    int(bool(renormalize)), _type_code(logits.dtype, "logits"), float(scale))
     grad = torch.empty_like(logits)
     epl_route_backward(p, logits, topk_idx, grad_weights, grad, stream)
     return grad
@@ -1013,15 +1057,14 @@ def expert_product(x, weight, expert_start_loc, num_tokens_per_expert, bias=None
         out_dtype = out.dtype
     elif out_dtype is None:
         out_dtype = torch.bfloat16
-    p = Product(x.shape[0], int(expected_rows), E, x.shape[1], N,
-                EPL_WEIGHT_IN_OUT if transposed else EPL_WEIGHT_OUT_IN, act,
-                _type_code(out_dtype, "out"), 0)
-    _check(epl_product_validate(p), "epl_product_validate")
+    p, ws_bytes = _product_for(x.shape[0], int(expected_rows), E, x.shape[1], N,
+                               EPL_WEIGHT_IN_OUT if transposed else EPL_WEIGHT_OUT_IN, act,
+                               _type_code(out_dtype, "out"))
     if out is None:
         cols = N // 2 if act == EPL_ACT_SWIGLU else 2 * N if act == EPL_ACT_SWIGLU_GRAD else N
         out = torch.empty((x.shape[0], cols), dtype=out_dtype, device=x.device)
     if workspace is None and x.is_cuda:
-        workspace = _split_ws(epl_product_workspace_bytes(p), x.device, stream)
+        workspace = _split_ws(ws_bytes, x.device, stream)
     epl_expert_product(p, x, weight, bias, residual, expert_start_loc, num_tokens_per_expert, pre,
                        out, workspace, stream)
     return out
@@ -1045,9 +1088,8 @@ def expert_weight_grad(grad, x, expert_start_loc, num_tokens_per_expert, out=Non
                           device=x.device)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise ValueError(f"out is {out.dtype}, out_dtype {out_dtype}")
-    p = Product(grad.shape[0], 0, E, K, N, EPL_WEIGHT_OUT_IN, EPL_ACT_NONE,
-                _type_code(out.dtype, "out"), 0)
-    _check(epl_product_validate(p), "epl_product_validate")
+    p, _ = _product_for(grad.shape[0], 0, E, K, N, EPL_WEIGHT_OUT_IN, EPL_ACT_NONE,
+                        _type_code(out.dtype, "out"))
     if workspace is None and x.is_cuda:
         workspace = _split_ws(epl_weight_grad_workspace_bytes(p), x.device, stream)
     epl_expert_weight_grad(p, grad, x, expert_start_loc, num_tokens_per_expert, accumulate, out,
