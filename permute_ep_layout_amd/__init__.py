@@ -958,6 +958,13 @@ def _router_for(*fields) -> Router:
 
 
 @functools.lru_cache(maxsize=256)
+def _combine_problem(T: int, K: int, H: int) -> Problem:
+    p = Problem.make(T, K, 1, 1, H, 0)
+    _check(epl_validate(p), "epl_validate")
+    return p
+
+
+@functools.lru_cache(maxsize=256)
 def _product_for(*fields):
     """A checked description and its workspace's bytes."""
     p = Product(*fields, 0)
@@ -1107,8 +1114,7 @@ def combine_backward(grad_y, expert_out, output_index, topk_weights, grad_rows=N
     _matrix(expert_out, "expert_out", 2)
     T, K = output_index.shape
     rows, H = expert_out.shape
-    p = Problem.make(T, K, 1, 1, H, 0)
-    _check(epl_validate(p), "epl_validate")
+    p = _combine_problem(T, K, H)
     if grad_rows is None:
         grad_rows = torch.empty_like(expert_out)
     grad_weights = torch.empty((T, K), dtype=torch.float32, device=expert_out.device)

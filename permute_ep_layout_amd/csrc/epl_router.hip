@@ -5,6 +5,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "epl.h"
 #include "epl_router_kernels.h"
@@ -86,6 +87,7 @@ int epl_route(const epl_router *p, const void *logits, const float *bias,
     a.bf16 = p->logits_type == EPL_OUT_BF16;
     a.need_scores = bias || (a.G > 1 && a.group_top == 2);
     a.vec = vector_rows(*p, logits, logits);
+    a.bias_vec = aligned(bias, 16);
     a.scale = p->scale;
     hipStream_t s = static_cast<hipStream_t>(stream);
 
@@ -105,22 +107,24 @@ int epl_route(const epl_router *p, const void *logits, const float *bias,
         // GPU; with few tokens as many lanes as there are pieces, the
         // shortest path for one token.
         const bool many = a.T > 4096;
-        if (pieces <= 8 && per <= 8)
-            return launch(R::route_kernel<8, 1>, 8);
-        if (pieces <= 16 && per <= 8 && many)
-            return launch(R::route_kernel<8, 2>, 8);
-        if (pieces <= 16 && per <= 16)
-            return launch(R::route_kernel<16, 1>, 16);
-        if (pieces <= 32 && per <= 8 && many)
-            return launch(R::route_kernel<8, 4>, 8);
-        if (pieces <= 32 && per <= 32)
-            return launch(R::route_kernel<32, 1>, 32);
-        if (pieces <= 64 && per <= 16 && many)
-            return launch(R::route_kernel<16, 4>, 16);
-        if (pieces <= 64 && per <= 64)
-            return launch(R::route_kernel<64, 1>, 64);
+        auto order = [&](auto o) {
+            constexpr R::Order O = decltype(o)::value;
+            if (pieces <= 8 && per <= 8)
+                return launch(R::route_kernel<8, 1, O>, 8);
+            if (pieces <= 16 && per <= 16)
+                return launch(R::route_kernel<16, 1, O>, 16);
+            if (pieces <= 32 && per <= 8 && many)
+                return launch(R::route_kernel<8, 4, O>, 8);
+            if (pieces <= 32 && per <= 32)
+                return launch(R::route_kernel<32, 1, O>, 32);
+            if (pieces <= 64 && per <= 64)
+                return launch(R::route_kernel<64, 1, O>, 64);
+            return launch(R::route_kernel<64, 4, O>, 64);
+        };
         if (pieces <= 256 && per <= 64)
-            return launch(R::route_kernel<64, 4>, 64);
+            return !a.need_scores ? order(std::integral_constant<R::Order, R::kLogits>{})
+                   : a.softmax    ? order(std::integral_constant<R::Order, R::kSoftmax>{})
+                                  : order(std::integral_constant<R::Order, R::kSigmoid>{});
     }
     hipLaunchKernelGGL(R::route_any_kernel, dim3((unsigned)std::min<int64_t>(a.T, 1 << 16)),
                        dim3(64), 0, s, a);

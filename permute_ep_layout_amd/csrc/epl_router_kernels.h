@@ -9,8 +9,10 @@
 // carries the index, and the selection is a sorting network on registers.
 // Without a bias (and without sums of two) the score is the logit itself,
 // which orders the experts as any score does and leaves the low 29 bits of a
-// binary64 free: the order is exact. With them scores are computed in
-// binary64, to about 2^-44, and compared to 41 bits.
+// binary64 free: the order is exact. With them scores are compared as
+// binary64 numbers, good to about 2^-44, to 41 bits. They are first computed
+// in binary32; where two that matter lie within its error of each other, a
+// few tokens in a thousand, the choice is done again in binary64.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -34,7 +36,7 @@ struct Args {
     float *w;                      // [T, K]
     int64_t T;
     int K, E, G, topk_groups, group_top;
-    bool softmax, renorm, bf16, need_scores, vec;
+    bool softmax, renorm, bf16, need_scores, vec, bias_vec;
     float scale;
 };
 
@@ -81,10 +83,12 @@ __device__ __forceinline__ double rcp64(double d)
     return fma(fma(-d, y, 1.0), y, y);
 }
 
-// 0 below -700, where exp64 stops growing.
+// 0 below -700, where exp64 stops growing. (No branch: a select of the
+// finished value. A branch an element made the choice twice as slow.)
 __device__ __forceinline__ double sigmoid64(double x)
 {
-    return x < -700.0 ? 0.0 : rcp64(1.0 + exp64(-x));
+    const double s = rcp64(1.0 + exp64(-x));
+    return x < -700.0 ? 0.0 : s;
 }
 
 // +inf competes as the largest finite logit; a NaN stays one.
@@ -96,12 +100,20 @@ __device__ __forceinline__ float load_logit(const void *p, bool bf16, int64_t at
                        : static_cast<const float *>(p)[at]);
 }
 
-// A key that may win: not -inf (no candidate).
-__device__ __forceinline__ double make_key(double score, int index)
+// Keys at or below it are no candidates; every score's key is above it, the
+// lowest finite binary32 too.
+constexpr double kNone = -1e300;
+
+// The key of a score, or one that is no candidate.
+__device__ __forceinline__ double make_key(double score, int index, bool candidate)
 {
-    uint64_t u = __builtin_bit_cast(uint64_t, score + 0.0);      // -0 becomes +0
-    const uint64_t tail = (u >> 63) ? (uint64_t)index : kIndexMask - (uint64_t)index;
-    return __builtin_bit_cast(double, (u & ~kIndexMask) | tail);
+    const uint64_t u = __builtin_bit_cast(uint64_t, score + 0.0);      // -0 becomes +0
+    const uint32_t hi = (uint32_t)(u >> 32);
+    // of a negative score the larger index has the larger magnitude
+    const uint32_t flip = (uint32_t)((int32_t)hi >> 31) & (uint32_t)kIndexMask;
+    const uint32_t lo = ((uint32_t)u & ~(uint32_t)kIndexMask) |
+                        (((uint32_t)kIndexMask - (uint32_t)index) ^ flip);
+    return __builtin_bit_cast(double, ((uint64_t)(candidate ? hi : 0xffefffffu) << 32) | lo);
 }
 
 __device__ __forceinline__ int key_index(double key)
@@ -111,15 +123,47 @@ __device__ __forceinline__ int key_index(double key)
     return (u >> 63) ? tail : (int)kIndexMask - tail;
 }
 
-// Choice score of a logit, or -inf where the expert cannot be chosen. `m`
-// and `inv` are the row's largest logit and 1 / sum of exponentials.
-__device__ __forceinline__ double choice(const Args &a, float l, float bias, double m, double inv)
+// What orders the experts: the logits themselves, or scores (with a bias, or
+// summed over groups).
+enum Order { kLogits, kSigmoid, kSoftmax };
+
+// Whether an expert may be chosen, by its logit and its bias.
+__device__ __forceinline__ bool usable(float l, float bias) { return l > -INFINITY && bias > -INFINITY; }
+
+// Choice score of a logit. `m` and `inv` are the row's largest logit and 1 /
+// sum of exponentials.
+template <Order ORDER>
+__device__ __forceinline__ double exact_score(float l, float bias, double m, double inv)
 {
-    const bool out = !(l > -INFINITY) || !(bias > -INFINITY);
-    if (!a.need_scores)
-        return out ? -INFINITY : (double)l;
-    const double s = a.softmax ? exp64((double)l - m) * inv : sigmoid64((double)l);
-    return out ? -INFINITY : s + (double)no_inf(bias);
+    if constexpr (ORDER == kLogits)
+        return (double)l;
+    else if constexpr (ORDER == kSoftmax)
+        return exp64((double)l - m) * inv + (double)no_inf(bias);
+    else
+        return sigmoid64((double)l) + (double)no_inf(bias);
+}
+
+template <Order ORDER>
+__device__ __forceinline__ float fast_score(float l, float bias, float m, float inv)
+{
+    if constexpr (ORDER == kLogits)
+        return l;
+    else if constexpr (ORDER == kSoftmax)
+        return __expf(l - m) * inv + no_inf(bias);
+    else
+        return __builtin_amdgcn_rcpf(1.0f + __expf(-l)) + no_inf(bias);
+}
+
+// How far two choice scores in binary32 must lie apart for their order to be
+// sure, given the larger one's magnitude and the row's largest score s. Of a
+// sigmoid: exp and the reciprocal are good to a step each and the argument's
+// rounding passes on s (1 - s) |l| < 1/4 of a step, in all below 4 2^-24 s,
+// for either score; a softmax's sum adds 45 2^-24 for up to 40 additions; the
+// sum with the bias half a step. Doubled, and rounded up.
+template <Order ORDER>
+__device__ __forceinline__ double margin(double c, double top)
+{
+    return (ORDER == kSoftmax ? 0x1p-17 : 0x1p-20) * top + 0x1p-21 * fabs(c);
 }
 
 // ---- register sorting ------------------------------------------------------
@@ -235,8 +279,11 @@ __device__ __forceinline__ void two_best(double &a, double &b, double c, double 
 // Group score from its two best keys: a group of one candidate has that one.
 __device__ __forceinline__ double group_score(const Args &a, double best, double next)
 {
-    return a.group_top == 2 && next > -INFINITY ? best + next : best;
+    return a.group_top == 2 && next > kNone ? best + next : best;
 }
+
+// LDS operations of one wave are in order: this keeps the compiler's order.
+__device__ __forceinline__ void wave_lds() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local"); }
 
 // Logits of 8 neighbouring experts; -inf past the row's end.
 __device__ __forceinline__ void load8(const void *p, bool bf16, bool vec, int64_t row, int E, int e0,
@@ -291,73 +338,133 @@ __device__ __forceinline__ float weight_of(const Args &a, float l, double m, dou
     return (float)(s * (double)a.scale);
 }
 
+// ---- any top-k, any groups: a wave a token, its keys in LDS ----------------
+//
+// Scores in binary64; K rounds, each the largest key below the last round's.
+// For sizes that the kernel below does not cover (K above 8, groups that end
+// inside a piece), and for its tokens whose choice binary32 leaves in doubt.
+__device__ __forceinline__ void route_token(const Args &a, int64_t t, int lane, double *key,
+                                            double *score)
+{
+    double m = 0.0, inv = 1.0;
+    if (a.softmax) {
+        float mx = -INFINITY;
+        for (int e = lane; e < a.E; e += 64)
+            mx = fmaxf(mx, usable(load_logit(a.logits, a.bf16, t * a.E + e)));
+        mx = lane_max<64>(mx);
+        m = mx > -INFINITY ? (double)mx : 0.0;
+        double s = 0.0;
+        for (int e = lane; e < a.E; e += 64) {
+            const float l = load_logit(a.logits, a.bf16, t * a.E + e);
+            const double x = exp64((double)l - m);
+            s += l > -INFINITY ? x : 0.0;
+        }
+        s = lane_sum<64>(s);
+        inv = s > 0.0 ? 1.0 / s : 0.0;
+    }
+    for (int e = lane; e < a.E; e += 64) {
+        const float l = load_logit(a.logits, a.bf16, t * a.E + e), b = a.bias ? a.bias[e] : 0.0f;
+        const double c = !a.need_scores ? exact_score<kLogits>(l, b, m, inv)
+                         : a.softmax    ? exact_score<kSoftmax>(l, b, m, inv)
+                                        : exact_score<kSigmoid>(l, b, m, inv);
+        key[e] = make_key(c, e, usable(l, b));
+    }
+    wave_lds();
+    if (a.G > 1) {
+        const int size = a.E / a.G;
+        if (lane < a.G) {
+            double x = 2.0 * kNone, y = 2.0 * kNone;
+            for (int i = 0; i < size; ++i)
+                two_best(x, y, key[lane * size + i], 2.0 * kNone);
+            score[lane] = group_score(a, x, y);
+        }
+        wave_lds();
+        if (lane < a.G) {
+            // Sums of two that agree to 2^-38 are equal: the same scores and
+            // biases paired otherwise, whose sums differ by rounding and by
+            // the index bits of their keys.
+            const double own = score[lane];
+            const double near = a.need_scores && own > kNone ? 0x1p-38 * fabs(own) : 0.0;
+            int before = 0;
+            for (int o = 0; o < a.G; ++o)
+                before += score[o] > own + near || (score[o] >= own - near && o < lane) ? 1 : 0;
+            if (before >= a.topk_groups)
+                for (int i = 0; i < size; ++i)
+                    key[lane * size + i] = 2.0 * kNone;
+        }
+        wave_lds();
+    }
+    const bool live = !a.mask || a.mask[t] != 0;
+    double last = INFINITY;
+    int mine = -1;
+    for (int k = 0; k < a.K; ++k) {
+        double x = 2.0 * kNone;
+        for (int e = lane; e < a.E; e += 64) {
+            const double v = key[e];
+            x = v < last && v > x ? v : x;
+        }
+        last = lane_max<64>(x);
+        mine = lane == k && live && last > kNone ? key_index(last) : mine;
+    }
+    const float l = mine >= 0 ? load_logit(a.logits, a.bf16, t * a.E + mine) : -INFINITY;
+    const float w = weight_of<64>(a, l, m, inv);
+    if (lane < a.K) {
+        a.idx[t * a.K + lane] = mine;
+        a.w[t * a.K + lane] = mine >= 0 ? w : 0.0f;
+    }
+    wave_lds();
+}
+
+__global__ __launch_bounds__(64) void route_any_kernel(Args a)
+{
+    __shared__ double key[kMaxExperts];
+    __shared__ double score[kMaxGroups];
+    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x)
+        route_token(a, t, threadIdx.x, key, score);
+}
+
 // ---- top-k of at most 8, L lanes a token, CH pieces of 8 experts a lane ----
 //
 // Piece c of lane i holds experts (c L + i) 8 .. + 7. Each lane sorts its
 // pieces, merges them to its 8 best, and log2(L) merges across lanes leave
 // the token's 8 best, in order, in every lane. Bound by its vector
 // instructions: about 50 binary64 maxima and minima a token at L = 8.
-template <int L, int CH>
-__global__ __launch_bounds__(kThreads) void route_kernel(Args a)
+
+// The token's 8 best keys in every lane; false, on one of its lanes at least,
+// where the error of binary32 leaves their order in doubt. `groups` and
+// `gone`: the token's LDS, of kMaxGroups each.
+template <int L, int CH, Order ORDER>
+__device__ __forceinline__ bool choose(const Args &a, const float (&l)[CH][8], int lane, float m,
+                                       float inv, double *groups, int *gone, double (&best)[8])
 {
-    __shared__ double groups[kThreads / L][kMaxGroups + 1];
-    const int lane = threadIdx.x % L, slot = threadIdx.x / L;
-    const int64_t t = (int64_t)blockIdx.x * (kThreads / L) + slot;
-    const bool in = t < a.T;
-    const int64_t row = in ? t : a.T - 1;
-
-    float l[CH][8];
-#pragma unroll
-    for (int c = 0; c < CH; ++c)
-        load8(a.logits, a.bf16, a.vec, row, a.E, (c * L + lane) * 8, l[c]);
-
-    double m = 0.0, inv = 1.0;
-    if (a.softmax && (a.need_scores || !a.renorm)) {
-        float mx = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < CH; ++c)
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                mx = fmaxf(mx, usable(l[c][i]));
-        mx = lane_max<L>(mx);
-        m = mx > -INFINITY ? (double)mx : 0.0;
-        if (a.need_scores) {
-            double s = 0.0;
-#pragma unroll
-            for (int c = 0; c < CH; ++c)
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    s += l[c][i] > -INFINITY ? exp64((double)l[c][i] - m) : 0.0;
-            s = lane_sum<L>(s);
-            inv = s > 0.0 ? rcp64(s) : 0.0;
-        } else {
-            float s = 0.0f;
-#pragma unroll
-            for (int c = 0; c < CH; ++c)
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    s += l[c][i] > -INFINITY ? __expf(l[c][i] - (float)m) : 0.0f;
-            s = lane_sum<L>(s);
-            inv = s > 0.0f ? 1.0 / (double)s : 0.0;
-        }
-    }
-
-    double best[8];
+    const double top = ORDER == kSoftmax ? (double)inv : 1.0;
     double key[CH][8];
+    bool sure = true;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
+        const int e0 = (c * L + lane) * 8;
+        float b[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (a.bias) {
+            if (e0 + 8 <= a.E && a.bias_vec) {
+                const float4 x = *reinterpret_cast<const float4 *>(a.bias + e0);
+                const float4 y = *reinterpret_cast<const float4 *>(a.bias + e0 + 4);
+                b[0] = x.x, b[1] = x.y, b[2] = x.z, b[3] = x.w;
+                b[4] = y.x, b[5] = y.y, b[6] = y.z, b[7] = y.w;
+            } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int e = (c * L + lane) * 8 + i;
-            const double s = choice(a, l[c][i], a.bias && e < a.E ? a.bias[e] : 0.0f, m, inv);
-            key[c][i] = s > -INFINITY ? make_key(s, e) : -INFINITY;
+                for (int i = 0; i < 8; ++i)
+                    b[i] = e0 + i < a.E ? a.bias[e0 + i] : 0.0f;
+            }
         }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            key[c][i] = make_key((double)fast_score<ORDER>(l[c][i], b[i], m, inv), e0 + i,
+                                 usable(l[c][i], b[i]));
         sort8(key[c]);
     }
     if (a.G > 1) {
         // pieces lie within groups of `per` pieces (a power of two): the two
-        // best keys of a group by exchanges, its score and those of the
-        // token's other groups from LDS
+        // best keys of a group by exchanges; lane g then ranks group g
         const int per = a.E / a.G / 8;
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
@@ -374,23 +481,32 @@ __global__ __launch_bounds__(kThreads) void route_kernel(Args a)
                 if (per > 32) { two_best(x, y, lane_swap<32>(x), lane_swap<32>(y)); }
             const int piece = c * L + lane;
             if (piece % per == 0 && piece / per < a.G)
-                groups[slot][piece / per] = group_score(a, x, y);
+                groups[piece / per] = group_score(a, x, y);
         }
-        __syncthreads();
+        wave_lds();
+        for (int g = lane; g < a.G; g += L) {
+            const double own = groups[g], near = 2.0 * margin<ORDER>(own, top);
+            int before = 0, close = 0;
+            for (int o = 0; o < a.G; ++o) {
+                const double s = groups[o];
+                before += (int)(s > own) | ((int)(s == own) & (int)(o < g));
+                if (ORDER != kLogits)
+                    close += (int)(fabs(s - own) <= near);
+            }
+            gone[g] = before >= a.topk_groups;
+            // the last group that stays must stand clear of the others
+            if (ORDER != kLogits)
+                sure &= !(before == a.topk_groups - 1 && close > 1 && own > kNone);
+        }
+        wave_lds();
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-            const int g = min((c * L + lane) / per, a.G - 1);
-            const double own = groups[slot][g];
-            int before = 0;
-            for (int o = 0; o < a.G; ++o) {
-                const double s = groups[slot][o];
-                before += s > own || (s == own && o < g) ? 1 : 0;
-            }
-            if (before >= a.topk_groups)
+            const bool out = gone[min((c * L + lane) / per, a.G - 1)] != 0;
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    key[c][i] = -INFINITY;
+            for (int i = 0; i < 8; ++i)
+                key[c][i] = out ? 2.0 * kNone : key[c][i];
         }
+        wave_lds();
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -399,97 +515,95 @@ __global__ __launch_bounds__(kThreads) void route_kernel(Args a)
     for (int c = 1; c < CH; ++c)
         merge8(best, key[c]);
     merge_lanes<L>(best);
+    if (ORDER == kLogits)
+        return true;
+
+    // The chosen stand clear of each other and, counted, of the rest.
+    double last = 0.0;
+    int over = 0, want = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const bool is = i < a.K && best[i] > kNone;
+        if (i > 0)
+            sure &= !is || best[i > 0 ? i - 1 : 0] - best[i] > margin<ORDER>(best[i > 0 ? i - 1 : 0], top);
+        last = is ? best[i] : last;
+        want += (int)is;
+    }
+    const double bar = last - margin<ORDER>(last, top);
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            over += (int)(key[c][i] >= bar);
+    const int all = lane_sum<L>(over);
+    return sure & (want == 0 || all == want);
+}
+
+template <int L, int CH, Order ORDER>
+__global__ __launch_bounds__(kThreads) void route_kernel(Args a)
+{
+    constexpr int TOK = kThreads / L;
+    __shared__ double groups[TOK][kMaxGroups];
+    __shared__ int gone[TOK][kMaxGroups];
+    __shared__ double again[ORDER == kLogits ? 1 : kThreads / 64][ORDER == kLogits ? 1 : L * CH * 8];
+    const int lane = threadIdx.x % L, slot = threadIdx.x / L;
+    const int64_t t = (int64_t)blockIdx.x * TOK + slot;
+    const bool in = t < a.T;
+    const int64_t row = in ? t : a.T - 1;
+
+    float l[CH][8];
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+        load8(a.logits, a.bf16, a.vec, row, a.E, (c * L + lane) * 8, l[c]);
+
+    float m = 0.0f, inv = 1.0f;
+    if (ORDER == kSoftmax || (ORDER == kLogits && a.softmax && !a.renorm)) {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                mx = fmaxf(mx, l[c][i]);             // (fmaxf passes over a NaN)
+        mx = lane_max<L>(mx);
+        m = mx > -INFINITY ? mx : 0.0f;
+        float s = 0.0f;
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                s += l[c][i] > -INFINITY ? __expf(l[c][i] - m) : 0.0f;
+        s = lane_sum<L>(s);
+        inv = s > 0.0f ? 1.0f / s : 0.0f;
+    }
+
+    double best[8];
+    const bool sure = choose<L, CH, ORDER>(a, l, lane, m, inv, groups[slot], gone[slot], best);
 
     // lane k keeps the k-th best
-    double mine = -INFINITY;
+    double mine = 2.0 * kNone;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         mine = lane == i ? best[i] : mine;
     const bool live = in && lane < a.K && (!a.mask || a.mask[row] != 0);
-    const bool found = live && mine > -INFINITY;
+    const bool found = live && mine > kNone;
     const int e = found ? key_index(mine) : -1;
     const float chosen = found ? load_logit(a.logits, a.bf16, row * a.E + e) : -INFINITY;
-    const float w = weight_of<L>(a, chosen, m, inv);
-    if (in && lane < a.K) {
+    const float w = weight_of<L>(a, chosen, (double)m, (double)inv);
+    constexpr uint64_t lanes = L == 64 ? ~0ull : (1ull << (L % 64)) - 1;      // of a token
+    uint64_t doubt = ORDER == kLogits ? 0 : __builtin_amdgcn_ballot_w64(!sure && in);
+    if (in && lane < a.K && ((doubt >> (threadIdx.x % 64 - lane)) & lanes) == 0) {
         a.idx[t * a.K + lane] = e;
         a.w[t * a.K + lane] = found ? w : 0.0f;
     }
-}
-
-// ---- any top-k, any groups: a wave a token, its keys in LDS ----------------
-//
-// K rounds, each the largest key below the last round's. For sizes that the
-// kernel above does not cover (K above 8, groups that end inside a piece).
-__global__ __launch_bounds__(64) void route_any_kernel(Args a)
-{
-    __shared__ double key[kMaxExperts];
-    __shared__ double score[kMaxGroups];
-    __shared__ int kept[kMaxTopk];
-    const int lane = threadIdx.x;
-    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-        double m = 0.0, inv = 1.0;
-        if (a.softmax) {
-            float mx = -INFINITY;
-            for (int e = lane; e < a.E; e += 64)
-                mx = fmaxf(mx, usable(load_logit(a.logits, a.bf16, t * a.E + e)));
-            mx = lane_max<64>(mx);
-            m = mx > -INFINITY ? (double)mx : 0.0;
-            double s = 0.0;
-            for (int e = lane; e < a.E; e += 64) {
-                const float l = load_logit(a.logits, a.bf16, t * a.E + e);
-                s += l > -INFINITY ? exp64((double)l - m) : 0.0;
-            }
-            s = lane_sum<64>(s);
-            inv = s > 0.0 ? 1.0 / s : 0.0;
+    if constexpr (ORDER != kLogits) {
+        // tokens in doubt, one after the other, by the whole wave
+        const int wave = threadIdx.x / 64;
+        const int64_t t0 = (int64_t)blockIdx.x * TOK + wave * (64 / L);
+        while (doubt != 0) {
+            const int which = __builtin_ctzll(doubt) / L;
+            doubt &= ~(lanes << (which * L % 64));
+            route_token(a, t0 + which, threadIdx.x % 64, again[wave], groups[wave * (64 / L)]);
         }
-        for (int e = lane; e < a.E; e += 64) {
-            const double s = choice(a, load_logit(a.logits, a.bf16, t * a.E + e),
-                                    a.bias ? a.bias[e] : 0.0f, m, inv);
-            key[e] = s > -INFINITY ? make_key(s, e) : -INFINITY;
-        }
-        __syncthreads();
-        if (a.G > 1) {
-            const int size = a.E / a.G;
-            if (lane < a.G) {
-                double x = -INFINITY, y = -INFINITY;
-                for (int i = 0; i < size; ++i)
-                    two_best(x, y, key[lane * size + i], -INFINITY);
-                score[lane] = group_score(a, x, y);
-            }
-            __syncthreads();
-            bool gone = false;
-            if (lane < a.G) {
-                int before = 0;
-                for (int o = 0; o < a.G; ++o)
-                    before += score[o] > score[lane] || (score[o] == score[lane] && o < lane) ? 1 : 0;
-                gone = before >= a.topk_groups;
-            }
-            if (gone)
-                for (int i = 0; i < size; ++i)
-                    key[lane * size + i] = -INFINITY;
-            __syncthreads();
-        }
-        const bool live = !a.mask || a.mask[t] != 0;
-        double last = INFINITY;
-        for (int k = 0; k < a.K; ++k) {
-            double x = -INFINITY;
-            for (int e = lane; e < a.E; e += 64) {
-                const double v = key[e];
-                x = v < last && v > x ? v : x;
-            }
-            last = lane_max<64>(x);
-            if (lane == k)
-                kept[k] = live && last > -INFINITY ? key_index(last) : -1;
-        }
-        __syncthreads();
-        const int e = lane < a.K ? kept[lane] : -1;
-        const float l = e >= 0 ? load_logit(a.logits, a.bf16, t * a.E + e) : -INFINITY;
-        const float w = weight_of<64>(a, l, m, inv);
-        if (lane < a.K) {
-            a.idx[t * a.K + lane] = e;
-            a.w[t * a.K + lane] = e >= 0 ? w : 0.0f;
-        }
-        __syncthreads();
     }
 }
 
