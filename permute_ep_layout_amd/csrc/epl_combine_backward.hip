@@ -49,8 +49,8 @@ __device__ __forceinline__ void load_dy(const void *p, int64_t at, float (&d)[8]
 }
 
 // WAVES waves a token share its columns; their partial dot products are
-// added in wave order through LDS.
-template <bool BF16, int WAVES>
+// added in wave order through LDS. STREAM: rows past the caches, in and out.
+template <bool BF16, int WAVES, bool STREAM>
 __global__ __launch_bounds__(WAVES * 64) void kernel(Args a)
 {
     __shared__ float part[WAVES][kSlots];
@@ -78,8 +78,10 @@ __global__ __launch_bounds__(WAVES * 64) void kernel(Args a)
                 bf16x8 v[kSlots];
 #pragma unroll
                 for (int s = 0; s < kSlots; ++s)
-                    if (row[s] >= 0)
-                        v[s] = *reinterpret_cast<const bf16x8 *>(a.v + row[s] * a.H + h);
+                    if (row[s] >= 0) {
+                        const auto *at = reinterpret_cast<const bf16x8 *>(a.v + row[s] * a.H + h);
+                        v[s] = STREAM ? __builtin_nontemporal_load(at) : *at;
+                    }
 #pragma unroll
                 for (int s = 0; s < kSlots; ++s) {
                     if (row[s] < 0)
@@ -90,7 +92,11 @@ __global__ __launch_bounds__(WAVES * 64) void kernel(Args a)
                         dot[s] = fmaf(d[i], (float)v[s][i], dot[s]);
                         g[i] = (__bf16)(w[s] * d[i]);
                     }
-                    *reinterpret_cast<bf16x8 *>(a.dv + row[s] * a.H + h) = g;
+                    auto *at = reinterpret_cast<bf16x8 *>(a.dv + row[s] * a.H + h);
+                    if (STREAM)
+                        __builtin_nontemporal_store(g, at);
+                    else
+                        *at = g;
                 }
             }
 #pragma unroll
@@ -155,11 +161,17 @@ extern "C" int epl_combine_backward(const epl_problem *p, int grad_type, const v
         hipLaunchKernelGGL(kernel, grid, dim3(waves * 64), 0, s, a);
     };
     const bool bf16 = grad_type == EPL_OUT_BF16;
-    // waves a token: one pass of 512 columns each where the row is short,
-    // four for longer rows
+    // A wave a token where a row is two passes of 512 columns at most; more
+    // share longer rows: 8 where the rows stay in the caches (64 tokens, top-8,
+    // 7168 columns: 8.5 us, against 8.9 with 4), and 4 that pass them by where
+    // they do not (4096 tokens: 192 us, 5.2 TB/s, against 205 through them).
+    const bool stream_rows = a.T * a.K * (int64_t)a.H * 2 > (int64_t(128) << 20);
     if (a.H <= 1024)
-        bf16 ? launch(C::kernel<true, 1>, 1) : launch(C::kernel<false, 1>, 1);
+        stream_rows ? (bf16 ? launch(C::kernel<true, 1, true>, 1) : launch(C::kernel<false, 1, true>, 1))
+                    : (bf16 ? launch(C::kernel<true, 1, false>, 1) : launch(C::kernel<false, 1, false>, 1));
+    else if (stream_rows)
+        bf16 ? launch(C::kernel<true, 4, true>, 4) : launch(C::kernel<false, 4, true>, 4);
     else
-        bf16 ? launch(C::kernel<true, 4>, 4) : launch(C::kernel<false, 4>, 4);
+        bf16 ? launch(C::kernel<true, 8, false>, 8) : launch(C::kernel<false, 8, false>, 8);
     return hipGetLastError() == hipSuccess ? EPL_OK : EPL_EHIP;
 }
