@@ -96,8 +96,9 @@ __device__ __forceinline__ void load_bf16(const __bf16 *p, float (&v)[C])
         v[i] = (float)r[i];
 }
 
-// One rounding to nearest even, of the finished binary32 value.
-template <int C>
+// One rounding to nearest even, of the finished binary32 value. PAST: past
+// the caches.
+template <int C, bool PAST = false>
 __device__ __forceinline__ void store_bf16(__bf16 *p, const float (&v)[C])
 {
     typedef __bf16 vec __attribute__((ext_vector_type(C)));
@@ -105,19 +106,27 @@ __device__ __forceinline__ void store_bf16(__bf16 *p, const float (&v)[C])
 #pragma unroll
     for (int i = 0; i < C; ++i)
         r[i] = (__bf16)v[i];
-    *reinterpret_cast<vec *>(p) = r;
+    if (PAST)
+        __builtin_nontemporal_store(r, reinterpret_cast<vec *>(p));
+    else
+        *reinterpret_cast<vec *>(p) = r;
 }
 
-template <int C>
+template <int C, bool PAST = false>
 __device__ __forceinline__ void store_out(const Args &a, int64_t at, const float (&v)[C])
 {
     if (a.out_f32) {
         float *y = static_cast<float *>(a.y) + at;
 #pragma unroll
-        for (int i = 0; i < C; i += 4)
-            *reinterpret_cast<f32x4 *>(y + i) = f32x4{v[i], v[i + 1], v[i + 2], v[i + 3]};
+        for (int i = 0; i < C; i += 4) {
+            const f32x4 r = {v[i], v[i + 1], v[i + 2], v[i + 3]};
+            if (PAST)
+                __builtin_nontemporal_store(r, reinterpret_cast<f32x4 *>(y + i));
+            else
+                *reinterpret_cast<f32x4 *>(y + i) = r;
+        }
     } else {
-        store_bf16<C>(static_cast<__bf16 *>(a.y) + at, v);
+        store_bf16<C, PAST>(static_cast<__bf16 *>(a.y) + at, v);
     }
 }
 
@@ -169,99 +178,124 @@ __device__ __forceinline__ float gelu_slope(float z)
     return fabsf(z) > 15.0f ? (z > 0.0f ? 1.0f : 0.0f) : fmaf(z * 0.39894228040143268f, g, c);
 }
 
-// C columns n .. n + C - 1 of one row of the finished product (without bias).
+// What the epilogue of C columns of a row reads besides the product, as it
+// is in memory: of a gradient activation the saved columns (of the gated one
+// the gate's and the up half's), of the others the residual.
 template <int C>
-__device__ __forceinline__ void emit(const Args &a, int e, int64_t row, int n, float (&z)[C])
+struct Side {
+    typedef __bf16 vec __attribute__((ext_vector_type(C)));
+    vec x, y;
+};
+
+template <int C>
+__device__ __forceinline__ Side<C> side_of(const Args &a, int64_t row, int n)
+{
+    typedef typename Side<C>::vec vec;
+    Side<C> s = {};
+    if (a.act == EPL_ACT_SWIGLU_GRAD) {
+        s.x = *reinterpret_cast<const vec *>(a.pre + row * 2 * a.N + n);
+        s.y = *reinterpret_cast<const vec *>(a.pre + row * 2 * a.N + a.N + n);
+    } else if (a.act >= EPL_ACT_SILU_GRAD) {
+        s.x = *reinterpret_cast<const vec *>(a.pre + row * a.N + n);
+    } else if (a.residual) {
+        s.x = *reinterpret_cast<const vec *>(a.residual + row * (a.act == EPL_ACT_SWIGLU ? a.N / 2 : a.N) + n);
+    }
+    return s;
+}
+
+// The bias of C columns, or zeros.
+template <int C>
+__device__ __forceinline__ void bias_of(const Args &a, int e, int n, float (&b)[C])
+{
+#pragma unroll
+    for (int i = 0; i < C; i += 4) {
+        f32x4 v = {0, 0, 0, 0};
+        if (a.bias)
+            v = *reinterpret_cast<const f32x4 *>(a.bias + (int64_t)e * a.N + n + i);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            b[i + j] = v[j];
+    }
+}
+
+// C columns n .. n + C - 1 of one row of the finished product.
+template <int C>
+__device__ __forceinline__ void emit(const Args &a, int64_t row, int n, const float (&b)[C],
+                                     const Side<C> &s, float (&z)[C])
 {
     if (a.act == EPL_ACT_SWIGLU_GRAD) {
         // saved [rows, 2 N]: gate, up; y likewise
-        float gate[C], up[C], dg[C], du[C];
-        const int64_t at = row * 2 * a.N + n;
-        load_bf16<C>(a.pre + at, gate);
-        load_bf16<C>(a.pre + at + a.N, up);
+        float dg[C], du[C];
 #pragma unroll
         for (int i = 0; i < C; ++i) {
-            dg[i] = z[i] * up[i] * silu_slope(gate[i]);
-            du[i] = z[i] * silu(gate[i]);
+            dg[i] = z[i] * (float)s.y[i] * silu_slope((float)s.x[i]);
+            du[i] = z[i] * silu((float)s.x[i]);
         }
-        store_out<C>(a, at, dg);
-        store_out<C>(a, at + a.N, du);
+        store_out<C>(a, row * 2 * a.N + n, dg);
+        store_out<C>(a, row * 2 * a.N + a.N + n, du);
         return;
     }
     const int64_t at = row * a.N + n;
-    if (a.act == EPL_ACT_SILU_GRAD || a.act == EPL_ACT_GELU_GRAD) {
-        float s[C];
-        load_bf16<C>(a.pre + at, s);
+    if (a.act == EPL_ACT_SILU_GRAD) {
 #pragma unroll
         for (int i = 0; i < C; ++i)
-            z[i] *= a.act == EPL_ACT_SILU_GRAD ? silu_slope(s[i]) : gelu_slope(s[i]);
-        store_out<C>(a, at, z);
-        return;
-    }
-    if (a.bias) {
-        const float *b = a.bias + (int64_t)e * a.N + n;
+            z[i] *= silu_slope((float)s.x[i]);
+    } else if (a.act == EPL_ACT_GELU_GRAD) {
 #pragma unroll
-        for (int i = 0; i < C; i += 4) {
-            const f32x4 v = *reinterpret_cast<const f32x4 *>(b + i);
+        for (int i = 0; i < C; ++i)
+            z[i] *= gelu_slope((float)s.x[i]);
+    } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                z[i + j] += v[j];
+        for (int i = 0; i < C; ++i)
+            z[i] += b[i];
+        if (a.pre)
+            store_bf16<C, true>(a.pre + at, z);          // read by the backward pass, much later
+        if (a.act == EPL_ACT_SILU) {
+#pragma unroll
+            for (int i = 0; i < C; ++i)
+                z[i] = silu(z[i]);
+        } else if (a.act == EPL_ACT_GELU) {
+#pragma unroll
+            for (int i = 0; i < C; ++i)
+                z[i] = gelu(z[i]);
         }
-    }
-    if (a.pre)
-        store_bf16<C>(a.pre + at, z);
-    if (a.act == EPL_ACT_SILU) {
+        if (a.residual)
 #pragma unroll
-        for (int i = 0; i < C; ++i)
-            z[i] = silu(z[i]);
-    } else if (a.act == EPL_ACT_GELU) {
-#pragma unroll
-        for (int i = 0; i < C; ++i)
-            z[i] = gelu(z[i]);
-    }
-    if (a.residual) {
-        float r[C];
-        load_bf16<C>(a.residual + at, r);
-#pragma unroll
-        for (int i = 0; i < C; ++i)
-            z[i] += r[i];
+            for (int i = 0; i < C; ++i)
+                z[i] += (float)s.x[i];
     }
     store_out<C>(a, at, z);
 }
 
 // The gated activation: columns f .. f + C - 1 of the gate half and of the up half.
 template <int C>
-__device__ __forceinline__ void emit_pair(const Args &a, int e, int64_t row, int f, float (&g)[C],
+__device__ __forceinline__ void emit_pair(const Args &a, int64_t row, int f, const float (&bg)[C],
+                                          const float (&bu)[C], const Side<C> &s, float (&g)[C],
                                           float (&u)[C])
 {
     const int F = a.N / 2;
-    if (a.bias) {
-        const float *b = a.bias + (int64_t)e * a.N + f;
-#pragma unroll
-        for (int i = 0; i < C; ++i) {
-            g[i] += b[i];
-            u[i] += b[F + i];
-        }
-    }
-    if (a.pre) {
-        store_bf16<C>(a.pre + row * a.N + f, g);
-        store_bf16<C>(a.pre + row * a.N + F + f, u);
-    }
     float v[C];
 #pragma unroll
-    for (int i = 0; i < C; ++i)
+    for (int i = 0; i < C; ++i) {
+        g[i] += bg[i];
+        u[i] += bu[i];
         v[i] = silu(g[i]) * u[i];
-    if (a.residual) {
-        float r[C];
-        load_bf16<C>(a.residual + row * F + f, r);
+    }
+    if (a.pre) {
+        store_bf16<C, true>(a.pre + row * a.N + f, g);
+        store_bf16<C, true>(a.pre + row * a.N + F + f, u);
+    }
+    if (a.residual)
 #pragma unroll
         for (int i = 0; i < C; ++i)
-            v[i] += r[i];
-    }
+            v[i] += (float)s.x[i];
     store_out<C>(a, row * F + f, v);
 }
 
-// C neighbouring elements of a weight gradient.
+// C neighbouring elements of a weight gradient: past the caches, which hold
+// the operands that tiles share (64 experts of 192 rows, 2048 x 4096 in
+// binary32: 653 us through them, 584 past them; of 500 rows, 2048 x 2048: 415,
+// 350). Whoever reads gradients of this size next finds them in memory anyway.
 template <int C>
 __device__ __forceinline__ void emit_weight(const Args &a, int64_t at, float (&v)[C])
 {
@@ -278,7 +312,7 @@ __device__ __forceinline__ void emit_weight(const Args &a, int64_t at, float (&v
         for (int x = 0; x < C; ++x)
             v[x] += old[x];
     }
-    store_out<C>(a, at, v);
+    store_out<C, true>(a, at, v);
 }
 
 // ----------------------------------------------------------- tile kernel --
@@ -481,15 +515,13 @@ __device__ __forceinline__ void emit_rows(const Args &a, const Tile &x, const fl
     const bool four = FORM == kWeightGrad && a.out_f32;
     const int lanes = four ? 16 : paired ? 4 : 8;             // a row
     const int last = FORM == kWeightGrad ? a.N : x.cnt;
+    const int c = (lane % lanes) * (64 / lanes), n = x.tn * BN + n0 + c, step = 64 / lanes;
+    if (FORM == kWeightGrad) {
+        if (n >= a.K)
+            return;
 #pragma unroll 1
-    for (int row = lane / lanes; row < rows; row += 64 / lanes) {
-        const int m = m0 + row, c = (lane % lanes) * (64 / lanes), n = x.tn * BN + n0 + c;
-        if (m >= last)
-            break;
-        if (FORM == kWeightGrad) {
-            if (n >= a.K)
-                continue;
-            const int64_t at = ((int64_t)x.e * a.N + m) * a.K + n;
+        for (int row = lane / lanes; row < rows && m0 + row < last; row += step) {
+            const int64_t at = ((int64_t)x.e * a.N + m0 + row) * a.K + n;
             if (four) {
                 float v[4];
                 take<4>(mine, row, c, v);
@@ -499,16 +531,38 @@ __device__ __forceinline__ void emit_rows(const Args &a, const Tile &x, const fl
                 take<8>(mine, row, c, v);
                 emit_weight<8>(a, at, v);
             }
-            continue;
         }
-        float v[8], u[8];
-        take<8>(mine, row, c, v);
-        if (paired) {
-            take<8>(mine, row, c + 8, u);
-            if (n / 2 < a.N / 2)
-                emit_pair<8>(a, x.e, x.lo + m, n / 2, v, u);
-        } else if (n < a.N) {
-            emit<8>(a, x.e, x.lo + m, n, v);
+        return;
+    }
+    if (n >= a.N)
+        return;
+    const int f = paired ? n / 2 : n;                         // column of y
+    float b[8], bu[8];
+    bias_of<8>(a, x.e, f, b);
+    bias_of<8>(a, x.e, paired ? a.N / 2 + f : f, bu);
+    // what four rows read is on its way before the first is finished (one at
+    // a time, the gated gradient of 12289 x 2048 outputs took 385 us, not
+    // {TIMES})
+    constexpr int ahead = 4;
+#pragma unroll 1
+    for (int row0 = lane / lanes; row0 < rows && m0 + row0 < last; row0 += ahead * step) {
+        Side<8> s[ahead];
+#pragma unroll
+        for (int i = 0; i < ahead; ++i)
+            s[i] = side_of<8>(a, x.lo + min(m0 + row0 + i * step, last - 1), f);
+#pragma unroll
+        for (int i = 0; i < ahead; ++i) {
+            const int row = row0 + i * step;
+            if (row >= rows || m0 + row >= last)
+                break;
+            float v[8], u[8];
+            take<8>(mine, row, c, v);
+            if (paired) {
+                take<8>(mine, row, c + 8, u);
+                emit_pair<8>(a, x.lo + m0 + row, f, b, bu, s[i], v, u);
+            } else {
+                emit<8>(a, x.lo + m0 + row, n, b, s[i], v);
+            }
         }
     }
 }
@@ -906,16 +960,23 @@ __device__ __forceinline__ void few_rows(const Args &a, int e, int64_t row0, int
 #pragma unroll
         for (int x = 0; x < 4; ++x)
             g[x] = sum[0][x], u[x] = sum[1][x];
-        if (f < a.N / 2)
-            emit_pair<4>(a, e, row0 + m, f, g, u);
+        if (f < a.N / 2) {
+            float bg[4], bu[4];
+            bias_of<4>(a, e, f, bg);
+            bias_of<4>(a, e, a.N / 2 + f, bu);
+            emit_pair<4>(a, row0 + m, f, bg, bu, side_of<4>(a, row0 + m, f), g, u);
+        }
     } else {
         const int n = nb * 32 + q * 8;
         float v[8];
 #pragma unroll
         for (int x = 0; x < 8; ++x)
             v[x] = sum[x >> 2][x & 3];
-        if (n < a.N)
-            emit<8>(a, e, row0 + m, n, v);
+        if (n < a.N) {
+            float b[8];
+            bias_of<8>(a, e, n, b);
+            emit<8>(a, row0 + m, n, b, side_of<8>(a, row0 + m, n), v);
+        }
     }
 }
 
