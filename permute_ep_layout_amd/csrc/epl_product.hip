@@ -219,7 +219,7 @@ int epl_expert_product(const epl_product_desc *p, const uint16_t *x, const uint1
     const Kind k = kind_of(*p);
     if (k == kFew) {
         // 16 waves a workgroup where 4 would leave the GPU mostly empty
-        const int nb = a.act == EPL_ACT_SWIGLU ? (a.N / 2 + 15) / 16 : (a.N + 31) / 32;
+        const int nb = (a.N + P::kFewCols - 1) / P::kFewCols;
         const dim3 grid((unsigned)nb, (unsigned)a.E);
         if ((int64_t)nb * a.E <= kCus)
             hipLaunchKernelGGL((P::few_rows_kernel<16>), grid, dim3(1024), 0, s, a);

@@ -878,9 +878,12 @@ __global__ __launch_bounds__(tile_threads(BN)) void join_kernel(Args a, int grid
 // contraction (128 deep a turn each) and add their sums through LDS in wave
 // order. Workgroups start at different places of the contraction and come
 // round, so that those under way at one time read different columns of their
-// rows, which lie on different memory channels.
+// rows, which lie on different memory channels (64 experts of one row, 4096
+// -> 2048: 231 us without, 178 with).
 
-constexpr int kFewCols = 32;
+constexpr int kFewCols = 32;            // two matrix instructions wide
+// (64 columns, which read x half as often: 8 experts of 1, 8, 14 rows, 7168 ->
+// 4096, 93, 98, 103 us against 87, 98, 108; more rows go to the tiles.)
 
 template <int WAVES, int MT>
 __device__ __forceinline__ void few_rows(const Args &a, int e, int64_t row0, int left, int nb,
@@ -888,34 +891,38 @@ __device__ __forceinline__ void few_rows(const Args &a, int e, int64_t row0, int
 {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, q = lane >> 4;
     const bool paired = a.act == EPL_ACT_SWIGLU;
+    constexpr int J = kFewCols / 16;
+    const int F = a.N / 2;
     const __bf16 *w = a.q + (int64_t)e * a.N * a.K;
-    const __bf16 *pw[2], *px[MT];
+    const __bf16 *pw[J], *px[MT];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < J; ++j) {
         // lane q holds 8 neighbouring columns, or 4 of the gate and the same 4 of the up half
-        int n = paired ? min(nb * 16 + r, a.N / 2 - 1) + j * (a.N / 2)
-                       : min(nb * 32 + (r >> 2) * 8 + j * 4 + (r & 3), a.N - 1);
+        const int n = paired ? min(nb * 16 + r, F - 1) + j * F
+                             : min(nb * 32 + (r >> 2) * 8 + j * 4 + (r & 3), a.N - 1);
         pw[j] = w + (int64_t)n * a.K + q * 8;
     }
 #pragma unroll
     for (int i = 0; i < MT; ++i)
         px[i] = a.p + (row0 + min(i * 16 + r, left - 1)) * a.K + q * 8;
-    f32x4 acc[MT][2];
+    f32x4 acc[MT][J];
 #pragma unroll
     for (int i = 0; i < MT; ++i)
-        acc[i][0] = acc[i][1] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+            acc[i][j] = f32x4{0, 0, 0, 0};
 
     const bf16x8 zero = {};
     const int turns = (a.K + 127) / 128;
     int at = (int)((uint32_t)(e * 13 + nb * 3 + wave) % (uint32_t)turns);
     for (int t = wave; t < turns; t += WAVES) {
-        bf16x8 fw[4][2], fx[4][MT];
+        bf16x8 fw[4][J], fx[4][MT];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             const int k = at * 128 + u * 32;
             const bool in = k + q * 8 < a.K;
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < J; ++j)
                 fw[u][j] = in ? *reinterpret_cast<const bf16x8 *>(pw[j] + k) : zero;
 #pragma unroll
             for (int i = 0; i < MT; ++i)
@@ -926,7 +933,7 @@ __device__ __forceinline__ void few_rows(const Args &a, int e, int64_t row0, int
 #pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
+                for (int j = 0; j < J; ++j)
                     acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fw[u][j], fx[u][i],
                                                                         acc[i][j], 0, 0, 0);
         at += WAVES;
@@ -938,52 +945,50 @@ __device__ __forceinline__ void few_rows(const Args &a, int e, int64_t row0, int
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-            red[((wave * MT + i) * 2 + j) * 64 + lane] = acc[i][j];
+        for (int j = 0; j < J; ++j)
+            red[((wave * MT + i) * J + j) * 64 + lane] = acc[i][j];
     __syncthreads();
     if (wave >= MT)
         return;
-    f32x4 sum[2];
+    float v[J * 4];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        sum[j] = red[(wave * 2 + j) * 64 + lane];
+    for (int j = 0; j < J; ++j) {
+        f32x4 sum = red[(wave * J + j) * 64 + lane];
 #pragma unroll
-        for (int v = 1; v < WAVES; ++v)
-            sum[j] += red[((v * MT + wave) * 2 + j) * 64 + lane];
+        for (int o = 1; o < WAVES; ++o)
+            sum += red[((o * MT + wave) * J + j) * 64 + lane];
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            v[j * 4 + x] = sum[x];
     }
-    const int m = wave * 16 + r;
-    if (m >= left)
+    const int64_t row = row0 + wave * 16 + r;
+    if (wave * 16 + r >= left)
         return;
     if (paired) {
         const int f = nb * 16 + q * 4;
-        float g[4], u[4];
+        if (f < F) {
+            float bg[4], bu[4], g[4], u[4];
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
-            g[x] = sum[0][x], u[x] = sum[1][x];
-        if (f < a.N / 2) {
-            float bg[4], bu[4];
+            for (int x = 0; x < 4; ++x)
+                g[x] = v[x], u[x] = v[4 + x];
             bias_of<4>(a, e, f, bg);
-            bias_of<4>(a, e, a.N / 2 + f, bu);
-            emit_pair<4>(a, row0 + m, f, bg, bu, side_of<4>(a, row0 + m, f), g, u);
+            bias_of<4>(a, e, F + f, bu);
+            emit_pair<4>(a, row, f, bg, bu, side_of<4>(a, row, f), g, u);
         }
     } else {
         const int n = nb * 32 + q * 8;
-        float v[8];
-#pragma unroll
-        for (int x = 0; x < 8; ++x)
-            v[x] = sum[x >> 2][x & 3];
         if (n < a.N) {
             float b[8];
             bias_of<8>(a, e, n, b);
-            emit<8>(a, row0 + m, n, b, side_of<8>(a, row0 + m, n), v);
+            emit<8>(a, row, n, b, side_of<8>(a, row, n), v);
         }
     }
 }
 
 template <int WAVES>
-__global__ __launch_bounds__(WAVES * 64, 4) void few_rows_kernel(Args a)
+__global__ __launch_bounds__(WAVES * 64, WAVES == 4 ? 2 : 4) void few_rows_kernel(Args a)
 {
-    __shared__ f32x4 red[WAVES * 2 * 2 * 64];
+    __shared__ f32x4 red[WAVES * 2 * (kFewCols / 16) * 64];
     const int e = blockIdx.y, nb = blockIdx.x;
     int64_t lo;
     const int cnt = block_of(a, e, lo);
