@@ -248,9 +248,15 @@ def load() -> ctypes.CDLL:
 
 # ----------------------------------------------------------- marshalling --
 
+_TORCH = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = torch
+    return _TORCH
 
 
 def _ptr(t) -> Optional[int]:
@@ -643,7 +649,7 @@ def _launch(name: str, dev, stream, *args):
     launched on the current device, which need not be the tensors') and the
     stream last."""
     torch = _torch()
-    fn = getattr(load(), name)
+    fn = getattr(_LIB or load(), name)
     current = torch.cuda.current_device()
     index = current if dev.index is None else dev.index
     raw = _raw_stream(index) if stream is None else _stream(stream)
