@@ -144,11 +144,6 @@ int epl_route_backward(const epl_router *p, const void *logits, const int64_t *t
         return EPL_EINVAL;
     namespace R = epl_router_k;
     R::GradArgs a{};
-    a.logits = logits;
-    a.idx = topk_idx;
-    a.g = grad_weights;
-    a.out = grad_logits;
-    a.T = p->num_tokens;
     a.K = p->num_topk;
     a.E = p->num_experts;
     a.softmax = p->score == EPL_SCORE_SOFTMAX;
@@ -160,8 +155,18 @@ int epl_route_backward(const epl_router *p, const void *logits, const int64_t *t
     const int pieces = (a.E + 7) / 8;
     auto launch = [&](auto kernel, int L) {
         const int tok = R::kThreads / L;
-        hipLaunchKernelGGL(kernel, dim3((unsigned)((a.T + tok - 1) / tok)), dim3(R::kThreads), 0, s,
-                           a);
+        // at most 2^30 work-items a launch (a loop over tokens in the kernel
+        // took 27.7 us instead of 25.9 for 65536 x 256 logits)
+        const int64_t most = (int64_t)tok << 22, T = p->num_tokens;
+        for (int64_t t0 = 0; t0 < T; t0 += most) {
+            a.T = std::min(T - t0, most);
+            a.logits = static_cast<const char *>(logits) + t0 * a.E * size;
+            a.idx = topk_idx + t0 * a.K;
+            a.g = grad_weights + t0 * a.K;
+            a.out = static_cast<char *>(grad_logits) + t0 * a.E * size;
+            hipLaunchKernelGGL(kernel, dim3((unsigned)((a.T + tok - 1) / tok)), dim3(R::kThreads),
+                               0, s, a);
+        }
         return launch_status();
     };
     if (pieces <= 8)

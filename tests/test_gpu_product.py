@@ -328,6 +328,72 @@ def test_repeats_bit_for_bit_and_streams():
     assert torch.equal(dw, dw2)
 
 
+def test_split_products_on_two_streams_and_in_a_graph():
+    """Calls that split their sums, each with a workspace of its own: at once
+    on two streams, and captured, replayed against the eager result."""
+    x, w = randn(300, 4096, seed=1).to(DEV), randn(1, 256, 4096, seed=2, std=0.02).to(DEV)
+    g = randn(300, 256, seed=3).to(DEV)
+    start, count = i32([0]), i32([300])
+
+    def run():
+        y = epl.expert_product(x, w, start, count, activation="silu", out_dtype=torch.float32)
+        dx = epl.expert_product(g, w, start, count, transposed=True)
+        return y, dx, epl.expert_weight_grad(g, x, start, count, out_dtype=torch.float32)
+
+    eager = run()
+    p = epl.Product(300, 0, 1, 4096, 256, 0, 1, 0, 0)
+    assert epl.epl_product_workspace_bytes(p) > 0
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    outs = []
+    for s in streams * 3:
+        with torch.cuda.stream(s):
+            outs.append(run())
+    torch.cuda.synchronize()
+    for out in outs:
+        for a, b in zip(out, eager):
+            assert torch.equal(a, b)
+    # a stream named in the call
+    y = epl.expert_product(x, w, start, count, activation="silu", out_dtype=torch.float32,
+                           stream=streams[0])
+    streams[0].synchronize()
+    assert torch.equal(y, eager[0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kept = run()
+    for n in range(4):
+        for t in kept:
+            t.zero_()
+        keep = x.clone()
+        x.mul_(2.0 if n % 2 else 1.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = run()
+        for a, b in zip(kept, want):
+            assert torch.equal(a, b)
+        x.copy_(keep)
+
+
+def test_workspace_is_checked():
+    x, w = randn(300, 4096, seed=1).to(DEV), randn(1, 256, 4096, seed=2).to(DEV)
+    p = epl.Product(300, 0, 1, 4096, 256, 0, 0, 1, 0)
+    y = torch.zeros(300, 256, dtype=torch.bfloat16, device=DEV)
+    need = epl.epl_product_workspace_bytes(p)
+    small = torch.zeros(need - 256, dtype=torch.uint8, device=DEV)
+    with pytest.raises(ValueError, match="workspace holds"):
+        epl.epl_expert_product(p, x, w, None, None, i32([0]), i32([300]), None, y, small)
+    odd = torch.zeros(need + 16, dtype=torch.uint8, device=DEV)[16:]
+    with pytest.raises(epl.EplError):
+        epl.epl_expert_product(p, x, w, None, None, i32([0]), i32([300]), None, y, odd)
+    with pytest.raises(ValueError, match="contiguous"):
+        epl.expert_product(x[:, ::2], w[:, :, ::2].contiguous(), i32([0]), i32([300]))
+    with pytest.raises(TypeError, match="num_tokens_per_expert"):
+        epl.expert_product(x, w, i32([0]), i32([300]).long())
+    with pytest.raises(epl.EplError):                 # x off a 16-byte boundary
+        flat = torch.zeros(300 * 4096 + 4, dtype=torch.bfloat16, device=DEV)
+        epl.expert_product(flat[4:].view(300, 4096), w, i32([0]), i32([300]))
+
+
 # ------------------------------------------------------- weight gradient --
 
 def check_weight_grad(counts, N, K, out=torch.float32, bias=True, accumulate=False, gap=0, rows=None,

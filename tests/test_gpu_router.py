@@ -311,6 +311,55 @@ def test_gradient(T, E, K, score, renorm, dtype):
     check_grad(x, idx, g, score, renorm, 2.5)
 
 
+def test_empty_batches_and_refusals():
+    for E in (16, 256):
+        idx, w = epl.route(torch.zeros(0, E, device=DEV), 4)
+        assert idx.shape == w.shape == (0, 4)
+        assert epl.route_backward(torch.zeros(0, E, device=DEV), idx, w).shape == (0, E)
+    x = torch.zeros(4, 32, device=DEV)
+    with pytest.raises(ValueError, match="contiguous"):
+        epl.route(x[:, ::2], 2)
+    with pytest.raises(ValueError, match="bias must have shape"):
+        epl.route(x, 2, bias=torch.zeros(16, device=DEV))
+    with pytest.raises(TypeError, match="token_mask"):
+        epl.route(x, 2, token_mask=torch.ones(4, dtype=torch.bool, device=DEV))
+    with pytest.raises(ValueError, match="must be a GPU tensor"):
+        epl.route(x, 2, bias=torch.zeros(32))
+    idx, w = epl.route(x, 2)
+    with pytest.raises(ValueError, match="grad_weights"):
+        epl.route_backward(x, idx, w[:2].contiguous())
+
+
+def test_router_captured_and_on_another_stream():
+    x = logits_of(4100, 256, torch.float32, seed=1).to(DEV)
+    b = torch.linspace(-0.1, 0.1, 256, device=DEV)
+    rules = dict(score="sigmoid", bias=b, num_groups=8, topk_groups=4, group_top=2,
+                 renormalize=True, scale=2.5)
+    g = torch.randn(4100, 8, device=DEV)
+
+    def run():
+        idx, w = epl.route(x, 8, **rules)
+        return idx, w, epl.route_backward(x, idx, g, score="sigmoid", renormalize=True, scale=2.5)
+
+    eager = run()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        other = run()
+    side.synchronize()
+    for a, c in zip(other, eager):
+        assert torch.equal(a, c)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kept = run()
+    for n in range(4):
+        x.add_(0.25 * x.flip(1))
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, c in zip(kept, run()):
+            assert torch.equal(a, c)
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("renorm", [False, True])
 def test_gradient_of_odd_choices(score, renorm):
