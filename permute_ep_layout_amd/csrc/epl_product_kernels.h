@@ -791,6 +791,8 @@ __global__ __launch_bounds__(tile_threads(BN), 2) void tile_kernel(Args a)
             turn(s + 1, sp1, sq1, sp0, sq0);
         }
         landed();                            // (what was fetched past the end too)
+        if (PT)
+            walk(ap[0], 4 % IP * 32);        // back from the 4 pieces read ahead
 
         const int m0 = tm * BM + wm * (BM / WM), n0 = wn * 64;
         own = tid & 63;

@@ -221,6 +221,17 @@ def test_split_rows(counts, N, K, accumulate):
     check_weight_grad(counts, N, K, accumulate=accumulate, seed=5)
 
 
+@pytest.mark.parametrize("transposed", [False, True])
+@pytest.mark.parametrize("counts,K,act", [
+    ([300, 10, 260, 700, 257] * 4, 136, "silu"),       # 448 tiles of 256 x 256
+    ([100, 30, 128, 129, 0] * 8, 72, "swiglu"),        # 640 of 128 x 128
+])
+def test_products_of_many_tiles(counts, K, act, transposed):
+    """Workgroups that make several tiles, one after the other."""
+    check_product(counts, K, 2048, act=act, bias=True, residual=True, pre=True,
+                  transposed=transposed, seed=K)
+
+
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("transposed", [False, True])
 @pytest.mark.parametrize("expected", [4, 4 * 100, 0])
@@ -437,6 +448,15 @@ def check_weight_grad(counts, N, K, out=torch.float32, bias=True, accumulate=Fal
 @pytest.mark.parametrize("accumulate", [False, True])
 def test_weight_grad(N, K, out, accumulate):
     check_weight_grad([0, 1, 63, 64, 65, 130, 300], N, K, out, accumulate=accumulate, seed=N)
+
+
+@pytest.mark.parametrize("counts,N,K", [
+    ([100, 40, 0, 130, 64], 2048, 4096),         # 640 tiles of 256 x 256
+    ([20, 70] * 20, 384, 1024),                  # 960 of 128 x 128
+])
+def test_weight_grad_of_many_tiles(counts, N, K):
+    """Workgroups that make several tiles, one after the other."""
+    check_weight_grad(counts, N, K, out=torch.bfloat16, seed=K)
 
 
 def test_weight_grad_blocks():
