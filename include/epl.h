@@ -495,7 +495,7 @@ int64_t epl_total(const void *workspace, void *stream);
 /* Static text for a status code. */
 const char *epl_strerror(int code);
 
-/* Library version, e.g. 0x000300 for 0.3.0. */
+/* Library version, e.g. 0x000400 for 0.4.0. */
 int epl_version(void);
 
 #ifdef __cplusplus

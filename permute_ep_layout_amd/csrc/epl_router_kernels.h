@@ -428,7 +428,8 @@ __global__ __launch_bounds__(64) void route_any_kernel(Args a)
 // Piece c of lane i holds experts (c L + i) 8 .. + 7. Each lane sorts its
 // pieces, merges them to its 8 best, and log2(L) merges across lanes leave
 // the token's 8 best, in order, in every lane. Bound by its vector
-// instructions: about 50 binary64 maxima and minima a token at L = 8.
+// instructions: 65536 tokens x 256 experts in binary32 take 22 us by softmax
+// (3.4 TB/s) and 40 us by sigmoid with a bias and 4 of 8 groups (1.8 TB/s).
 
 // The token's 8 best keys in every lane; false, on one of its lanes at least,
 // where the error of binary32 leaves their order in doubt. `groups` and
@@ -618,7 +619,10 @@ __global__ __launch_bounds__(kThreads) void route_kernel(Args a)
 //          softmax: d l_i = p_i (d p_i - sum_j p_j d p_j) for every expert
 // Slots that name the same expert add up. L lanes a token: each lane makes a
 // share of the K slots' values, puts them in LDS, and writes its pieces of 8
-// experts by comparing their indices with the slots'.
+// experts by comparing their indices with the slots'. Bound by memory:
+// 65536 x 256 in binary32, 23 us (4.7 TB/s); 16384 x 256 in bf16, 8.6 us, of
+// which 4 are its start and the two dependent reads. (A row built up in LDS
+// took 23.4 us for the first, and 34.8 against 29.5 for the dense softmax.)
 template <int L, int CH>
 __global__ __launch_bounds__(kThreads) void route_grad_kernel(GradArgs a)
 {
