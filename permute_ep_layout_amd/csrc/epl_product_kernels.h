@@ -398,11 +398,14 @@ __device__ __forceinline__ void walk(int &offset, int by)
 
 enum Form { kForward, kDataGrad, kWeightGrad };
 
-// The m tiles of the experts before each expert, and of all of them.
+// The m tiles of the experts before each expert, and of all of them: never
+// more than blocks apart from each other have, so that no sum overflows where
+// bad ones share rows.
 template <int BM, int THREADS>
 __device__ __forceinline__ void tile_prefix(const Args &a, int32_t *pre, int32_t *sums)
 {
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    const int most = (int)(a.rows / BM) + a.E;
     int base = 0;
     for (int e0 = 0; e0 < a.E; e0 += THREADS) {
         const int e = e0 + t;
@@ -418,11 +421,11 @@ __device__ __forceinline__ void tile_prefix(const Args &a, int32_t *pre, int32_t
         __syncthreads();
         int before = base;
         for (int w = 0; w < THREADS / 64; ++w) {
-            before += w < wave ? sums[w] : 0;
-            base += sums[w];
+            before = min(before + (w < wave ? sums[w] : 0), most);
+            base = min(base + sums[w], most);
         }
         if (e < a.E)
-            pre[e] = before + up - own;
+            pre[e] = min(before + up - own, most);
         __syncthreads();
     }
     if (t == 0)
