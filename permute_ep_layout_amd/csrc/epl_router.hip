@@ -95,6 +95,7 @@ int epl_route(const epl_router *p, const void *logits, const float *bias,
     const int pieces = (a.E + 7) / 8;
     const int per = a.G > 1 && (a.E / a.G) % 8 == 0 ? a.E / a.G / 8 : 0;
     const bool groups_fit = a.G == 1 || (per > 0 && (per & (per - 1)) == 0);
+    a.per_log = per > 0 ? 31 - __builtin_clz((unsigned)per) : 0;
     auto launch = [&](auto kernel, int L) {
         const int tok = R::kThreads / L;
         hipLaunchKernelGGL(kernel, dim3((unsigned)((a.T + tok - 1) / tok)), dim3(R::kThreads), 0, s,

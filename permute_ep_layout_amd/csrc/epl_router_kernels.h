@@ -36,6 +36,7 @@ struct Args {
     float *w;                      // [T, K]
     int64_t T;
     int K, E, G, topk_groups, group_top;
+    int per_log;                   // log2 of a group's pieces of 8 experts (route_kernel)
     bool softmax, renorm, bf16, need_scores, vec, bias_vec;
     float scale;
 };
@@ -143,15 +144,29 @@ __device__ __forceinline__ double exact_score(float l, float bias, double m, dou
         return sigmoid64((double)l) + (double)no_inf(bias);
 }
 
+// The key of the choice score in binary32, which make_key would give for it,
+// in fewer instructions: the score's binary64 has its low 29 bits clear, and a
+// sum with a score that is not negative is never -0. Of sigmoids `l` may be
+// +inf, which gives the same 1 as the largest finite logit.
 template <Order ORDER>
-__device__ __forceinline__ float fast_score(float l, float bias, float m, float inv)
+__device__ __forceinline__ double fast_key(float l, float bias, float m, float inv, int index)
 {
-    if constexpr (ORDER == kLogits)
-        return l;
-    else if constexpr (ORDER == kSoftmax)
-        return __expf(l - m) * inv + no_inf(bias);
-    else
-        return __builtin_amdgcn_rcpf(1.0f + __expf(-l)) + no_inf(bias);
+    float s;
+    bool candidate = l > -INFINITY;
+    if constexpr (ORDER == kLogits) {
+        s = l + 0.0f;                                                // -0 becomes +0
+    } else {
+        const float p = ORDER == kSoftmax ? __expf(l - m) * inv
+                                          : __builtin_amdgcn_rcpf(1.0f + __expf(-l));
+        const float sum = p + bias;
+        candidate &= sum > -INFINITY;                                // a NaN of either neither
+        s = __builtin_amdgcn_fmed3f(sum, -3.402823466e+38f, 3.402823466e+38f);
+    }
+    const uint64_t u = __builtin_bit_cast(uint64_t, (double)s);
+    const uint32_t hi = (uint32_t)(u >> 32);
+    const uint32_t flip = (uint32_t)((int32_t)hi >> 31) & (uint32_t)kIndexMask;
+    const uint32_t lo = (uint32_t)u | (((uint32_t)kIndexMask - (uint32_t)index) ^ flip);
+    return __builtin_bit_cast(double, ((uint64_t)(candidate ? hi : 0xffefffffu) << 32) | lo);
 }
 
 // How far two choice scores in binary32 must lie apart for their order to be
@@ -285,7 +300,8 @@ __device__ __forceinline__ double group_score(const Args &a, double best, double
 // LDS operations of one wave are in order: this keeps the compiler's order.
 __device__ __forceinline__ void wave_lds() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local"); }
 
-// Logits of 8 neighbouring experts; -inf past the row's end.
+// Logits of 8 neighbouring experts; -inf past the row's end. CLAMP: no_inf.
+template <bool CLAMP = true>
 __device__ __forceinline__ void load8(const void *p, bool bf16, bool vec, int64_t row, int E, int e0,
                                       float (&v)[8])
 {
@@ -296,14 +312,14 @@ __device__ __forceinline__ void load8(const void *p, bool bf16, bool vec, int64_
             const bf16x8 r = *reinterpret_cast<const bf16x8 *>(static_cast<const __bf16 *>(p) + at);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                v[i] = no_inf((float)r[i]);
+                v[i] = CLAMP ? no_inf((float)r[i]) : (float)r[i];
         } else {
             const float4 x = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + at);
             const float4 y = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + at + 4);
             const float t[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                v[i] = no_inf(t[i]);
+                v[i] = CLAMP ? no_inf(t[i]) : t[i];
         }
         return;
     }
@@ -428,8 +444,9 @@ __global__ __launch_bounds__(64) void route_any_kernel(Args a)
 // Piece c of lane i holds experts (c L + i) 8 .. + 7. Each lane sorts its
 // pieces, merges them to its 8 best, and log2(L) merges across lanes leave
 // the token's 8 best, in order, in every lane. Bound by its vector
-// instructions: 65536 tokens x 256 experts in binary32 take 22 us by softmax
-// (3.4 TB/s) and 40 us by sigmoid with a bias and 4 of 8 groups (1.8 TB/s).
+// instructions: 65536 tokens x 256 experts in binary32 take 20 us by sigmoid
+// (3.6 TB/s) and 34 us with a bias and 4 of 8 groups besides (2.1 TB/s), 1600
+// instructions a wave of 8 tokens, which issue in 84% of its cycles.
 
 // The token's 8 best keys in every lane; false, on one of its lanes at least,
 // where the error of binary32 leaves their order in doubt. `groups` and
@@ -459,14 +476,13 @@ __device__ __forceinline__ bool choose(const Args &a, const float (&l)[CH][8], i
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            key[c][i] = make_key((double)fast_score<ORDER>(l[c][i], b[i], m, inv), e0 + i,
-                                 usable(l[c][i], b[i]));
+            key[c][i] = fast_key<ORDER>(l[c][i], b[i], m, inv, e0 + i);
         sort8(key[c]);
     }
     if (a.G > 1) {
         // pieces lie within groups of `per` pieces (a power of two): the two
         // best keys of a group by exchanges; lane g then ranks group g
-        const int per = a.E / a.G / 8;
+        const int per = 1 << a.per_log;
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
             double x = key[c][0], y = key[c][1];
@@ -481,8 +497,8 @@ __device__ __forceinline__ bool choose(const Args &a, const float (&l)[CH][8], i
             if constexpr (L > 32)
                 if (per > 32) { two_best(x, y, lane_swap<32>(x), lane_swap<32>(y)); }
             const int piece = c * L + lane;
-            if (piece % per == 0 && piece / per < a.G)
-                groups[piece / per] = group_score(a, x, y);
+            if ((piece & (per - 1)) == 0 && piece >> a.per_log < a.G)
+                groups[piece >> a.per_log] = group_score(a, x, y);
         }
         wave_lds();
         for (int g = lane; g < a.G; g += L) {
@@ -502,10 +518,11 @@ __device__ __forceinline__ bool choose(const Args &a, const float (&l)[CH][8], i
         wave_lds();
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-            const bool out = gone[min((c * L + lane) / per, a.G - 1)] != 0;
+            // (a sum: half the instructions of a select)
+            const double out = gone[min((c * L + lane) >> a.per_log, a.G - 1)] ? -1e308 : 0.0;
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                key[c][i] = out ? 2.0 * kNone : key[c][i];
+                key[c][i] += out;
         }
         wave_lds();
     }
@@ -555,7 +572,7 @@ __global__ __launch_bounds__(kThreads) void route_kernel(Args a)
     float l[CH][8];
 #pragma unroll
     for (int c = 0; c < CH; ++c)
-        load8(a.logits, a.bf16, a.vec, row, a.E, (c * L + lane) * 8, l[c]);
+        load8<ORDER != kSigmoid>(a.logits, a.bf16, a.vec, row, a.E, (c * L + lane) * 8, l[c]);
 
     float m = 0.0f, inv = 1.0f;
     if (ORDER == kSoftmax || (ORDER == kLogits && a.softmax && !a.renorm)) {
