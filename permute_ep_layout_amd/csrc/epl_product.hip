@@ -70,18 +70,46 @@ int num_cus()
 // goes by the rows that the caller expects an expert to have on average.
 enum Kind { kFew, kLarge, kSmall };
 
-// Large tiles read the operands half as often as small ones, which come in
-// four times the number and share a CU in pairs. Measured (large, small), us:
-// 8 experts of 4096 rows, 7168 -> 4096: 1474, 1811; 64 of 192, 4096 -> 2048:
-// 277, 320; 8 of 256, 7168 -> 4096 (128 tiles): 149, 158; but 64 of 128:
-// 256, 218; 1 of 1000, 4096 -> 1024 (16 tiles): 37, 26; 16 of 500, 512 ->
-// 640 (96 tiles): 38, 21.
-Kind tiles_for(int64_t m, int64_t n, int64_t experts)
+int side_of(Kind k) { return k == kSmall ? 128 : 256; }
+
+// Parts that a contraction of `depth` is split into at most: of four stages
+// each at least.
+int max_parts(int64_t depth)
 {
-    const int64_t large = experts * ((m + 255) / 256) * ((n + 255) / 256);
-    // (and not where the last 256 columns of a few hold 128 at most)
-    const bool empty = n < 1024 && n % 256 >= 1 && n % 256 <= 128;
-    return m > 128 && large >= kCus / 2 && !empty ? kLarge : kSmall;
+    return (int)std::min<int64_t>(P::kMaxParts, depth / (4 * P::kTileK));
+}
+
+int stages_of(int64_t depth) { return (int)((depth + P::kTileK - 1) / P::kTileK); }
+
+// About how long (us) `experts` products of m x n outputs, `depth` deep, take
+// with tiles of one kind. A round of large tiles takes 13 us and 1.55 a stage,
+// one of as many small ones as the GPU holds (half their outputs) 7 and 1.1:
+// large tiles read the operands half as often, small ones leave less idle
+// where the last round is not full.
+double tiles_time(Kind k, int64_t m, int64_t n, int64_t experts, int64_t depth)
+{
+    const int side = side_of(k), round = kCus * P::tile_groups(side), stages = stages_of(depth);
+    const double start = k == kLarge ? 13.0 : 7.0, stage = k == kLarge ? 1.55 : 1.1;
+    const int64_t tiles = experts * ((m + side - 1) / side) * ((n + side - 1) / side);
+    const int left = (int)(tiles % round);
+    const int parts = P::parts_of(left, round, max_parts(depth), stages, side);
+    double t = (double)(tiles / round) * (start + stage * stages);
+    if (left > 0)
+        t += start + stage * stages / parts + (parts > 1 ? left * parts * stage / (k == kLarge ? 17 : 42) : 0.0);
+    return t;
+}
+
+// The faster kind by that. Measured (large, small), us: 8 experts of 4096
+// rows, 7168 -> 4096: 1474, 1811; 64 of 192, 4096 -> 2048: 277, 320; 8 of 256,
+// 7168 -> 4096 (128 large tiles): 149, 158; 8 of 768, 1024 -> 2048: 47, 58;
+// but 64 of 128, 4096 -> 2048: 256, 218; 8 of 512, 2048 -> 2048 (128 large
+// tiles): 58, 44; 16 of 500, 512 -> 640: 38, 21; weight gradients of 8
+// experts, 1536 x 2048, of 256 rows: 40, 32, of 1024: 78, 63, but of 4096:
+// 190, 194.
+Kind tiles_for(int64_t m, int64_t n, int64_t experts, int64_t depth)
+{
+    return tiles_time(kLarge, m, n, experts, depth) <= tiles_time(kSmall, m, n, experts, depth) ? kLarge
+                                                                                                : kSmall;
 }
 
 int64_t average_rows(const epl_product_desc &p)
@@ -95,29 +123,33 @@ Kind kind_of(const epl_product_desc &p)
     const int64_t avg = average_rows(p);
     if (p.weight_layout == EPL_WEIGHT_OUT_IN && avg <= kFewRows)
         return kFew;
-    return tiles_for(avg, p.out_cols, p.num_experts);
-}
-
-Kind grad_kind_of(const epl_product_desc &p) { return tiles_for(p.out_cols, p.in_cols, p.num_experts); }
-
-int side_of(Kind k) { return k == kSmall ? 128 : 256; }
-
-// Parts that a contraction of `depth` is worth being split into: at least
-// four stages each.
-int max_parts(int64_t depth)
-{
-    return (int)std::min<int64_t>(P::kMaxParts, depth / (4 * P::kTileK));
+    return tiles_for(avg, p.out_cols, p.num_experts, p.in_cols);
 }
 
 // The depth of a weight gradient's contraction is the expert's rows.
 int64_t grad_depth(const epl_product_desc &p) { return p.num_rows / p.num_experts; }
+
+Kind grad_kind_of(const epl_product_desc &p)
+{
+    return tiles_for(p.out_cols, p.in_cols, p.num_experts, grad_depth(p));
+}
+
+// A workspace: what tile_kernel tells join_kernel, then the partial tiles.
+constexpr size_t kHeaderBytes = 256;
 
 size_t tile_workspace(Kind k, int64_t tiles, int parts)
 {
     if (k == kFew || parts < 2)
         return 0;
     const int64_t slots = std::min<int64_t>(kCus * P::tile_groups(side_of(k)), tiles * parts);
-    return (size_t)slots * side_of(k) * side_of(k) * sizeof(float);
+    return kHeaderBytes + (size_t)slots * side_of(k) * side_of(k) * sizeof(float);
+}
+
+void use_workspace(P::Args &a, void *workspace)
+{
+    a.header = static_cast<int *>(workspace);
+    a.ws = workspace ? reinterpret_cast<P::f32x4 *>(static_cast<char *>(workspace) + kHeaderBytes)
+                     : nullptr;
 }
 
 int64_t product_tiles(const epl_product_desc &p, Kind k)
@@ -228,7 +260,8 @@ int epl_expert_product(const epl_product_desc *p, const uint16_t *x, const uint1
         return launch_status();
     }
     a.max_parts = max_parts(a.K);
-    a.ws = a.max_parts > 1 ? static_cast<P::f32x4 *>(workspace) : nullptr;
+    a.stages = stages_of(a.K);
+    use_workspace(a, a.max_parts > 1 ? workspace : nullptr);
     const int64_t tiles = product_tiles(*p, k);
     return p->weight_layout == EPL_WEIGHT_OUT_IN ? launch_kind<P::kForward>(k, a, tiles, s)
                                                  : launch_kind<P::kDataGrad>(k, a, tiles, s);
@@ -264,11 +297,13 @@ int epl_expert_weight_grad(const epl_product_desc *p, const uint16_t *grad, cons
     hipStream_t s = static_cast<hipStream_t>(stream);
     const Kind k = grad_kind_of(*p);
     const int64_t tiles = grad_tiles(*p, k);
-    // no tile is left over, or too many to share out: nothing to join
-    const int64_t round = num_cus() * P::tile_groups(side_of(k));
-    const bool even = tiles >= round && (tiles % round == 0 || tiles % round > round / 2);
     a.max_parts = max_parts(grad_depth(*p));
-    a.ws = a.max_parts > 1 && !even ? static_cast<P::f32x4 *>(workspace) : nullptr;
+    a.stages = stages_of(grad_depth(*p));
+    // (the number of tiles is known here: is any of them split?)
+    const int64_t round = std::min<int64_t>(num_cus() * P::tile_groups(side_of(k)), tiles * a.max_parts);
+    const bool join = a.max_parts > 1 &&
+                      P::parts_of((int)(tiles % round), (int)round, a.max_parts, a.stages, side_of(k)) > 1;
+    use_workspace(a, join ? workspace : nullptr);
     int rc = launch_kind<P::kWeightGrad>(k, a, tiles, s);
     if (rc == EPL_OK && grad_bias) {
         hipLaunchKernelGGL(P::bias_grad_kernel, dim3((unsigned)((a.N + 63) / 64), (unsigned)a.E),

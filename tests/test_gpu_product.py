@@ -223,7 +223,8 @@ def test_split_rows(counts, N, K, accumulate):
 
 @pytest.mark.parametrize("transposed", [False, True])
 @pytest.mark.parametrize("counts,K,act", [
-    ([300, 10, 260, 700, 257] * 4, 136, "silu"),       # 448 tiles of 256 x 256
+    ([300, 10, 260, 700, 257] * 4, 136, "silu"),
+    ([512, 400, 511, 512] * 4 + [500], 1032, "gelu"),  # 272 tiles of 256 x 256, 16 of them split
     ([100, 30, 128, 129, 0] * 8, 72, "swiglu"),        # 640 of 128 x 128
 ])
 def test_products_of_many_tiles(counts, K, act, transposed):
@@ -451,7 +452,8 @@ def test_weight_grad(N, K, out, accumulate):
 
 
 @pytest.mark.parametrize("counts,N,K", [
-    ([100, 40, 0, 130, 64], 2048, 4096),         # 640 tiles of 256 x 256
+    ([100, 40, 0, 130, 64], 2048, 4096),
+    ([100, 40, 0, 130], 2048, 4096),             # 512 tiles of 256 x 256
     ([20, 70] * 20, 384, 1024),                  # 960 of 128 x 128
 ])
 def test_weight_grad_of_many_tiles(counts, N, K):
