@@ -337,7 +337,7 @@ __device__ __forceinline__ void emit_weight(const Args &a, int64_t at, float (&v
 // Bound by the matrix instructions and the clock they leave: 8 x 4096 rows,
 // 7168 -> 4096, in 1.50 - 1.55 ms, 1.24 - 1.29 PFLOP/s (the same loop without
 // its loads takes 1.11 ms); with few rows an expert by the weights' bytes:
-// 64 x 192 rows, 4096 -> 2048, 290 us, 4.4 TB/s. Weight gradients: 29765
+// 64 x 192 rows, 4096 -> 2048, 285 - 293 us, 4.4 TB/s. Weight gradients: 29765
 // rows, 4096 x 7168, 1.35 - 1.40 ms (1.25 - 1.29 PFLOP/s); 64 x 192 rows,
 // 2048 x 4096 in binary32, 0.52 - 0.63 ms, by the 2.1 GB they write.
 
