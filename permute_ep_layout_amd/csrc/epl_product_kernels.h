@@ -869,8 +869,8 @@ __global__ __launch_bounds__(tile_threads(BN)) void join_kernel(Args a, int grid
     __shared__ int32_t sums[8];
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave / WN, wn = wave % WN;
-    if (a.header[0] == 0)          // (5 us to find that out from the counts, 2.5 so)
-        return;
+    if (a.header[0] == 0)          // (found from the counts: 16 experts of 500 rows, 512 ->
+        return;                    // 640, took 24 us rather than 22; 64 of 192 290, not 285)
     const int i = blockIdx.x;
     const int ntn = FORM == kWeightGrad ? (a.K + BN - 1) / BN : (a.N + BN - 1) / BN;
     const int ntm = FORM == kWeightGrad ? (a.N + BM - 1) / BM : 0;

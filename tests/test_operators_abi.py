@@ -137,18 +137,20 @@ def test_product_pointers(lib):
 
 
 def test_product_workspace_sizes(lib):
-    """Partial tiles: none for few rows or a short contraction, else at most
-    256 of 256 KB."""
+    """Partial tiles: none for few rows or a short contraction, else a header
+    and at most 256 of 256 KB."""
+    head = 256
     size = epl.epl_product_workspace_bytes
     assert size(product()) == 0 and size(product(in_cols=12)) == 0
     big = dict(num_rows=32768, in_cols=7168, out_cols=4096)
-    assert size(product(**big)) == 256 * 256 * 256 * 4
+    assert size(product(**big)) == head + 256 * 256 * 256 * 4
     assert size(product(expected_rows=8, **big)) == 0
-    assert size(product(num_rows=800, in_cols=512, out_cols=256)) == (800 // 128 + 8) * 2 * 128 * 1024
+    parts = (800 // 128 + 8) * 2 * 2
+    assert size(product(num_rows=800, in_cols=512, out_cols=256)) == head + parts * 64 * 1024
     grad = epl.epl_weight_grad_workspace_bytes
-    assert grad(product(**big)) == 256 * 256 * 256 * 4
+    assert grad(product(**big)) == head + 256 * 256 * 256 * 4
     assert grad(product(num_rows=800, in_cols=512, out_cols=256)) == 0
-    assert grad(product(num_rows=8 * 512, in_cols=64, out_cols=512)) == 8 * 2 * 2 * 128 * 1024
+    assert grad(product(num_rows=8 * 512, in_cols=64, out_cols=512)) == head + 8 * 2 * 2 * 128 * 1024
 
 
 def test_combine_backward_arguments(lib):
