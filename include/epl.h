@@ -371,8 +371,9 @@ int epl_router_validate(const epl_router *p);
  *   the sum of the choice's s with `renormalize` (0 where that sum is 0).
  * Equal scores go to the lower index (of group or expert). Without a bias
  * (and without sums of two over groups) the order is the exact order of the
- * logits; otherwise scores are binary64 and compare to 41 bits, and groups'
- * scores that agree to 2^-38 are equal.
+ * logits; otherwise experts' scores are binary64 and compare to 41 bits, and
+ * groups' scores, rounded to 40 bits each, compare exactly: topk_groups of
+ * them stay always.
  * An expert whose logit or bias is -inf or NaN is never chosen and has score
  * 0; a +inf logit or bias counts as the largest finite one; the lowest
  * finite logit is a candidate like any other. Where fewer than K candidates

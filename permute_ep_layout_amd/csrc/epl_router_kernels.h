@@ -297,6 +297,14 @@ __device__ __forceinline__ double group_score(const Args &a, double best, double
     return a.group_top == 2 && next > kNone ? best + next : best;
 }
 
+// A finite score to 40 significant bits, to nearest even: what binary64 and the
+// order of a sum leave uncertain of equal sums is far below.
+__device__ __forceinline__ double round40(double x)
+{
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    return __builtin_bit_cast(double, (u + 0xfff + ((u >> 13) & 1)) & ~(uint64_t)0x1fff);
+}
+
 // LDS operations of one wave are in order: this keeps the compiler's order.
 __device__ __forceinline__ void wave_lds() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local"); }
 
@@ -378,36 +386,57 @@ __device__ __forceinline__ void route_token(const Args &a, int64_t t, int lane, 
         s = lane_sum<64>(s);
         inv = s > 0.0 ? 1.0 / s : 0.0;
     }
+    const auto score_of = [&](int e, float bias) {
+        const float l = load_logit(a.logits, a.bf16, t * a.E + e);
+        return !a.need_scores ? exact_score<kLogits>(l, bias, m, inv)
+               : a.softmax    ? exact_score<kSoftmax>(l, bias, m, inv)
+                              : exact_score<kSigmoid>(l, bias, m, inv);
+    };
     for (int e = lane; e < a.E; e += 64) {
         const float l = load_logit(a.logits, a.bf16, t * a.E + e), b = a.bias ? a.bias[e] : 0.0f;
-        const double c = !a.need_scores ? exact_score<kLogits>(l, b, m, inv)
-                         : a.softmax    ? exact_score<kSoftmax>(l, b, m, inv)
-                                        : exact_score<kSigmoid>(l, b, m, inv);
-        key[e] = make_key(c, e, usable(l, b));
+        const double c = score_of(e, b);
+        // (groups are scored before the keys drop the scores' low bits)
+        key[e] = a.G == 1 ? make_key(c, e, usable(l, b)) : usable(l, b) ? c : 2.0 * kNone;
     }
     wave_lds();
     if (a.G > 1) {
-        const int size = a.E / a.G;
+        const int size = a.E / a.G, e0 = lane * size;
+        double own = 2.0 * kNone;
         if (lane < a.G) {
-            double x = 2.0 * kNone, y = 2.0 * kNone;
-            for (int i = 0; i < size; ++i)
-                two_best(x, y, key[lane * size + i], 2.0 * kNone);
-            score[lane] = group_score(a, x, y);
+            double x = own, y = own;
+            int ex = 0, ey = 0;
+            for (int i = 0; i < size; ++i) {
+                const double c = key[e0 + i];
+                if (c > x) {
+                    y = x, ey = ex;
+                    x = c, ex = e0 + i;
+                } else if (c > y) {
+                    y = c, ey = e0 + i;
+                }
+            }
+            own = x;
+            if (a.group_top == 2 && y > kNone) {
+                // scores and biases apart: two groups may hold the same ones
+                // paired otherwise, and these sums are equal then
+                const double bias = a.bias ? (double)no_inf(a.bias[ex]) + (double)no_inf(a.bias[ey]) : 0.0;
+                own = (score_of(ex, 0.0f) + score_of(ey, 0.0f)) + bias;
+            }
+            if (a.need_scores)
+                own = round40(own);
+            score[lane] = own;
         }
         wave_lds();
-        if (lane < a.G) {
-            // Sums of two that agree to 2^-38 are equal: the same scores and
-            // biases paired otherwise, whose sums differ by rounding and by
-            // the index bits of their keys.
-            const double own = score[lane];
-            const double near = a.need_scores && own > kNone ? 0x1p-38 * fabs(own) : 0.0;
-            int before = 0;
-            for (int o = 0; o < a.G; ++o)
-                before += score[o] > own + near || (score[o] >= own - near && o < lane) ? 1 : 0;
-            if (before >= a.topk_groups)
-                for (int i = 0; i < size; ++i)
-                    key[lane * size + i] = 2.0 * kNone;
-        }
+        // a total order, so that topk_groups of them stay whatever lies close
+        int before = 0;
+        for (int o = 0; o < a.G; ++o)
+            before += score[o] > own || (score[o] == own && o < lane) ? 1 : 0;
+        wave_lds();
+        if (lane < a.G && before >= a.topk_groups)
+            for (int i = 0; i < size; ++i)
+                key[e0 + i] = 2.0 * kNone;
+        wave_lds();
+        for (int e = lane; e < a.E; e += 64)
+            key[e] = make_key(key[e], e, key[e] > kNone);
         wave_lds();
     }
     const bool live = !a.mask || a.mask[t] != 0;

@@ -1,0 +1,77 @@
+"""The router and its gradient on the GPU where scores, biases or logits lie at
+the limits of their types, against their definitions in 64 bits."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import permute_ep_layout_amd as epl  # noqa: E402
+
+import redzones  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+DEV = torch.device("cuda:0")
+U = 2.0 ** -24                     # half a step of binary32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    epl.load()
+
+
+@pytest.fixture(autouse=True)
+def _red_zones():
+    yield
+    redzones.check()
+
+
+def sigmoid(x):
+    return 1.0 / (1.0 + np.exp(-np.asarray(x, dtype=np.float64)))
+
+
+def group_scores(s, G):
+    """Sums of two of [T, E] sigmoids, to 40 bits, and whether a rounding of
+    the sum in 64 bits (some 2^-52 of it) cannot change that."""
+    sums = np.sort(s.reshape(len(s), G, -1), axis=2)[:, :, -2:].sum(2)
+    part, power = np.frexp(sums)
+    scaled = part * 2.0 ** 40
+    clear = np.abs(scaled - np.floor(scaled) - 0.5) > 2.0 ** -8
+    return np.ldexp(np.round(scaled) * 2.0 ** -40, power), clear.all(1)
+
+
+@pytest.mark.parametrize("E,G,TG,K", [
+    (64, 8, 1, 8), (64, 8, 4, 8), (128, 8, 4, 8), (32, 8, 3, 4), (64, 8, 4, 32), (256, 8, 3, 48),
+    (60, 12, 5, 25)])
+@pytest.mark.parametrize("T", [300, 4500])
+def test_saturated_groups(T, E, G, TG, K):
+    """Sigmoids next to 1, whose sums over groups lie close together: exactly
+    TG groups stay, those of the largest sums, ties to the lower one."""
+    x = torch.empty(T, E).uniform_(24, 28, generator=torch.Generator().manual_seed(E + TG))
+    idx, _ = epl.route(x.to(DEV), K, score="sigmoid", num_groups=G, topk_groups=TG, group_top=2,
+                       renormalize=True)
+    idx = idx.cpu().numpy()
+    assert (idx >= 0).all()
+    assert (np.diff(np.sort(idx, axis=1), axis=1) > 0).all()
+    size = E // G
+    scores, clear = group_scores(sigmoid(x.numpy()), G)
+    assert clear.mean() > 0.8
+    stay = np.sort(np.argsort(-scores, axis=1, kind="stable")[:, :TG], axis=1)
+    for t in np.flatnonzero(clear):
+        assert np.isin(idx[t] // size, stay[t]).all(), t
+        if K == TG * size:
+            np.testing.assert_array_equal(np.unique(idx[t] // size), stay[t])
+
+
+@pytest.mark.parametrize("T", [1, 5000])
+def test_a_chain_of_near_groups(T):
+    """Each group's score within 2^-38 of the next one's, the ends further apart."""
+    x = torch.tensor([25.55, 26.02, 26.94]).repeat_interleave(8).repeat(T, 1)
+    for order, best in (([0, 1, 2], 2), ([2, 1, 0], 0), ([1, 2, 0], 1)):
+        v = x.view(T, 3, 8)[:, order].reshape(T, 24).contiguous().to(DEV)
+        idx, w = epl.route(v, 8, score="sigmoid", num_groups=3, topk_groups=1, group_top=2,
+                           renormalize=True)
+        assert torch.equal(idx.cpu(), torch.arange(best * 8, best * 8 + 8).expand(T, 8))
+        assert ((w - 0.125).abs() <= 2 * U * 0.125).all()
