@@ -860,6 +860,25 @@ def prepare(name: str, *args, stream=None):
 
 # ------------------------------------------------------- tensor helpers --
 
+def _run_on(stream, device, call, *args):
+    """call(*args) with `stream` as torch's current stream: what it allocates,
+    fills and launches is in that stream's order (memory taken from another
+    stream's pool may still be in use there, and a fill on another stream is
+    ordered with nothing). Its outputs are kept for the caller's stream too:
+    they may be used and dropped there once it has waited for `stream`."""
+    torch = _torch()
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    caller = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        out = call(*args)
+    if stream.cuda_stream != caller.cuda_stream:
+        for t in out if isinstance(out, tuple) else (out,):
+            if isinstance(t, torch.Tensor) and t.is_cuda:
+                t.record_stream(caller)
+    return out
+
+
 class DispatchResult(NamedTuple):
     out: "torch.Tensor"                  # [capacity, H] bf16 (rows >= total unwritten)
     out_scale: Optional["torch.Tensor"]  # [capacity, S] f32 or None
@@ -1143,5 +1162,8 @@ def dispatch_backward(grad_rows, output_index, out_dtype=None, workspace=None, s
     grad_rows, i.e. `combine` with unit weights."""
     torch = _torch()
     _matrix(output_index, "output_index", 2)
+    if stream is not None and output_index.is_cuda:
+        return _run_on(stream, output_index.device, dispatch_backward, grad_rows, output_index,
+                       out_dtype, workspace)
     ones = torch.ones(output_index.shape, dtype=torch.float32, device=output_index.device)
     return combine(grad_rows, output_index, ones, out_dtype, workspace, stream)
