@@ -9,6 +9,8 @@ PyTorch fallback, and using the package without the built library raises.
 
 ``dispatch`` and ``combine`` are tensor-level conveniences on top of them:
 they allocate outputs with ``torch.empty`` and call the same entry points.
+With ``stream=`` they run as under ``with torch.cuda.stream(stream)``: memory
+is taken from that stream's pool.
 """
 from __future__ import annotations
 
@@ -921,6 +923,9 @@ def dispatch(x, topk_idx, num_experts: int, num_ranks: int, x_scale=None,
     experts) with num_experts = the local expert count and num_ranks = 1.
     """
     torch = _torch()
+    if stream is not None and x.is_cuda:
+        return _run_on(stream, x.device, dispatch, x, topk_idx, num_experts, num_ranks, x_scale,
+                       capacity, mode, workspace, None, expert_alignment, ranks_per_node)
     T, H = x.shape
     K = topk_idx.shape[1]
     S = 0 if x_scale is None else x_scale.shape[1]
@@ -942,16 +947,16 @@ def dispatch(x, topk_idx, num_experts: int, num_ranks: int, x_scale=None,
         out_scale = torch.empty((cap, S), dtype=torch.float32, device=dev) if S else None
         m_idx = torch.empty(cap, dtype=i32, device=dev)
         epl_dispatch(p, topk_idx, x, x_scale, cap, cnt, per_rank, per_node, in_rank, start,
-                     total_host, out, out_scale, m_idx, oi, ws, stream)
+                     total_host, out, out_scale, m_idx, oi, ws)
     elif mode == "exact":
-        epl_layout(p, topk_idx, cnt, per_rank, per_node, in_rank, ws, stream)
-        epl_scan(p, cnt, start, total_host, ws, stream)
-        torch.cuda.current_stream(dev).synchronize() if stream is None else stream.synchronize()
+        epl_layout(p, topk_idx, cnt, per_rank, per_node, in_rank, ws)
+        epl_scan(p, cnt, start, total_host, ws)
+        torch.cuda.current_stream(dev).synchronize()
         cap = int(total_host[0])
         out = torch.empty((cap, H), dtype=torch.bfloat16, device=dev)
         out_scale = torch.empty((cap, S), dtype=torch.float32, device=dev) if S else None
         m_idx = torch.empty(cap, dtype=i32, device=dev)
-        epl_scatter(p, x, x_scale, topk_idx, start, ws, cap, out, out_scale, m_idx, oi, stream)
+        epl_scatter(p, x, x_scale, topk_idx, start, ws, cap, out, out_scale, m_idx, oi)
     else:
         raise ValueError(f"unknown mode {mode!r}")
     return DispatchResult(out, out_scale, m_idx, oi, start, cnt, per_rank, per_node, in_rank,
@@ -962,13 +967,16 @@ def combine(expert_out, output_index, topk_weights, out_dtype=None, workspace=No
             stream=None):
     """y[t] = sum_k w[t,k] * expert_out[output_index[t,k]] (fp32 accumulation)."""
     torch = _torch()
+    if stream is not None and expert_out.is_cuda:
+        return _run_on(stream, expert_out.device, combine, expert_out, output_index, topk_weights,
+                       out_dtype, workspace)
     out_dtype = torch.float32 if out_dtype is None else out_dtype
     T, K = output_index.shape
     rows, H = expert_out.shape
     p = Problem.make(T, K, 1, 1, H, 0)
     code = EPL_OUT_BF16 if out_dtype == torch.bfloat16 else EPL_OUT_F32
     y = torch.empty((T, H), dtype=out_dtype, device=expert_out.device)
-    epl_combine(p, expert_out, rows, output_index, topk_weights, code, y, workspace, stream)
+    epl_combine(p, expert_out, rows, output_index, topk_weights, code, y, workspace)
     return y
 
 
@@ -976,9 +984,10 @@ def expert_scale(res: DispatchResult, rows_in=None, stream=None):
     """The large-batch workload's synthetic expert applied to a dispatch result."""
     torch = _torch()
     rows_in = res.out if rows_in is None else rows_in
+    if stream is not None and rows_in.is_cuda:
+        return _run_on(stream, rows_in.device, expert_scale, res, rows_in)
     out = torch.empty_like(rows_in)
-    epl_expert_scale(res.problem, rows_in, res.m_indices, rows_in.shape[0], out, res.workspace,
-                     stream)
+    epl_expert_scale(res.problem, rows_in, res.m_indices, rows_in.shape[0], out, res.workspace)
     return out
 
 
@@ -1005,18 +1014,12 @@ def _product_for(*fields):
     return p, epl_product_workspace_bytes(p)
 
 
-def _split_ws(nbytes, device, stream):
-    """A product's workspace, from torch's allocator (kept for `stream` when
-    that is not torch's current one)."""
+def _split_ws(nbytes, device):
+    """A product's workspace, from torch's allocator."""
     if nbytes == 0:
         return None
     torch = _torch()
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    if stream is not None:
-        if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream, device=device)
-        ws.record_stream(stream)
-    return ws
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
 _SCORES = {"softmax": EPL_SCORE_SOFTMAX, "sigmoid": EPL_SCORE_SIGMOID}
@@ -1048,6 +1051,9 @@ def route(logits, num_topk: int, score: str = "softmax", bias=None, num_groups: 
     padding) gives a token no selection at all."""
     torch = _torch()
     _matrix(logits, "logits", 2)
+    if stream is not None and logits.is_cuda:
+        return _run_on(stream, logits.device, route, logits, num_topk, score, bias, num_groups,
+                       topk_groups, group_top, renormalize, scale, token_mask)
     T, E = logits.shape
     K = int(num_topk)
     p = _router_for(T, K, E, _named(_SCORES, score, "score"), int(num_groups), int(topk_groups),
@@ -1056,7 +1062,7 @@ def route(logits, num_topk: int, score: str = "softmax", bias=None, num_groups: 
     dev = logits.device
     idx = torch.empty(T, K, dtype=torch.int64, device=dev)       # (a tuple takes 0.7 us more)
     w = torch.empty(T, K, dtype=torch.float32, device=dev)
-    _route(p, logits, bias, token_mask, idx, w, stream)
+    _route(p, logits, bias, token_mask, idx, w, None)
     return idx, w
 
 
@@ -1067,11 +1073,14 @@ def route_backward(logits, topk_idx, grad_weights, score: str = "softmax",
     torch = _torch()
     _matrix(logits, "logits", 2)
     _matrix(topk_idx, "topk_idx", 2)
+    if stream is not None and logits.is_cuda:
+        return _run_on(stream, logits.device, route_backward, logits, topk_idx, grad_weights, score,
+                       renormalize, scale)
     T, E = logits.shape
     p = _router_for(T, topk_idx.shape[1], E, _named(_SCORES, score, "score"), 1, 1, 1,
                     int(bool(renormalize)), _type_code(logits.dtype, "logits"), float(scale))
     grad = torch.empty_like(logits)
-    epl_route_backward(p, logits, topk_idx, grad_weights, grad, stream)
+    epl_route_backward(p, logits, topk_idx, grad_weights, grad)
     return grad
 
 
@@ -1089,6 +1098,10 @@ def expert_product(x, weight, expert_start_loc, num_tokens_per_expert, bias=None
     torch = _torch()
     _matrix(x, "x", 2)
     _matrix(weight, "weight", 3)
+    if stream is not None and x.is_cuda:
+        return _run_on(stream, x.device, expert_product, x, weight, expert_start_loc,
+                       num_tokens_per_expert, bias, activation, residual, pre, out, out_dtype,
+                       transposed, expected_rows, workspace)
     E = weight.shape[0]
     N = weight.shape[2] if transposed else weight.shape[1]
     act = _named(_ACTIVATIONS, activation, "activation")
@@ -1105,9 +1118,9 @@ def expert_product(x, weight, expert_start_loc, num_tokens_per_expert, bias=None
         cols = N // 2 if act == EPL_ACT_SWIGLU else 2 * N if act == EPL_ACT_SWIGLU_GRAD else N
         out = torch.empty((x.shape[0], cols), dtype=out_dtype, device=x.device)
     if workspace is None and x.is_cuda:
-        workspace = _split_ws(ws_bytes, x.device, stream)
+        workspace = _split_ws(ws_bytes, x.device)
     epl_expert_product(p, x, weight, bias, residual, expert_start_loc, num_tokens_per_expert, pre,
-                       out, workspace, stream)
+                       out, workspace)
     return out
 
 
@@ -1121,6 +1134,9 @@ def expert_weight_grad(grad, x, expert_start_loc, num_tokens_per_expert, out=Non
     _matrix(grad, "grad", 2)
     _matrix(x, "x", 2)
     _matrix(expert_start_loc, "expert_start_loc", 1)
+    if stream is not None and x.is_cuda:
+        return _run_on(stream, x.device, expert_weight_grad, grad, x, expert_start_loc,
+                       num_tokens_per_expert, out, out_dtype, bias_grad, accumulate, workspace)
     E, N, K = expert_start_loc.shape[0], grad.shape[1], x.shape[1]
     if out is None:
         if accumulate:
@@ -1132,9 +1148,9 @@ def expert_weight_grad(grad, x, expert_start_loc, num_tokens_per_expert, out=Non
     p, _ = _product_for(grad.shape[0], 0, E, K, N, EPL_WEIGHT_OUT_IN, EPL_ACT_NONE,
                         _type_code(out.dtype, "out"))
     if workspace is None and x.is_cuda:
-        workspace = _split_ws(epl_weight_grad_workspace_bytes(p), x.device, stream)
+        workspace = _split_ws(epl_weight_grad_workspace_bytes(p), x.device)
     epl_expert_weight_grad(p, grad, x, expert_start_loc, num_tokens_per_expert, accumulate, out,
-                           bias_grad, workspace, stream)
+                           bias_grad, workspace)
     return out
 
 
@@ -1146,6 +1162,9 @@ def combine_backward(grad_y, expert_out, output_index, topk_weights, grad_rows=N
     torch = _torch()
     _matrix(output_index, "output_index", 2)
     _matrix(expert_out, "expert_out", 2)
+    if stream is not None and expert_out.is_cuda:
+        return _run_on(stream, expert_out.device, combine_backward, grad_y, expert_out,
+                       output_index, topk_weights, grad_rows, workspace)
     T, K = output_index.shape
     rows, H = expert_out.shape
     p = _combine_problem(T, K, H)
@@ -1153,7 +1172,7 @@ def combine_backward(grad_y, expert_out, output_index, topk_weights, grad_rows=N
         grad_rows = torch.empty_like(expert_out)
     grad_weights = torch.empty(T, K, dtype=torch.float32, device=expert_out.device)
     epl_combine_backward(p, grad_y, expert_out, rows, output_index, topk_weights, grad_rows,
-                         grad_weights, workspace, stream)
+                         grad_weights, workspace)
     return grad_rows, grad_weights
 
 
@@ -1166,4 +1185,4 @@ def dispatch_backward(grad_rows, output_index, out_dtype=None, workspace=None, s
         return _run_on(stream, output_index.device, dispatch_backward, grad_rows, output_index,
                        out_dtype, workspace)
     ones = torch.ones(output_index.shape, dtype=torch.float32, device=output_index.device)
-    return combine(grad_rows, output_index, ones, out_dtype, workspace, stream)
+    return combine(grad_rows, output_index, ones, out_dtype, workspace)

@@ -115,7 +115,33 @@ def gpu(*shape, dtype=torch.float32):
 T, K, E, H, F, ROWS = 6, 2, 4, 128, 32, 2048
 BF16, I32 = torch.bfloat16, torch.int32
 
+
+def _result():
+    return epl.DispatchResult(gpu(ROWS, H, dtype=BF16), None, gpu(ROWS, dtype=I32), None, None, None,
+                              None, None, None, None, gpu(1 << 20, dtype=torch.uint8),
+                              epl.Problem.make(T, K, E, 2, H))
+
+
+# sizes whose products split their contraction, so that they take a workspace
+DEEP = 4096
+
 CALLS = {
+    "dispatch": lambda **kw: epl.dispatch(
+        gpu(T, H, dtype=BF16), gpu(T, K, dtype=torch.int64), E, 2, **kw),
+    "combine": lambda **kw: epl.combine(
+        gpu(ROWS, H, dtype=BF16), gpu(T, K, dtype=I32), gpu(T, K), **kw),
+    "expert_scale": lambda **kw: epl.expert_scale(_result(), **kw),
+    "route": lambda **kw: epl.route(gpu(T, E), K, **kw),
+    "route_backward": lambda **kw: epl.route_backward(
+        gpu(T, E), gpu(T, K, dtype=torch.int64), gpu(T, K), **kw),
+    "expert_product": lambda **kw: epl.expert_product(
+        gpu(ROWS, DEEP, dtype=BF16), gpu(E, F, DEEP, dtype=BF16), gpu(E, dtype=I32),
+        gpu(E, dtype=I32), **kw),
+    "expert_weight_grad": lambda **kw: epl.expert_weight_grad(
+        gpu(ROWS, F, dtype=BF16), gpu(ROWS, H, dtype=BF16), gpu(E, dtype=I32), gpu(E, dtype=I32),
+        **kw),
+    "combine_backward": lambda **kw: epl.combine_backward(
+        gpu(T, H), gpu(ROWS, H, dtype=BF16), gpu(T, K, dtype=I32), gpu(T, K), **kw),
     "dispatch_backward": lambda **kw: epl.dispatch_backward(
         gpu(ROWS, H, dtype=BF16), gpu(T, K, dtype=I32), **kw),
 }
@@ -138,5 +164,13 @@ def test_what_a_call_makes_belongs_to_its_stream(streams, name, raw):
 def test_without_a_stream_the_current_one(streams, name):
     with streams.stream(Stream(0x55)):
         CALLS[name]()
-    assert all(s == 0x55 for _, s in streams.launches)
+    assert streams.made and all(s == 0x55 for _, s in streams.launches)
     assert all(t.owner.cuda_stream == 0x55 for t in streams.made)
+
+
+def test_products_here_take_a_workspace(streams):
+    """(else the calls above would not show where it comes from)"""
+    for name in ("expert_product", "expert_weight_grad"):
+        CALLS[name]()
+        assert any(t.dtype == torch.uint8 for t in streams.made)
+        streams.made.clear()
