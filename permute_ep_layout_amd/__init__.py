@@ -618,9 +618,8 @@ def epl_combine(p: Problem, expert_out, expert_rows, output_index, topk_weights,
     _need_ws_arg(workspace, dev, allow_none=True)
     if workspace is not None:
         _need_workspace(workspace, WS_HEADER_BYTES, "epl_combine")
-    _check(load().epl_combine(_prob(p), _ptr(expert_out), int(expert_rows), _ptr(output_index),
-                              _ptr(topk_weights), int(out_dtype), _ptr(y), _ptr(workspace),
-                              _stream(stream, dev)), "epl_combine")
+    _launch("epl_combine", dev, stream, _prob(p), _ptr(expert_out), int(expert_rows),
+            _ptr(output_index), _ptr(topk_weights), int(out_dtype), _ptr(y), _ptr(workspace))
 
 
 def epl_expert_scale(p: Problem, rows_in, m_indices, capacity_rows, rows_out, workspace,

@@ -174,3 +174,34 @@ def test_products_here_take_a_workspace(streams):
         CALLS[name]()
         assert any(t.dtype == torch.uint8 for t in streams.made)
         streams.made.clear()
+
+
+class OnSecond(OnGpu):
+    device = property(lambda t: torch.device("cuda:1"))
+
+
+def test_dispatch_backward_off_the_current_gpu(streams, monkeypatch):
+    """Kernels are launched on the current GPU: the tensors' has to be it."""
+    at = [0]
+
+    @contextlib.contextmanager
+    def device(index):
+        before, at[0] = at[0], index
+        yield
+        at[0] = before
+
+    where = []
+    inner = streams.entry
+
+    def entry(name):
+        call = inner(name)
+        return lambda *args: (where.append((name, at[0])), call(*args))[1]
+
+    monkeypatch.setattr(streams, "device", device, raising=False)
+    monkeypatch.setattr(streams, "current_device", lambda: at[0])
+    monkeypatch.setattr(streams, "entry", entry)
+    monkeypatch.setattr(streams, "_make", lambda make, *args, device=None, **kw:
+                        make(*args, **kw).as_subclass(OnSecond))
+    epl.dispatch_backward(torch.zeros(ROWS, H, dtype=BF16).as_subclass(OnSecond),
+                          torch.zeros(T, K, dtype=I32).as_subclass(OnSecond))
+    assert ("epl_combine", 1) in where and at[0] == 0, where
