@@ -706,17 +706,31 @@ __global__ __launch_bounds__(kThreads) void route_grad_kernel(GradArgs a)
         inv = s > 0.0f ? 1.0f / s : 0.0f;
     }
 
-    // the slots' logits, for the maximum of the chosen
+    // The chosen logits' maximum, from which the scores of a renormalised
+    // choice are taken: only their ratios matter, and scores that all leave
+    // binary32 (sigmoids of logits below -87) have some too.
     float top = -INFINITY;
-    if (a.softmax && a.renorm) {
+    const float floor = a.softmax ? -INFINITY : -700.0f;       // scores below it are 0 (sigmoid64)
+    const auto scored = [&](float l) { return l > -INFINITY && l >= floor; };
+    if (a.renorm) {
         for (int k = lane; k < a.K; k += L) {
             const int64_t e = a.idx[row * a.K + k];
-            if (e >= 0 && e < a.E)
-                top = fmaxf(top, usable(load_logit(a.logits, a.bf16, row * a.E + e)));
+            if (e >= 0 && e < a.E) {
+                const float l = load_logit(a.logits, a.bf16, row * a.E + e);
+                top = fmaxf(top, scored(l) ? l : -INFINITY);
+            }
         }
         top = lane_max<L>(top);
         top = top > -INFINITY ? top : 0.0f;
     }
+    // The score of a chosen logit; of a renormalised choice over that of
+    // `top` (a sigmoid's: over exp(top) where that is below 1). A sigmoid is
+    // exp(min(l, 0)) / (1 + exp(-|l|)).
+    const float from = !a.renorm ? 0.0f : a.softmax ? top : fminf(top, 0.0f);
+    const auto share = [&](float l) {
+        return a.softmax ? __expf(l - from)
+                         : __expf(fminf(l, 0.0f) - from) / (1.0f + __expf(-fabsf(l)));
+    };
     float sum = 0.0f, dot = 0.0f;
     for (int k = lane; k < a.K; k += L) {
         const int64_t e = a.idx[row * a.K + k];
@@ -724,8 +738,8 @@ __global__ __launch_bounds__(kThreads) void route_grad_kernel(GradArgs a)
         const float l = live ? load_logit(a.logits, a.bf16, row * a.E + e) : -INFINITY;
         const float g = live ? a.g[row * a.K + k] * a.scale : 0.0f;
         float s = 0.0f;
-        if (l > -INFINITY)
-            s = !a.softmax ? 1.0f / (1.0f + __expf(-l)) : dense ? __expf(l - m) * inv : __expf(l - top);
+        if (scored(l))
+            s = dense ? __expf(l - m) * inv : share(l);
         who[slot][k] = live ? (int)e : -1;
         val[slot][k] = g;
         sum += s;
@@ -739,15 +753,12 @@ __global__ __launch_bounds__(kThreads) void route_grad_kernel(GradArgs a)
         const int e = who[slot][k];
         const float l = e >= 0 ? load_logit(a.logits, a.bf16, row * a.E + e) : -INFINITY;
         float d = 0.0f;
-        if (l > -INFINITY) {
-            const float h = (val[slot][k] - mean) * over;
-            if (dense) {
-                d = h;
-            } else if (a.softmax) {
-                d = h * __expf(l - top);
-            } else {
-                const float s = 1.0f / (1.0f + __expf(-l));
-                d = h * s / (1.0f + __expf(l));             // 1 - s without cancellation
+        if (scored(l)) {
+            d = val[slot][k] - mean;
+            if (!dense) {
+                d *= share(l) * over;
+                if (!a.softmax)
+                    d /= 1.0f + __expf(l);                  // 1 - s without cancellation
             }
         }
         val[slot][k] = d;

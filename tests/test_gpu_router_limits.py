@@ -8,6 +8,7 @@ torch = pytest.importorskip("torch")
 import permute_ep_layout_amd as epl  # noqa: E402
 
 import redzones  # noqa: E402
+import test_gpu_router as router  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -75,3 +76,33 @@ def test_a_chain_of_near_groups(T):
                            renormalize=True)
         assert torch.equal(idx.cpu(), torch.arange(best * 8, best * 8 + 8).expand(T, 8))
         assert ((w - 0.125).abs() <= 2 * U * 0.125).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("K", [1, 2, 8])
+@pytest.mark.parametrize("base", [-87.0, -100.0, -300.0, -600.0, 0.0, 60.0])
+def test_gradient_of_far_sigmoids(base, K, dtype):
+    """Chosen logits far below zero: their sigmoids leave binary32, the ratios
+    of renormalised ones do not. The chosen lie within 30 of each other, so the
+    exponentials' (2 |x| + 4) u of them and of their sum stay below the 184 u
+    that check_grad allows at these sizes."""
+    E, T = 64, 200
+    g = torch.Generator().manual_seed(K)
+    x = (base + 30 * torch.rand(T, E, generator=g) - 15).to(dtype)
+    idx, grad = router.choice_of(T, E, K, seed=K)
+    router.check_grad(x, idx, grad * 20, "sigmoid", True, 2.5)
+    assert not (router.grad_reference(x.float().numpy(), idx.numpy(), grad.numpy() * 20, "sigmoid",
+                                      True, 2.5)[0] == 0).all() or base == 60 or K == 1
+
+
+def test_sigmoids_that_are_zero():
+    """Below -700 a sigmoid counts as 0: so do weights of nothing else, and
+    their gradients."""
+    x = torch.full((3, 64), -2000.0)
+    x[1] = torch.finfo(torch.float32).min
+    x[2, 5] = -690.0
+    idx, w = epl.route(x.to(DEV), 4, score="sigmoid", renormalize=True)
+    assert (w[:2] == 0).all() and w[2].tolist() == [1, 0, 0, 0] and idx[2, 0] == 5
+    g = torch.randn(3, 4, generator=torch.Generator().manual_seed(0)).to(DEV)
+    dx = epl.route_backward(x.to(DEV), idx, g, score="sigmoid", renormalize=True)
+    assert (dx[:2] == 0).all() and (dx[2].abs() <= 4 * U * g[2, 0].abs()).all()
