@@ -291,10 +291,24 @@ __device__ __forceinline__ void two_best(double &a, double &b, double c, double 
     b = fmax(lo, fmax(b, d));
 }
 
-// Group score from its two best keys: a group of one candidate has that one.
-__device__ __forceinline__ double group_score(const Args &a, double best, double next)
+// A group's score from its two best keys (a group of one candidate has that
+// one, a group of none -infinity), and how far another's must lie from it.
+struct GroupScore {
+    float score, near;
+};
+
+// The error of a sum follows its terms, not the sum: biases may cancel in it.
+// Both are halved where scores add, so that no sum leaves binary32; the
+// rounding of the sum fits into the margins, which are twice the errors.
+template <Order ORDER>
+__device__ __forceinline__ double group_score(const Args &a, double best, double next, double top)
 {
-    return a.group_top == 2 && next > kNone ? best + next : best;
+    const bool two = a.group_top == 2 && next > kNone;
+    const double half = ORDER == kLogits ? 1.0 : 0.5;
+    const double sum = two ? best + next : best;
+    const double near = margin<ORDER>(best, top) + (two ? margin<ORDER>(next, top) : 0.0);
+    const GroupScore g{(float)(half * sum), best > kNone ? (float)(half * near) : 0.0f};
+    return __builtin_bit_cast(double, g);
 }
 
 // A finite score to 40 significant bits, to nearest even: what binary64 and the
@@ -478,8 +492,8 @@ __global__ __launch_bounds__(64) void route_any_kernel(Args a)
 // instructions a wave of 8 tokens, which issue in 84% of its cycles.
 
 // The token's 8 best keys in every lane; false, on one of its lanes at least,
-// where the error of binary32 leaves their order in doubt. `groups` and
-// `gone`: the token's LDS, of kMaxGroups each.
+// where the error of binary32 leaves their order in doubt. `groups` (of
+// GroupScore) and `gone`: the token's LDS, of kMaxGroups each.
 template <int L, int CH, Order ORDER>
 __device__ __forceinline__ bool choose(const Args &a, const float (&l)[CH][8], int lane, float m,
                                        float inv, double *groups, int *gone, double (&best)[8])
@@ -527,22 +541,22 @@ __device__ __forceinline__ bool choose(const Args &a, const float (&l)[CH][8], i
                 if (per > 32) { two_best(x, y, lane_swap<32>(x), lane_swap<32>(y)); }
             const int piece = c * L + lane;
             if ((piece & (per - 1)) == 0 && piece >> a.per_log < a.G)
-                groups[piece >> a.per_log] = group_score(a, x, y);
+                groups[piece >> a.per_log] = group_score<ORDER>(a, x, y, top);
         }
         wave_lds();
         for (int g = lane; g < a.G; g += L) {
-            const double own = groups[g], near = 2.0 * margin<ORDER>(own, top);
+            const auto [own, near] = __builtin_bit_cast(GroupScore, groups[g]);
             int before = 0, close = 0;
             for (int o = 0; o < a.G; ++o) {
-                const double s = groups[o];
+                const auto [s, far] = __builtin_bit_cast(GroupScore, groups[o]);
                 before += (int)(s > own) | ((int)(s == own) & (int)(o < g));
                 if (ORDER != kLogits)
-                    close += (int)(fabs(s - own) <= near);
+                    close += (int)(fabsf(s - own) <= fmaxf(near, far));
             }
             gone[g] = before >= a.topk_groups;
             // the last group that stays must stand clear of the others
             if (ORDER != kLogits)
-                sure &= !(before == a.topk_groups - 1 && close > 1 && own > kNone);
+                sure &= !(before == a.topk_groups - 1 && close > 1 && own > -INFINITY);
         }
         wave_lds();
 #pragma unroll

@@ -78,6 +78,37 @@ def test_a_chain_of_near_groups(T):
         assert ((w - 0.125).abs() <= 2 * U * 0.125).all()
 
 
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E", [64, 256])
+@pytest.mark.parametrize("B", [16.0, 50.0, 200.0, 1000.0])
+def test_groups_of_cancelling_biases(B, E, score):
+    """A group's two best lie B above and B below the rest: their scores round
+    by steps of B in binary32, which their small sum does not show."""
+    T, G = 4500, 8
+    g = torch.Generator().manual_seed(int(B) + E)
+    x = torch.full((T, G, E // G), -float("inf"))
+    x[:, :, :2] = torch.randn(T, 1, 1, generator=g) + 3e-5 * torch.randn(T, G, 2, generator=g)
+    b = torch.zeros(G, E // G)
+    b[:, 0], b[:, 1] = B, -B
+    idx, _ = epl.route(x.view(T, E).to(DEV), 2, score=score, bias=b.view(E).to(DEV), num_groups=G,
+                       topk_groups=1, group_top=2)
+    s = x[:, :, :2].double()
+    p = torch.sigmoid(s) if score == "sigmoid" else torch.softmax(s.view(T, -1), 1).view(T, G, 2)
+    at = p.sum(2).argmax(1) * (E // G)
+    assert torch.equal(idx.cpu(), torch.stack([at, at + 1], 1))
+
+
+def test_groups_of_the_smallest_logits():
+    """Denormal logits one step apart order the groups, empty groups last."""
+    step = 2.0 ** -149
+    x = torch.full((4, 64), -float("inf"))
+    x[0, ::8] = step * torch.tensor([3.0, 1, 2, 4, 0, 5, 7, 6])
+    x[1, ::8] = step * torch.tensor([-3.0, -1, -2, -4, 0, -5, -7, -6])
+    x[2, 8:16] = -step
+    idx, _ = epl.route(x.to(DEV), 2, score="sigmoid", num_groups=8, topk_groups=2, renormalize=True)
+    assert idx.tolist() == [[48, 56], [32, 8], [8, 9], [-1, -1]]
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("K", [1, 2, 8])
 @pytest.mark.parametrize("base", [-87.0, -100.0, -300.0, -600.0, 0.0, 60.0])
