@@ -400,57 +400,70 @@ __device__ __forceinline__ void route_token(const Args &a, int64_t t, int lane, 
         s = lane_sum<64>(s);
         inv = s > 0.0 ? 1.0 / s : 0.0;
     }
-    const auto score_of = [&](int e, float bias) {
-        const float l = load_logit(a.logits, a.bf16, t * a.E + e);
+    const auto score_of = [&](float l, float bias) {
         return !a.need_scores ? exact_score<kLogits>(l, bias, m, inv)
                : a.softmax    ? exact_score<kSoftmax>(l, bias, m, inv)
                               : exact_score<kSigmoid>(l, bias, m, inv);
     };
-    for (int e = lane; e < a.E; e += 64) {
-        const float l = load_logit(a.logits, a.bf16, t * a.E + e), b = a.bias ? a.bias[e] : 0.0f;
-        const double c = score_of(e, b);
-        // (groups are scored before the keys drop the scores' low bits)
-        key[e] = a.G == 1 ? make_key(c, e, usable(l, b)) : usable(l, b) ? c : 2.0 * kNone;
-    }
-    wave_lds();
-    if (a.G > 1) {
-        const int size = a.E / a.G, e0 = lane * size;
-        double own = 2.0 * kNone;
-        if (lane < a.G) {
-            double x = own, y = own;
-            int ex = 0, ey = 0;
-            for (int i = 0; i < size; ++i) {
-                const double c = key[e0 + i];
-                if (c > x) {
-                    y = x, ey = ex;
-                    x = c, ex = e0 + i;
-                } else if (c > y) {
-                    y = c, ey = e0 + i;
-                }
-            }
-            own = x;
-            if (a.group_top == 2 && y > kNone) {
-                // scores and biases apart: two groups may hold the same ones
-                // paired otherwise, and these sums are equal then
-                const double bias = a.bias ? (double)no_inf(a.bias[ex]) + (double)no_inf(a.bias[ey]) : 0.0;
-                own = (score_of(ex, 0.0f) + score_of(ey, 0.0f)) + bias;
-            }
-            if (a.need_scores)
-                own = round40(own);
-            score[lane] = own;
+    if (a.G == 1) {
+        for (int e = lane; e < a.E; e += 64) {
+            const float b = a.bias ? a.bias[e] : 0.0f;
+            const float l = load_logit(a.logits, a.bf16, t * a.E + e);
+            key[e] = make_key(score_of(l, b), e, usable(l, b));
         }
         wave_lds();
+    } else {
+        // `per` lanes a group, a power of two: the two best of its scores,
+        // which are full ones yet (keys drop their low bits)
+        const int per = 1 << (31 - __builtin_clz(64 / a.G)), size = a.E / a.G;
+        const int g = lane / per, first = lane % per, e0 = g * size;
+        double x = 2.0 * kNone, y = x;
+        int ex = 0, ey = 0;
+        const auto take = [&](double c, int e) {
+            const bool best = c > x, next = c > y;
+            y = best ? x : next ? c : y;
+            ey = best ? ex : next ? e : ey;
+            x = best ? c : x;
+            ex = best ? e : ex;
+        };
+        if (g < a.G)
+            for (int i = first; i < size; i += per) {
+                const int e = e0 + i;
+                const float b = a.bias ? a.bias[e] : 0.0f;
+                const float l = load_logit(a.logits, a.bf16, t * a.E + e);
+                const double c = usable(l, b) ? score_of(l, b) : 2.0 * kNone;
+                key[e] = c;
+                take(c, e);
+            }
+        for (int d = 1; d < per; d <<= 1) {
+            const double ox = __shfl_xor(x, d), oy = __shfl_xor(y, d);
+            const int oex = __shfl_xor(ex, d), oey = __shfl_xor(ey, d);
+            take(ox, oex);
+            take(oy, oey);
+        }
+        double own = x;
+        if (a.group_top == 2 && y > kNone) {
+            // scores and biases apart: two groups may hold the same ones
+            // paired otherwise, and these sums are equal then
+            const double bias = a.bias ? (double)no_inf(a.bias[ex]) + (double)no_inf(a.bias[ey]) : 0.0;
+            own = (score_of(load_logit(a.logits, a.bf16, t * a.E + ex), 0.0f) +
+                   score_of(load_logit(a.logits, a.bf16, t * a.E + ey), 0.0f)) + bias;
+        }
+        if (a.need_scores)
+            own = round40(own);
+        if (g < a.G && first == 0)
+            score[g] = own;
+        wave_lds();
+        own = score[g];              // (lanes may have summed equal scores differently)
         // a total order, so that topk_groups of them stay whatever lies close
         int before = 0;
-        for (int o = 0; o < a.G; ++o)
-            before += score[o] > own || (score[o] == own && o < lane) ? 1 : 0;
-        wave_lds();
-        if (lane < a.G && before >= a.topk_groups)
-            for (int i = 0; i < size; ++i)
-                key[e0 + i] = 2.0 * kNone;
-        wave_lds();
-        for (int e = lane; e < a.E; e += 64)
-            key[e] = make_key(key[e], e, key[e] > kNone);
+        for (int o = first; o < a.G; o += per)
+            before += score[o] > own || (score[o] == own && o < g) ? 1 : 0;
+        for (int d = 1; d < per; d <<= 1)
+            before += __shfl_xor(before, d);
+        if (g < a.G)
+            for (int e = e0 + first; e < e0 + size; e += per)
+                key[e] = make_key(key[e], e, before < a.topk_groups && key[e] > kNone);
         wave_lds();
     }
     const bool live = !a.mask || a.mask[t] != 0;
