@@ -700,7 +700,7 @@ template <int L, int CH>
 __global__ __launch_bounds__(kThreads) void route_grad_kernel(GradArgs a)
 {
     constexpr int TOK = kThreads / L;
-    __shared__ float val[TOK][kMaxTopk];
+    __shared__ float val[TOK][kMaxTopk], grad[TOK][kMaxTopk];
     __shared__ int who[TOK][kMaxTopk];
     const int lane = threadIdx.x % L, slot = threadIdx.x / L;
     const int64_t t = (int64_t)blockIdx.x * TOK + slot;
@@ -733,55 +733,50 @@ __global__ __launch_bounds__(kThreads) void route_grad_kernel(GradArgs a)
         inv = s > 0.0f ? 1.0f / s : 0.0f;
     }
 
-    // The chosen logits' maximum, from which the scores of a renormalised
-    // choice are taken: only their ratios matter, and scores that all leave
-    // binary32 (sigmoids of logits below -87) have some too.
+    // The slots' logits and gradients, read once; and the chosen logits'
+    // maximum, from which the scores of a renormalised choice are taken: only
+    // their ratios matter, and scores that all leave binary32 (sigmoids of
+    // logits below -87) have some too.
     float top = -INFINITY;
     const float floor = a.softmax ? -INFINITY : -700.0f;       // scores below it are 0 (sigmoid64)
     const auto scored = [&](float l) { return l > -INFINITY && l >= floor; };
-    if (a.renorm) {
-        for (int k = lane; k < a.K; k += L) {
-            const int64_t e = a.idx[row * a.K + k];
-            if (e >= 0 && e < a.E) {
-                const float l = load_logit(a.logits, a.bf16, row * a.E + e);
-                top = fmaxf(top, scored(l) ? l : -INFINITY);
-            }
-        }
-        top = lane_max<L>(top);
-        top = top > -INFINITY ? top : 0.0f;
+    for (int k = lane; k < a.K; k += L) {
+        const int64_t e = a.idx[row * a.K + k];
+        const bool live = e >= 0 && e < a.E;
+        const float l = live ? load_logit(a.logits, a.bf16, row * a.E + e) : -INFINITY;
+        who[slot][k] = live ? (int)e : -1;
+        val[slot][k] = l;
+        grad[slot][k] = live ? a.g[row * a.K + k] * a.scale : 0.0f;
+        top = fmaxf(top, scored(l) ? l : -INFINITY);
     }
+    if (a.renorm)
+        top = lane_max<L>(top);
     // The score of a chosen logit; of a renormalised choice over that of
     // `top` (a sigmoid's: over exp(top) where that is below 1). A sigmoid is
     // exp(min(l, 0)) / (1 + exp(-|l|)).
-    const float from = !a.renorm ? 0.0f : a.softmax ? top : fminf(top, 0.0f);
+    const float from = !a.renorm || top == -INFINITY ? 0.0f : a.softmax ? top : fminf(top, 0.0f);
     const auto share = [&](float l) {
         return a.softmax ? __expf(l - from)
                          : __expf(fminf(l, 0.0f) - from) / (1.0f + __expf(-fabsf(l)));
     };
     float sum = 0.0f, dot = 0.0f;
     for (int k = lane; k < a.K; k += L) {
-        const int64_t e = a.idx[row * a.K + k];
-        const bool live = e >= 0 && e < a.E;
-        const float l = live ? load_logit(a.logits, a.bf16, row * a.E + e) : -INFINITY;
-        const float g = live ? a.g[row * a.K + k] * a.scale : 0.0f;
+        const float l = val[slot][k];
         float s = 0.0f;
         if (scored(l))
             s = dense ? __expf(l - m) * inv : share(l);
-        who[slot][k] = live ? (int)e : -1;
-        val[slot][k] = g;
         sum += s;
-        dot += s * g;
+        dot += s * grad[slot][k];
     }
     sum = lane_sum<L>(sum);
     dot = lane_sum<L>(dot);
     const float over = a.renorm ? (sum > 0.0f ? 1.0f / sum : 0.0f) : 1.0f;
     const float mean = a.renorm ? dot * over : 0.0f;
     for (int k = lane; k < a.K; k += L) {
-        const int e = who[slot][k];
-        const float l = e >= 0 ? load_logit(a.logits, a.bf16, row * a.E + e) : -INFINITY;
+        const float l = val[slot][k];
         float d = 0.0f;
         if (scored(l)) {
-            d = val[slot][k] - mean;
+            d = grad[slot][k] - mean;
             if (!dense) {
                 d *= share(l) * over;
                 if (!a.softmax)
