@@ -173,8 +173,9 @@ __device__ __forceinline__ double fast_key(float l, float bias, float m, float i
 // sure, given the larger one's magnitude and the row's largest score s. Of a
 // sigmoid: exp and the reciprocal are good to a step each and the argument's
 // rounding passes on s (1 - s) |l| < 1/4 of a step, in all below 4 2^-24 s,
-// for either score; a softmax's sum adds 45 2^-24 for up to 40 additions; the
-// sum with the bias half a step. Doubled, and rounded up.
+// for either score; a softmax's exponentials are off by (2 |x| + 4) 2^-24 of
+// themselves, below 5 2^-24 of the largest score, and their sum by 2 ln E + 4
+// of that at most; the sum with the bias half a step. Doubled, and rounded up.
 template <Order ORDER>
 __device__ __forceinline__ double margin(double c, double top)
 {
@@ -631,6 +632,7 @@ __global__ __launch_bounds__(kThreads) void route_kernel(Args a)
         load8<ORDER != kSigmoid>(a.logits, a.bf16, a.vec, row, a.E, (c * L + lane) * 8, l[c]);
 
     float m = 0.0f, inv = 1.0f;
+    double over = 1.0;
     if (ORDER == kSoftmax || (ORDER == kLogits && a.softmax && !a.renorm)) {
         float mx = -INFINITY;
 #pragma unroll
@@ -640,14 +642,21 @@ __global__ __launch_bounds__(kThreads) void route_kernel(Args a)
                 mx = fmaxf(mx, l[c][i]);             // (fmaxf passes over a NaN)
         mx = lane_max<L>(mx);
         m = mx > -INFINITY ? mx : 0.0f;
-        float s = 0.0f;
+        // Exponentials in binary32, by pieces; the pieces' sums and the inverse
+        // in binary64, so that the weights are rounded once: what errors of
+        // some steps leave of a sum of many terms is a fraction of a step.
+        double s = 0.0;
 #pragma unroll
-        for (int c = 0; c < CH; ++c)
+        for (int c = 0; c < CH; ++c) {
+            float x[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                s += l[c][i] > -INFINITY ? __expf(l[c][i] - m) : 0.0f;
+                x[i] = l[c][i] > -INFINITY ? __expf(l[c][i] - m) : 0.0f;
+            s += (double)(((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7])));
+        }
         s = lane_sum<L>(s);
-        inv = s > 0.0f ? 1.0f / s : 0.0f;
+        over = s > 0.0 ? rcp64(s) : 0.0;
+        inv = (float)over;
     }
 
     double best[8];
@@ -662,7 +671,7 @@ __global__ __launch_bounds__(kThreads) void route_kernel(Args a)
     const bool found = live && mine > kNone;
     const int e = found ? key_index(mine) : -1;
     const float chosen = found ? load_logit(a.logits, a.bf16, row * a.E + e) : -INFINITY;
-    const float w = weight_of<L>(a, chosen, (double)m, (double)inv);
+    const float w = weight_of<L>(a, chosen, (double)m, over);
     constexpr uint64_t lanes = L == 64 ? ~0ull : (1ull << (L % 64)) - 1;      // of a token
     uint64_t doubt = ORDER == kLogits ? 0 : __builtin_amdgcn_ballot_w64(!sure && in);
     if (in && lane < a.K && ((doubt >> (threadIdx.x % 64 - lane)) & lanes) == 0) {

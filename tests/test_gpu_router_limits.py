@@ -137,3 +137,20 @@ def test_sigmoids_that_are_zero():
     g = torch.randn(3, 4, generator=torch.Generator().manual_seed(0)).to(DEV)
     dx = epl.route_backward(x.to(DEV), idx, g, score="sigmoid", renormalize=True)
     assert (dx[:2] == 0).all() and (dx[2].abs() <= 4 * U * g[2, 0].abs()).all()
+
+
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("T", [100, 5000])
+@pytest.mark.parametrize("E", [128, 256, 512])
+def test_softmax_weights_are_rounded_once(E, T, biased):
+    """Weights of a softmax over all experts. Their rounding is off by u at
+    most, u / sqrt 3 as a root mean square; the row's sum, of exponentials each
+    good to about a step, whose errors average out over some hundred equal
+    terms, may add 0.45 u to that: 0.75 u together."""
+    g = torch.Generator().manual_seed(E)
+    x = torch.rand(T, E, generator=g) - 0.5
+    b = torch.linspace(-0.2, 0.2, E) if biased else None
+    idx, w = epl.route(x.to(DEV), 8, bias=None if b is None else b.to(DEV))
+    ref = torch.softmax(x.double(), 1).gather(1, idx.cpu())
+    off = (w.cpu().double() - ref) / ref
+    assert off.square().mean().sqrt() < 0.75 * U, float(off.square().mean().sqrt() / U)
