@@ -1124,18 +1124,22 @@ def expert_product(x, weight, expert_start_loc, num_tokens_per_expert, bias=None
 
 
 def expert_weight_grad(grad, x, expert_start_loc, num_tokens_per_expert, out=None, out_dtype=None,
-                       bias_grad=None, accumulate: bool = False, workspace=None, stream=None):
+                       bias_grad=None, accumulate: bool = False, workspace=None, stream=None,
+                       expected_rows: int = 0):
     """Gradient of expert_product's weight, [E, N, K], from that of its
     product `grad` (bf16 [rows, N]) and its input x (bf16 [rows, K]).
     `bias_grad` (fp32 [E, N]) receives the bias's. accumulate=True adds to
-    what `out` and `bias_grad` hold."""
+    what `out` and `bias_grad` hold. `expected_rows` chooses the kernel, as
+    for expert_product: give it where the buffers have many more rows than
+    the experts."""
     torch = _torch()
     _matrix(grad, "grad", 2)
     _matrix(x, "x", 2)
     _matrix(expert_start_loc, "expert_start_loc", 1)
     if stream is not None and x.is_cuda:
         return _run_on(stream, x.device, expert_weight_grad, grad, x, expert_start_loc,
-                       num_tokens_per_expert, out, out_dtype, bias_grad, accumulate, workspace)
+                       num_tokens_per_expert, out, out_dtype, bias_grad, accumulate, workspace,
+                       None, expected_rows)
     E, N, K = expert_start_loc.shape[0], grad.shape[1], x.shape[1]
     if out is None:
         if accumulate:
@@ -1144,7 +1148,7 @@ def expert_weight_grad(grad, x, expert_start_loc, num_tokens_per_expert, out=Non
                           device=x.device)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise ValueError(f"out is {out.dtype}, out_dtype {out_dtype}")
-    p, _ = _product_for(grad.shape[0], 0, E, K, N, EPL_WEIGHT_OUT_IN, EPL_ACT_NONE,
+    p, _ = _product_for(grad.shape[0], int(expected_rows), E, K, N, EPL_WEIGHT_OUT_IN, EPL_ACT_NONE,
                         _type_code(out.dtype, "out"))
     if workspace is None and x.is_cuda:
         workspace = _split_ws(epl_weight_grad_workspace_bytes(p), x.device)

@@ -112,10 +112,14 @@ Kind tiles_for(int64_t m, int64_t n, int64_t experts, int64_t depth)
                                                                                                 : kSmall;
 }
 
+int64_t expected_rows(const epl_product_desc &p)
+{
+    return p.expected_rows > 0 ? std::min(p.expected_rows, p.num_rows) : p.num_rows;
+}
+
 int64_t average_rows(const epl_product_desc &p)
 {
-    const int64_t rows = p.expected_rows > 0 ? std::min(p.expected_rows, p.num_rows) : p.num_rows;
-    return (rows + p.num_experts - 1) / p.num_experts;
+    return (expected_rows(p) + p.num_experts - 1) / p.num_experts;
 }
 
 Kind kind_of(const epl_product_desc &p)
@@ -127,7 +131,7 @@ Kind kind_of(const epl_product_desc &p)
 }
 
 // The depth of a weight gradient's contraction is the expert's rows.
-int64_t grad_depth(const epl_product_desc &p) { return p.num_rows / p.num_experts; }
+int64_t grad_depth(const epl_product_desc &p) { return expected_rows(p) / p.num_experts; }
 
 Kind grad_kind_of(const epl_product_desc &p)
 {

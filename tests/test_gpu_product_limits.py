@@ -78,3 +78,29 @@ def test_gelu_in_its_tails(expected, out):
         tol = 32 * U * mag + half * ref.abs() + 2.0 ** -126
         off = (got[:, 0] - ref).abs()
         assert (off <= tol).all(), (act, float((off / mag).max() / U), z[(off / mag).argmax()])
+
+
+@pytest.mark.parametrize("N,K", [(256, 512), (64, 1032)])
+def test_weight_gradient_of_a_large_buffer(N, K):
+    """Few rows in a buffer of many: with the rows expected, the bits that the
+    rows by themselves give, whatever lies behind them."""
+    counts = [300, 0, 41, 700]
+    rows, cap = sum(counts), 20000
+    g = torch.Generator().manual_seed(N)
+    d = torch.full((cap, N), float("nan")).bfloat16()
+    x = torch.full((cap, K), float("nan")).bfloat16()
+    d[:rows] = torch.randn(rows, N, generator=g).bfloat16()
+    x[:rows] = torch.randn(rows, K, generator=g).bfloat16()
+    d, x = d.to(DEV), x.to(DEV)
+    at, n = i32([0, 300, 300, 341]), i32(counts)
+    kw = dict(out_dtype=torch.float32)
+    want = epl.expert_weight_grad(d[:rows], x[:rows], at, n, **kw)
+    assert torch.equal(epl.expert_weight_grad(d, x, at, n, expected_rows=rows, **kw), want)
+    start = 0
+    for e, c in enumerate(counts):
+        de, xe = d[start:start + c].cpu().double(), x[start:start + c].cpu().double()
+        for got in (want, epl.expert_weight_grad(d, x, at, n, **kw),
+                    epl.expert_weight_grad(d, x, at, n, expected_rows=4, **kw)):
+            tol = 2 * (c + 1) * U * (de.abs().t() @ xe.abs())
+            assert ((got[e].cpu().double() - de.t() @ xe).abs() <= tol).all()
+        start += c
