@@ -409,7 +409,7 @@ int epl_route_backward(const epl_router *p, const void *logits, const int64_t *t
                                    in])                                         */
 
 typedef struct epl_product_desc {
-    int64_t num_rows;      /* rows of the ragged buffers, 0 .. INT32_MAX        */
+    int64_t num_rows;      /* rows of the ragged buffers, 0 .. INT32_MAX - 1023 */
     int64_t expected_rows; /* rows that the experts together are expected to
                               have, 0 = num_rows. Chooses the kernel only: the
                               results hold for any counts. Give it where the

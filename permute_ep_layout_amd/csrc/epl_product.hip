@@ -24,6 +24,10 @@ constexpr int64_t kFewRows = 12;
 constexpr int32_t kMaxCols = 1 << 20;
 constexpr int64_t kMaxWeight = int64_t(1) << 29;
 
+// The kernels step through an expert's rows in 32-bit counts, by up to a tile
+// and the four rows read ahead of it.
+constexpr int64_t kMaxRows = INT32_MAX - 1023;
+
 bool is_grad(int act)
 {
     return act == EPL_ACT_SILU_GRAD || act == EPL_ACT_GELU_GRAD || act == EPL_ACT_SWIGLU_GRAD;
@@ -35,7 +39,7 @@ bool desc_ok(const epl_product_desc *p)
         return false;
     if (p->num_experts < 1 || p->num_experts > P::kMaxExperts)
         return false;
-    if (p->num_rows < 0 || p->num_rows > INT32_MAX || p->expected_rows < 0)
+    if (p->num_rows < 0 || p->num_rows > kMaxRows || p->expected_rows < 0)
         return false;
     if (p->in_cols < 8 || p->in_cols % 8 != 0 || p->in_cols > kMaxCols || p->out_cols < 8 ||
         p->out_cols % 8 != 0 || p->out_cols > kMaxCols)

@@ -25,3 +25,14 @@ def test_weight_gradient_goes_by_the_expected_rows(rows):
     assert size(product(65536, expected=1 << 40)) == size(product(65536))
     sizes = {size(product(n)) for n in (8, 4096, 65536)}
     assert len(sizes) > 1                     # (they differ)
+
+
+def test_rows_that_32_bit_counts_cannot_step_past():
+    """Kernels advance by tiles: a block that ended at the last 32-bit count
+    would be stepped over, so such buffers are refused."""
+    most = 2 ** 31 - 1
+    for rows in (most, most - 31, most - 1022):
+        p = product(rows, K=8, N=8)
+        assert epl.epl_product_validate(p) == epl.EPL_EINVAL
+        assert epl.epl_product_workspace_bytes(p) == 0
+    assert epl.epl_product_validate(product(most - 1023, K=8, N=8)) == epl.EPL_OK
