@@ -293,11 +293,8 @@ __device__ __forceinline__ void two_best(double &a, double &b, double c, double 
 }
 
 // A group's score from its two best keys (a group of one candidate has that
-// one, a group of none -infinity), and how far another's must lie from it.
-struct GroupScore {
-    float score, near;
-};
-
+// one, a group of none -infinity), and how far another's must lie from it, as
+// the low and the high half of 8 bytes. (As a struct it went through memory.)
 // The error of a sum follows its terms, not the sum: biases may cancel in it.
 // Both are halved where scores add, so that no sum leaves binary32; the
 // rounding of the sum fits into the margins, which are twice the errors.
@@ -308,8 +305,17 @@ __device__ __forceinline__ double group_score(const Args &a, double best, double
     const double half = ORDER == kLogits ? 1.0 : 0.5;
     const double sum = two ? best + next : best;
     const double near = margin<ORDER>(best, top) + (two ? margin<ORDER>(next, top) : 0.0);
-    const GroupScore g{(float)(half * sum), best > kNone ? (float)(half * near) : 0.0f};
-    return __builtin_bit_cast(double, g);
+    const uint32_t lo = __builtin_bit_cast(uint32_t, (float)(half * sum));
+    const uint32_t hi = __builtin_bit_cast(uint32_t, best > kNone ? (float)(half * near) : 0.0f);
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+__device__ __forceinline__ float score_half(double g)
+{
+    return __builtin_bit_cast(float, (uint32_t)__builtin_bit_cast(uint64_t, g));
+}
+__device__ __forceinline__ float near_half(double g)
+{
+    return __builtin_bit_cast(float, (uint32_t)(__builtin_bit_cast(uint64_t, g) >> 32));
 }
 
 // A finite score to 40 significant bits, to nearest even: what binary64 and the
@@ -507,7 +513,7 @@ __global__ __launch_bounds__(64) void route_any_kernel(Args a)
 
 // The token's 8 best keys in every lane; false, on one of its lanes at least,
 // where the error of binary32 leaves their order in doubt. `groups` (of
-// GroupScore) and `gone`: the token's LDS, of kMaxGroups each.
+// group_score) and `gone`: the token's LDS, of kMaxGroups each.
 template <int L, int CH, Order ORDER>
 __device__ __forceinline__ bool choose(const Args &a, const float (&l)[CH][8], int lane, float m,
                                        float inv, double *groups, int *gone, double (&best)[8])
@@ -559,10 +565,10 @@ __device__ __forceinline__ bool choose(const Args &a, const float (&l)[CH][8], i
         }
         wave_lds();
         for (int g = lane; g < a.G; g += L) {
-            const auto [own, near] = __builtin_bit_cast(GroupScore, groups[g]);
+            const float own = score_half(groups[g]), near = near_half(groups[g]);
             int before = 0, close = 0;
             for (int o = 0; o < a.G; ++o) {
-                const auto [s, far] = __builtin_bit_cast(GroupScore, groups[o]);
+                const float s = score_half(groups[o]), far = near_half(groups[o]);
                 before += (int)(s > own) | ((int)(s == own) & (int)(o < g));
                 if (ORDER != kLogits)
                     close += (int)(fabsf(s - own) <= fmaxf(near, far));
