@@ -395,7 +395,8 @@ int epl_route_backward(const epl_router *p, const void *logits, const int64_t *t
 /* ---- experts' products ---------------------------------------------------- */
 #define EPL_ACT_NONE        0   /* y = z                                        */
 #define EPL_ACT_SILU        1   /* y = z * sigmoid(z)                           */
-#define EPL_ACT_GELU        2   /* y = z * (1 + erf(z / sqrt 2)) / 2            */
+#define EPL_ACT_GELU        2   /* y = z * (1 + erf(z / sqrt 2)) / 2, to 2^-19
+                                   of itself, in the tail too                   */
 #define EPL_ACT_SWIGLU      3   /* y [rows, N/2] = silu(z[:, :N/2]) * z[:, N/2:];
                                    N % 16 == 0                                  */
 #define EPL_ACT_SILU_GRAD   4   /* y = z * silu'(pre)                           */

@@ -71,7 +71,8 @@ int num_cus()
 
 // The kernel that a product takes: straight from memory for a few rows, or
 // tiles of 256 x 256 or 128 x 128. The counts are on the GPU, so the choice
-// goes by the rows that the caller expects an expert to have on average.
+// goes by the rows that the caller expects an expert to have on average, however
+// unevenly they fall.
 enum Kind { kFew, kLarge, kSmall };
 
 int side_of(Kind k) { return k == kSmall ? 128 : 256; }

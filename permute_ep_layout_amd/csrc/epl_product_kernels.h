@@ -154,7 +154,9 @@ __device__ __forceinline__ float silu_slope(float z)
 // the least relative error (9.3e-8), fitted in binary64 by reweighted least
 // squares to erfc(a / sqrt 2) / 2 over g. The exponent -a^2 log2(e) / 2 is kept
 // in two words, y and yl: rounded to one it would cost 2^-24 a^2 of the result,
-// 25 u at 5. (The constant's own error is in P.)
+// 25 u at 5. (The constant's own error is in P.) 12288 x 2048 outputs of 64
+// experts take 290 us; with a formula of the same cost less 5 instructions that
+// is good to 1.5e-7 absolute, and so to 1e-3 in the tail, 286.
 __device__ __forceinline__ float normal_tail(float a, float &g)
 {
     const float h = a * a, c = 0.721347511f;
@@ -343,11 +345,12 @@ __device__ __forceinline__ void emit_weight(const Args &a, int64_t at, float (&v
 //                       of a 4-row block, 4 consecutive k
 //
 // Bound by the matrix instructions and the clock they leave: 8 x 4096 rows,
-// 7168 -> 4096, in 1.50 - 1.55 ms, 1.24 - 1.29 PFLOP/s (the same loop without
+// 7168 -> 4096, in 1.49 - 1.55 ms, 1.24 - 1.29 PFLOP/s (the same loop without
 // its loads takes 1.11 ms); with few rows an expert by the weights' bytes:
-// 64 x 192 rows, 4096 -> 2048, 285 - 293 us, 4.4 TB/s. Weight gradients: 29765
+// 64 x 192 rows, 4096 -> 2048, 289 - 294 us, 4.4 TB/s. Weight gradients: 29765
 // rows, 4096 x 7168, 1.35 - 1.40 ms (1.25 - 1.29 PFLOP/s); 64 x 192 rows,
-// 2048 x 4096 in binary32, 0.52 - 0.63 ms, by the 2.1 GB they write.
+// 2048 x 4096 in binary32, 0.63 - 0.65 ms, by the 2.1 GB they write (into the
+// same buffers every time 0.49 - 0.53).
 
 __device__ __forceinline__ int swz(int row) { return (row >> 1) & 7; }
 __device__ __forceinline__ int swz_t(int k) { return ((k & 3) << 1) | (((k >> 3) & 1) << 3); }
@@ -399,7 +402,9 @@ __device__ __forceinline__ const uint16_t *at(const uint16_t *stage, int bytes, 
 
 // offset ^= by, in place: the compiler must not keep a register for every value
 // (with those the weight gradient's loop spills: 1.86 ms against 1.35 for
-// 29765 rows of 7168 x 4096).
+// 29765 rows of 7168 x 4096). Left outside the loops: 2 vector registers of the
+// data gradient's 256 x 256 tile, and scalar ones, which go to lanes of a vector
+// register.
 __device__ __forceinline__ void walk(int &offset, int by)
 {
     offset ^= by;
@@ -913,7 +918,10 @@ __global__ __launch_bounds__(tile_threads(BN)) void join_kernel(Args a, int grid
 // ------------------------------------------------------ few-rows kernel --
 //
 // For experts with a few rows the weights' bytes are the cost: each is read
-// once, straight into the registers of the matrix instruction. A workgroup
+// once for 32 rows, straight into the registers of the matrix instruction (an
+// expert of many among experts of few has its weights read that much oftener:
+// 768 rows over 64 experts, 4096 -> 2048, evenly 221 us, with 705 of them in
+// one expert 429). A workgroup
 // of WAVES waves takes 32 columns of one expert; the waves share the
 // contraction (128 deep a turn each) and add their sums through LDS in wave
 // order. Workgroups start at different places of the contraction and come
@@ -1044,7 +1052,9 @@ __global__ __launch_bounds__(WAVES * 64, WAVES == 4 ? 2 : 4) void few_rows_kerne
 //
 // db[e, n] = sum over the expert's rows of d[p, n], in binary32. A workgroup
 // takes 64 columns (8 lanes of 8) of one expert; its 32 row lanes add rows
-// 32 apart and are added in order through LDS.
+// 32 apart and are added in order through LDS. 12288 rows over 64 experts, 2048
+// columns: 10 us. Rows are not shared over workgroups, so that one expert of
+// 16384 rows and 64 columns takes 142 us, four times its weight gradient.
 
 constexpr int kBiasThreads = 256;
 

@@ -11,8 +11,11 @@
 // which orders the experts as any score does and leaves the low 29 bits of a
 // binary64 free: the order is exact. With them scores are compared as
 // binary64 numbers, good to about 2^-44, to 41 bits. They are first computed
-// in binary32; where two that matter lie within its error of each other, a
-// few tokens in a thousand, the choice is done again in binary64.
+// in binary32; where two that matter lie within its error of each other, the
+// choice is done again in binary64: 1 or 2 tokens in a thousand with binary32
+// logits, but every third where scores tie, as those of bf16 logits do with a
+// bias of zero (65536 tokens, 256 experts: 94 us, not 28; of 4 of 8 groups 115,
+// not 35). Equal logits with equal biases would need no second look.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -53,8 +56,8 @@ struct GradArgs {
 };
 
 // exp(x) in binary64 to a few units of 2^-47: x = n ln 2 + r with |r| <=
-// ln 2 / 2 (ln 2 split in two words), the Taylor polynomial of degree 11 in
-// r (its remainder is below 2^-47), and an exponent shift.
+// ln 2 / 2 (ln 2 in the two words of fdlibm's e_exp.c), the Taylor polynomial
+// of degree 11 in r (its remainder is below 2^-47), and an exponent shift.
 __device__ __forceinline__ double exp64(double x)
 {
     x = fmin(fmax(x, -700.0), 700.0);
@@ -388,6 +391,8 @@ __device__ __forceinline__ float weight_of(const Args &a, float l, double m, dou
 // Scores in binary64; K rounds, each the largest key below the last round's.
 // For sizes that the kernel below does not cover (K above 8, groups that end
 // inside a piece), and for its tokens whose choice binary32 leaves in doubt.
+// 16384 tokens, top-10 of 512 experts: 107 - 110 us; top-6 of 160 in 8 groups:
+// 49 - 55 us; by the K rounds over LDS and the binary64 scores.
 __device__ __forceinline__ void route_token(const Args &a, int64_t t, int lane, double *key,
                                             double *score)
 {
@@ -508,7 +513,7 @@ __global__ __launch_bounds__(64) void route_any_kernel(Args a)
 // pieces, merges them to its 8 best, and log2(L) merges across lanes leave
 // the token's 8 best, in order, in every lane. Bound by its vector
 // instructions: 65536 tokens x 256 experts in binary32 take 20 us by sigmoid
-// (3.6 TB/s) and 34 us with a bias and 4 of 8 groups besides (2.1 TB/s), 1600
+// (3.6 TB/s) and 35 us with a bias and 4 of 8 groups besides (2.1 TB/s), 1600
 // instructions a wave of 8 tokens, which issue in 84% of its cycles.
 
 // The token's 8 best keys in every lane; false, on one of its lanes at least,
