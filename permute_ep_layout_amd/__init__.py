@@ -618,8 +618,9 @@ def epl_combine(p: Problem, expert_out, expert_rows, output_index, topk_weights,
     _need_ws_arg(workspace, dev, allow_none=True)
     if workspace is not None:
         _need_workspace(workspace, WS_HEADER_BYTES, "epl_combine")
-    _launch("epl_combine", dev, stream, _prob(p), _ptr(expert_out), int(expert_rows),
-            _ptr(output_index), _ptr(topk_weights), int(out_dtype), _ptr(y), _ptr(workspace))
+    _check(load().epl_combine(_prob(p), _ptr(expert_out), int(expert_rows), _ptr(output_index),
+                              _ptr(topk_weights), int(out_dtype), _ptr(y), _ptr(workspace),
+                              _stream(stream, dev)), "epl_combine")
 
 
 def epl_expert_scale(p: Problem, rows_in, m_indices, capacity_rows, rows_out, workspace,
@@ -1187,5 +1188,9 @@ def dispatch_backward(grad_rows, output_index, out_dtype=None, workspace=None, s
     if stream is not None and output_index.is_cuda:
         return _run_on(stream, output_index.device, dispatch_backward, grad_rows, output_index,
                        out_dtype, workspace)
-    ones = torch.ones(output_index.shape, dtype=torch.float32, device=output_index.device)
+    dev = output_index.device
+    ones = torch.ones(output_index.shape, dtype=torch.float32, device=dev)
+    if output_index.is_cuda and dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev.index):         # kernels go to the current GPU
+            return combine(grad_rows, output_index, ones, out_dtype, workspace)
     return combine(grad_rows, output_index, ones, out_dtype, workspace)
