@@ -1,17 +1,18 @@
 """Cases of the MoE layer's operators on 8-bit rows: the cast of rows and of
-weights to e4m3 with a scale for each block of 128, the way back, and the
-experts' matrix products on such rows and weights, with the gated activation
-and the cast of its result in the epilogue, forwards and backwards. Each can
-run in a plain form (elementary torch operations in 32 bits) or through the
-package.
+weights to e4m3 with a scale for each block of 128, the way back, the experts'
+matrix products on such rows and weights, and the experts' gated feed-forward
+block on them, forwards and backwards. Each can run in a plain form (elementary
+torch operations in 32 bits) or through the package.
 
 A case is one call of one operator, ``case["op"]``:
 
     quantize         rows [, gate] -> e4m3 codes, a scale for each 128 columns
     dequantize       codes, scales -> rows
     quantize_weight  weights -> e4m3 codes, a scale for each 128 x 128 block
-    product          8-bit rows @ 8-bit weight of their expert, with bias, activation and
-                     residual; result in bf16 or fp32, as codes and scales, or both
+    product          8-bit rows @ 8-bit weight of their expert, with bias, activation, residual
+    block            8-bit rows -> gate and up projection, gated activation, its cast to 8 bits,
+                     down projection
+    block_grad       gradient of a block's result -> of its projections and of its rows
 
 Codes are returned as float8_e4m3fn numbers next to their scales. Scales are
 fp32 ("f32") or powers of two as exponents ("ue8m0"): of rows packed four to
@@ -49,31 +50,28 @@ def listed():
         # a rank's gate and up projections after the optimizer's step
         dict(name="quantize_weight, 8 experts", op="quantize_weight", experts=8, n=4096, k=7168,
              dtype="bf16", fmt="f32"),
-        # decode: gate and up projection, activation and cast in one call; weights' bytes cost
-        dict(name="product, decode", op="product", experts=8, rows=64, k=7168, n=4096,
-             act="swiglu", bias=False, residual=False, pre=False, transposed=False, out="none",
-             codes=True, fmt="f32", spread="uniform", spare=0),
         # 2048 tokens, top-6 of 64 experts: bytes and operations in balance, whole epilogue
         dict(name="product, 64 experts", op="product", experts=64, rows=12288, k=4096, n=2048,
-             act="gelu", bias=True, residual=True, pre=False, transposed=False, out="bf16",
-             codes=False, fmt="f32", spread="uniform", spare=0),
-        # receive side, training: gated block whose first product is kept for the way back
-        dict(name="product, 32768 rows", op="product", experts=8, rows=32768, k=7168, n=4096,
-             act="swiglu", bias=False, residual=False, pre=True, transposed=False, out="none",
-             codes=True, fmt="f32", spread="uniform", spare=0),
-        # its second product, scales that are powers of two
-        dict(name="product, second, ue8m0", op="product", experts=8, rows=32768, k=2048, n=7168,
-             act="none", bias=False, residual=False, pre=False, transposed=False, out="bf16",
-             codes=False, fmt="ue8m0", spread="uniform", spare=0),
-        # data gradient of the second product through the gated activation: bf16 for the weight
-        # gradient and codes for the next product at once; uneven experts
-        dict(name="product, data gradient", op="product", experts=8, rows=12289, k=7168, n=2048,
-             act="swiglu_grad", bias=False, residual=False, pre=True, transposed=True,
-             out="bf16", codes=True, fmt="f32", spread="skew", spare=511),
-        # data gradient of the first product, decoder-sized batch of a small layer
+             act="gelu", bias=True, residual=True, pre=False, transposed=False, fmt="f32",
+             spread="uniform", spare=0),
+        # data gradient of a small layer's first product, a few rows behind the last expert
         dict(name="product, small", op="product", experts=16, rows=500, k=640, n=512,
-             act="none", bias=False, residual=False, pre=False, transposed=True, out="f32",
-             codes=False, fmt="f32", spread="uniform", spare=12),
+             act="none", bias=False, residual=False, pre=False, transposed=True, fmt="f32",
+             spread="uniform", spare=12),
+        # decode: 64 routed rows over the 8 experts of a rank, in the low-latency rectangle; the
+        # weights' bytes are the cost
+        dict(name="block, decode", op="block", experts=8, rows=64, k=7168, f=2048, pre=False,
+             fmt="rect", spread="uniform", spare=0),
+        # receive side, training: 32768 rows over a rank's 8 experts; the projections are kept
+        # for the way back
+        dict(name="block, 32768 rows", op="block", experts=8, rows=32768, k=7168, f=2048,
+             pre=True, fmt="f32", spread="uniform", spare=0),
+        # a small step of fine-tuning, scales that are powers of two
+        dict(name="block_grad, small", op="block_grad", experts=16, rows=500, k=640, f=256,
+             fmt="ue8m0", spread="uniform", spare=0),
+        # the way back through a rank's experts, unevenly filled, in a buffer with room to spare
+        dict(name="block_grad, 12289 rows", op="block_grad", experts=8, rows=12289, k=7168,
+             f=2048, fmt="f32", spread="skew", spare=511),
     ]
 
 
@@ -83,7 +81,8 @@ def _spread(rng, low, high):
 
 
 def draw(rng):
-    op = rng.choice(["quantize", "dequantize", "quantize_weight", "product", "product", "product"])
+    op = rng.choice(["quantize", "dequantize", "quantize_weight", "product", "product", "block",
+                     "block", "block_grad"])
     if op == "quantize":
         act = rng.choice(["none", "swiglu"])
         while True:
@@ -110,26 +109,31 @@ def draw(rng):
                 break
         return dict(op=op, experts=experts, n=n, k=k, dtype=rng.choice(["bf16", "f32"]),
                     fmt=rng.choice(["f32", "ue8m0"]))
+    experts = rng.choice([1, 2, 8, 16, 64])
+    common = dict(op=op, experts=experts, spread=rng.choice(["uniform", "skew"]),
+                  spare=rng.choice([0, 0, 37]))
+    if op != "product":
+        while True:
+            rows, k, f = _spread(rng, 1, 16384), 128 * _spread(rng, 1, 56), \
+                128 * _spread(rng, 1, 32)
+            if experts * k * f <= 64 * 2048 * 1024 and rows * k * f <= 12289 * 7168 * 2048:
+                break
+        return dict(common, rows=rows, k=k, f=f,
+                    fmt=rng.choice(["f32", "ue8m0"] if op == "block_grad" else
+                                   ["f32", "ue8m0", "rect"]),
+                    **(dict(pre=rng.random() < 0.5) if op == "block" else {}))
     while True:
-        experts = rng.choice([1, 2, 8, 16, 64])
-        rows = _spread(rng, 1, 16384)
-        k = 16 * _spread(rng, 4, 448)
-        n = 16 * _spread(rng, 4, 256)
+        rows, k, n = _spread(rng, 1, 16384), 16 * _spread(rng, 4, 448), 16 * _spread(rng, 4, 256)
         if experts * k * n <= 64 * 4096 * 2048 and rows * k * n <= 16384 * 7168 * 2048:
             break
     act = rng.choice(["none", "silu", "gelu", "swiglu", "swiglu", "silu_grad", "gelu_grad",
                       "swiglu_grad"])
     grad = act.endswith("_grad")
-    codes = rng.random() < 0.5
-    if codes:                            # whole blocks of the result
-        n = 256 * max(1, round(n / 256))
-    return dict(op=op, experts=experts, rows=rows, k=k, n=n, act=act,
-                bias=not grad and rng.random() < 0.4, residual=not grad and rng.random() < 0.3,
+    return dict(common, rows=rows, k=k, n=n, act=act, bias=not grad and rng.random() < 0.4,
+                residual=not grad and rng.random() < 0.3,
                 pre=grad or (act != "none" and rng.random() < 0.4),
                 transposed=rng.random() < (0.7 if grad else 0.2),
-                out=rng.choice(["bf16", "none"]) if codes else rng.choice(["bf16", "bf16", "f32"]),
-                codes=codes, fmt=rng.choice(["f32", "ue8m0", "rect"]),
-                spread=rng.choice(["uniform", "skew"]), spare=rng.choice([0, 0, 37]))
+                fmt=rng.choice(["f32", "ue8m0", "rect"]))
 
 
 _DTYPE = {"f32": torch.float32, "bf16": torch.bfloat16}
@@ -287,26 +291,38 @@ def prepare(case, seed):
         s["scale"] = torch.zeros((groups + 3) // 4, total, dtype=torch.int32, device=dev) \
             if fmt == "ue8m0" else torch.zeros(total, groups, device=dev)
         return s
+    e = case["experts"]
+    weight_fmt = "ue8m0" if fmt == "ue8m0" else "f32"
+
+    def weight(n, k):
+        return _cast_weight(normal(e, n, k, std=1.0 / math.sqrt(k)), weight_fmt)
+
+    if op in ("block", "block_grad"):
+        s["w1"], s["w1_scale"] = weight(2 * case["f"], case["k"])
+        s["w2"], s["w2_scale"] = weight(case["k"], case["f"])
+        s["y"] = torch.zeros(total, case["k"], dtype=torch.bfloat16, device=dev)
+        s["pre"] = None
+        if op == "block_grad":
+            s["pre"] = normal(total, 2 * case["f"], dtype=torch.bfloat16)
+            s["dy"] = rows_of(total, case["k"]).to(torch.bfloat16)
+            s["dz"] = torch.zeros_like(s["pre"])
+            return s
+        if case["pre"]:
+            s["pre"] = torch.zeros(total, 2 * case["f"], dtype=torch.bfloat16, device=dev)
     k = case["cols"] if op == "dequantize" else case["k"]
     codes, scale = _cast_rows(rows_of(total, k), fmt)
     s["x"] = codes.view(torch.uint8)
     s["x_scale"] = _lay(case, scale, _blocks_of(k))
     if op == "dequantize":
         s["y"] = torch.zeros(total, k, dtype=_DTYPE[case["dtype"]], device=dev)
+    if op != "product":
         return s
-    e, n, act = case["experts"], case["n"], case["act"]
-    w = normal(*((e, k, n) if case["transposed"] else (e, n, k)), std=1.0 / math.sqrt(k))
-    s["w"], s["w_scale"] = _cast_weight(w, "ue8m0" if fmt == "ue8m0" else "f32")
-    del w
+    n, act = case["n"], case["act"]
+    s["w"], s["w_scale"] = weight(k, n) if case["transposed"] else weight(n, k)
     s["b"] = normal(e, n, std=0.5) if case["bias"] else None
     cols = n // 2 if act == "swiglu" else 2 * n if act == "swiglu_grad" else n
     s["res"] = normal(total, cols, dtype=torch.bfloat16) if case["residual"] else None
-    s["y"] = None if case["out"] == "none" else torch.zeros(total, cols, dtype=_DTYPE[case["out"]],
-                                                            device=dev)
-    s["codes"] = s["scale"] = None
-    if case["codes"]:
-        s["codes"] = torch.zeros(total, cols, dtype=torch.uint8, device=dev)
-        s["scale"] = torch.zeros(total, cols // BLOCK, device=dev)
+    s["y"] = torch.zeros(total, cols, dtype=torch.bfloat16, device=dev)
     s["pre"] = None
     if act.endswith("_grad"):
         s["pre"] = normal(total, cols, dtype=torch.bfloat16)
@@ -365,23 +381,31 @@ def _plain_quantize_weight(c, s):
     return codes.view(torch.float8_e4m3fn), scale
 
 
-def _outputs(y, codes, scale, z):
-    return [v for v in (y, None if codes is None else codes.view(torch.float8_e4m3fn), scale, z)
-            if v is not None]
-
-
-def _plain_product(c, s):
-    act, total = c["act"], s["x"].shape[0]
-    used, expert, place = _used(s, total)
-    x = _decode(s["x"], _row_scales(c, s["x_scale"])[:, :_blocks_of(c["k"])])
-    w = _decode_weight(s["w"], s["w_scale"])
+def _plain_rows(s, x, w, transposed):
+    """z [rows, n] of fp32 rows x and fp32 weights w: each row with its expert's."""
+    total = x.shape[0]
+    _, expert, place = _used(s, total)
     longest = max(s["longest"], 1)
     at = torch.arange(longest, device=x.device)
     live = at < s["counts"][:, None]
     rows = (s["starts"][:, None] + at).clamp(max=total - 1).long()
     z = torch.bmm(torch.where(live[:, :, None], x[rows], 0.0),
-                  w if c["transposed"] else w.transpose(1, 2))
-    z = z[expert, place.clamp(max=longest - 1)]
+                  w if transposed else w.transpose(1, 2))
+    return z[expert, place.clamp(max=longest - 1)]
+
+
+def _gate_grad(z, pre):
+    """Gradient of silu(a) u with respect to pre = [a, u]."""
+    half = z.shape[1]
+    gate, up = pre[:, :half].float(), pre[:, half:].float()
+    return torch.cat([z * up * _slope("silu", gate), z * _silu_gelu("silu", gate)], 1)
+
+
+def _plain_product(c, s):
+    act = c["act"]
+    used, expert, _ = _used(s, s["x"].shape[0])
+    x = _decode(s["x"], _row_scales(c, s["x_scale"])[:, :_blocks_of(c["k"])])
+    z = _plain_rows(s, x, _decode_weight(s["w"], s["w_scale"]), c["transposed"])
     if s["b"] is not None:
         z = z + s["b"][expert]
     if act == "none":
@@ -390,9 +414,7 @@ def _plain_product(c, s):
         half = z.shape[1] // 2
         y = _silu_gelu("silu", z[:, :half]) * z[:, half:]
     elif act == "swiglu_grad":
-        half = z.shape[1]
-        gate, up = s["pre"][:, :half].float(), s["pre"][:, half:].float()
-        y = torch.cat([z * up * _slope("silu", gate), z * _silu_gelu("silu", gate)], 1)
+        y = _gate_grad(z, s["pre"])
     elif act.endswith("_grad"):
         y = z * _slope(act[:4], s["pre"].float())
     else:
@@ -400,20 +422,41 @@ def _plain_product(c, s):
     if s["res"] is not None:
         y = y + s["res"].float()
     used = used[:, None]
-    codes = scale = None
-    if c["codes"]:
-        codes, scale = _cast_rows(y, "f32")
-        codes = torch.where(used, codes.view(torch.uint8), s["codes"])
-        scale = torch.where(used, scale, s["scale"])
-    kept = None
-    if s["pre"] is not None and not act.endswith("_grad"):
-        kept = torch.where(used, z.to(torch.bfloat16), s["pre"])
-    y = None if s["y"] is None else torch.where(used, y.to(s["y"].dtype), s["y"])
-    return _outputs(y, codes, scale, kept)
+    y = torch.where(used, y.to(torch.bfloat16), s["y"])
+    if s["pre"] is None or act.endswith("_grad"):
+        return y
+    return y, torch.where(used, z.to(torch.bfloat16), s["pre"])
+
+
+def _again(x, fmt):
+    """fp32 rows through 8 bits and back, with the scales that a block uses inside."""
+    codes, scale = _cast_rows(x, fmt)
+    return _decode(codes.view(torch.uint8), _two_to(scale) if fmt == "ue8m0" else scale)
+
+
+def _plain_block(c, s):
+    x = _decode(s["x"], _row_scales(c, s["x_scale"])[:, :_blocks_of(c["k"])])
+    z = _plain_rows(s, x, _decode_weight(s["w1"], s["w1_scale"]), False)
+    h = _silu_gelu("silu", z[:, :c["f"]]) * z[:, c["f"]:]
+    y = _plain_rows(s, _again(h, "f32"), _decode_weight(s["w2"], s["w2_scale"]), False)
+    used = _used(s, x.shape[0])[0][:, None]
+    y = torch.where(used, y.to(torch.bfloat16), s["y"])
+    return y if s["pre"] is None else (y, torch.where(used, z.to(torch.bfloat16), s["pre"]))
+
+
+def _plain_block_grad(c, s):
+    used = _used(s, s["dy"].shape[0])[0][:, None]
+    dh = _plain_rows(s, _again(s["dy"].float(), "f32"), _decode_weight(s["w2"], s["w2_scale"]),
+                     True)
+    dz = _gate_grad(dh, s["pre"])
+    dx = _plain_rows(s, _again(dz, "f32"), _decode_weight(s["w1"], s["w1_scale"]), True)
+    return (torch.where(used, dx.to(torch.bfloat16), s["y"]),
+            torch.where(used, dz.to(torch.bfloat16), s["dz"]))
 
 
 _PLAIN = {"quantize": _plain_quantize, "dequantize": _plain_dequantize,
-          "quantize_weight": _plain_quantize_weight, "product": _plain_product}
+          "quantize_weight": _plain_quantize_weight, "product": _plain_product,
+          "block": _plain_block, "block_grad": _plain_block_grad}
 
 
 # -------------------------------------------------- the package's operators --
@@ -436,16 +479,30 @@ def _own_quantize_weight(epl, c, s):
 
 
 def _own_product(epl, c, s):
-    epl.expert_product_fp8(s["x"], s["x_scale"], s["w"], s["w_scale"], s["starts"], s["counts"],
-                           bias=s["b"], activation=c["act"], residual=s["res"], pre=s["pre"],
-                           out=s["y"], quantized=(s["codes"], s["scale"]) if c["codes"] else None,
-                           transposed=c["transposed"], expected_rows=c["rows"])
-    return _outputs(s["y"], s["codes"], s["scale"],
-                    None if c["act"].endswith("_grad") else s["pre"])
+    y = epl.expert_product_fp8(s["x"], s["x_scale"], s["w"], s["w_scale"], s["starts"],
+                               s["counts"], bias=s["b"], activation=c["act"], residual=s["res"],
+                               pre=s["pre"], out=s["y"], transposed=c["transposed"],
+                               expected_rows=c["rows"])
+    return y if s["pre"] is None or c["act"].endswith("_grad") else (y, s["pre"])
+
+
+def _own_block(epl, c, s):
+    y = epl.gated_block_fp8(s["x"], s["x_scale"], s["w1"], s["w1_scale"], s["w2"], s["w2_scale"],
+                            s["starts"], s["counts"], pre=s["pre"], out=s["y"],
+                            expected_rows=c["rows"])
+    return y if s["pre"] is None else (y, s["pre"])
+
+
+def _own_block_grad(epl, c, s):
+    return epl.gated_block_fp8_backward(s["dy"], s["pre"], s["w1"], s["w1_scale"], s["w2"],
+                                        s["w2_scale"], s["starts"], s["counts"],
+                                        grad_x=s["y"], grad_pre=s["dz"],
+                                        expected_rows=c["rows"])
 
 
 _OWN = {"quantize": _own_quantize, "dequantize": _own_dequantize,
-        "quantize_weight": _own_quantize_weight, "product": _own_product}
+        "quantize_weight": _own_quantize_weight, "product": _own_product, "block": _own_block,
+        "block_grad": _own_block_grad}
 
 
 def run(state):
@@ -471,15 +528,21 @@ def work(case):
         gated = case.get("act") == "swiglu"
         return {"bytes": rows * (cols * (size * (2 if gated else 1) + 1) + _blocks_of(cols) * per),
                 "flops": rows * cols * (8 if gated else 3)}
-    e, k, n = case["experts"], case["k"], case["n"]
+    e, k = case["experts"], case["k"]
     used = e * (1.0 - (1.0 - 1.0 / e) ** rows)        # experts with at least one row
-    act = case["act"]
+    if op in ("block", "block_grad"):
+        f = case["f"]
+        weights = used * 3 * (f * k + _blocks_of(f) * _blocks_of(k) * per)
+        if op == "block":                             # x, y and, where it is kept, z
+            return {"bytes": weights + rows * (k + _blocks_of(k) * per + 2 * k +
+                                               (4 * f if case["pre"] else 0)),
+                    "flops": 6.0 * rows * k * f + 20 * rows * f}
+        return {"bytes": weights + rows * (4 * k + 8 * f),           # dy, dx, z, dz
+                "flops": 6.0 * rows * k * f + 30 * rows * f}
+    n, act = case["n"], case["act"]
     cols = n / 2 if act == "swiglu" else 2 * n if act == "swiglu_grad" else n
-    out = {"none": 0, "bf16": 2, "f32": 4}[case["out"]] * cols
-    if case["codes"]:
-        out += cols + 4 * cols / BLOCK
     return {"bytes": rows * (k + _blocks_of(k) * per) +
-            used * (n * k + _blocks_of(n) * _blocks_of(k) * per) + rows * out +
+            used * (n * k + _blocks_of(n) * _blocks_of(k) * per) + 2 * rows * cols +
             (4 * used * n if case["bias"] else 0) + (2 * rows * cols if case["residual"] else 0) +
             (2 * rows * (cols if act.endswith("_grad") else n) if case["pre"] else 0),
             "flops": 2.0 * rows * k * n + 10 * rows * n}
@@ -487,7 +550,8 @@ def work(case):
 
 # ------------------------------------------- definitions, in 64 bits --
 #
-# A code is held to the number that it rounds, x / scale.
+# A code that is returned is held to the number that it rounds, x / scale; one that a block
+# casts inside is rounded as the definition says.
 
 def _exact_cast(x, fmt):
     """(x / scale, scale or exponent byte) by groups of 128 columns, in 64 bits."""
@@ -580,25 +644,45 @@ def _exact_quantize_weight(c, s):
     return codes, scale.to(torch.uint8) if c["fmt"] == "ue8m0" else scale
 
 
-def _exact_weight(s, e):
-    w = s["w"][e].view(torch.float8_e4m3fn).double()
-    sc = s["w_scale"][e]
+def _exact_weight(s, e, name):
+    w = s[name][e].view(torch.float8_e4m3fn).double()
+    sc = s[name + "_scale"][e]
     sc = torch.exp2(sc.double() - 127) if sc.dtype == torch.uint8 else sc.double()
     for i in range(sc.shape[0]):
         w[i * BLOCK:(i + 1) * BLOCK] *= sc[i].repeat_interleave(BLOCK)[:w.shape[1]]
     return w
 
 
+def _exact_gate_grad(z, kept):
+    gate, up = kept.double().chunk(2, 1)
+    p = torch.sigmoid(gate)
+    return torch.cat([z * up * (p + gate * p * torch.sigmoid(-gate)), z * gate * p], 1)
+
+
+def _exact_again(x):
+    """Rows through 8 bits and back: to the nearest of the 127 magnitudes, ties to even codes.
+    The cast is defined in binary32 steps (x times the rounded 448 / amax): in exact numbers
+    many bf16 values would lie right between two codes."""
+    x = x.float()
+    v, wide = torch.empty_like(x), torch.empty_like(x)
+    for g in range(0, x.shape[1], BLOCK):
+        part = x[:, g:g + BLOCK]
+        amax = part.abs().max(dim=1, keepdim=True).values
+        v[:, g:g + BLOCK] = torch.where(amax > 0, part * (TOP / amax), torch.zeros_like(part))
+        wide[:, g:g + BLOCK] = amax / TOP
+    v = v.double()
+    step = torch.exp2(torch.floor(torch.log2(v.abs().clamp(min=2.0 ** -6))) - 3)
+    return (torch.round(v / step) * step).clamp(-TOP, TOP) * wide.double()
+
+
 def _exact_product(c, s):
     act = c["act"]
     grad = act.endswith("_grad")
     keeps = s["pre"] is not None and not grad
-    total = s["x"].shape[0]
-    cols = c["n"] // 2 if act == "swiglu" else 2 * c["n"] if act == "swiglu_grad" else c["n"]
-    y = torch.zeros(total, cols, dtype=torch.float64, device=s["x"].device)
+    y = s["y"].double()
     pre = s["pre"].double() if keeps else None
     for e, a, b in _each(s):
-        w = _exact_weight(s, e)
+        w = _exact_weight(s, e, "w")
         z = _exact_rows(c, s, a, b, c["k"]) @ (w if c["transposed"] else w.t())
         if s["b"] is not None:
             z += s["b"][e].double()
@@ -621,20 +705,37 @@ def _exact_product(c, s):
             v = z * (0.5 * torch.erfc(-kept / math.sqrt(2.0)) +
                      kept * torch.exp(-kept.square() / 2) * 0.3989422804014327)
         else:
-            gate, up = kept.chunk(2, 1)
-            p = torch.sigmoid(gate)
-            v = torch.cat([z * up * (p + gate * p * torch.sigmoid(-gate)), z * gate * p], 1)
+            v = _exact_gate_grad(z, kept)
         if s["res"] is not None:
             v = v + s["res"][a:b].double()
         y[a:b] = v
-    codes = scale = None
-    if c["codes"]:
-        codes, scale = _exact_cast(y, "f32")
-    return [v for v in (None if s["y"] is None else y, codes, scale, pre) if v is not None]
+    return (y, pre) if keeps else y
+
+
+def _exact_block(c, s):
+    y = s["y"].double()
+    pre = None if s["pre"] is None else s["pre"].double()
+    for e, a, b in _each(s):
+        z = _exact_rows(c, s, a, b, c["k"]) @ _exact_weight(s, e, "w1").t()
+        if pre is not None:
+            pre[a:b] = z
+        gate, up = z.chunk(2, 1)
+        y[a:b] = _exact_again(gate * torch.sigmoid(gate) * up) @ _exact_weight(s, e, "w2").t()
+    return y if pre is None else (y, pre)
+
+
+def _exact_block_grad(c, s):
+    dx, dz = s["y"].double(), s["dz"].double()
+    for e, a, b in _each(s):
+        dh = _exact_again(s["dy"][a:b].double()) @ _exact_weight(s, e, "w2")
+        dz[a:b] = _exact_gate_grad(dh, s["pre"][a:b])
+        dx[a:b] = _exact_again(dz[a:b]) @ _exact_weight(s, e, "w1")
+    return dx, dz
 
 
 _EXACT = {"quantize": _exact_quantize, "dequantize": _exact_dequantize,
-          "quantize_weight": _exact_quantize_weight, "product": _exact_product}
+          "quantize_weight": _exact_quantize_weight, "product": _exact_product,
+          "block": _exact_block, "block_grad": _exact_block_grad}
 
 
 def exact(case, seed):
