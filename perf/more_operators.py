@@ -165,7 +165,8 @@ def _cast(x, fmt):
         inv = 1.0 / _two_to(scale)
     else:
         scale = amax / TOP
-        inv = torch.where(amax > 0, TOP / amax, 0.0)
+        # (a number over a tensor is its reciprocal times the number: two roundings)
+        inv = torch.where(amax > 0, torch.full_like(amax, TOP) / amax, 0.0)
     return (x * inv[..., None]).to(torch.float8_e4m3fn), scale
 
 
@@ -190,7 +191,7 @@ def _row_scales(c, scale):
     """Scales [rows, groups] as numbers, from any layout."""
     if c["fmt"] == "ue8m0":
         words, rows = scale.shape
-        b = scale.t().contiguous().view(torch.uint8).view(rows, 4 * words)
+        b = scale.t().reshape(-1).view(torch.uint8).view(rows, 4 * words)
         return _two_to(b.int())
     if c["fmt"] == "rect":
         return scale.transpose(1, 2).reshape(-1, scale.shape[1])
@@ -668,7 +669,8 @@ def _exact_again(x):
     for g in range(0, x.shape[1], BLOCK):
         part = x[:, g:g + BLOCK]
         amax = part.abs().max(dim=1, keepdim=True).values
-        v[:, g:g + BLOCK] = torch.where(amax > 0, part * (TOP / amax), torch.zeros_like(part))
+        inv = torch.full_like(amax, TOP) / amax
+        v[:, g:g + BLOCK] = torch.where(amax > 0, part * inv, torch.zeros_like(part))
         wide[:, g:g + BLOCK] = amax / TOP
     v = v.double()
     step = torch.exp2(torch.floor(torch.log2(v.abs().clamp(min=2.0 ** -6))) - 3)
