@@ -89,6 +89,9 @@ extern "C" {
                                out_scale[j * capacity + p], the transposed layout
                                sglang allocates for UE8M0 scales ("参考sglang代码，
                                重构vllm021中EP高吞吐代码，消除空泡问题", section 2.2) */
+#define EPL_SCALE_F32_RECT 3 /* fp32 [E, S, cap], the scales of epl_ll_dispatch's rectangle
+                               (8-bit operators only): group g of row j of expert e at
+                               (e * S + g) * cap + j                               */
 
 /* ---- problem description ----------------------------------------------- */
 typedef struct epl_problem {
@@ -468,6 +471,117 @@ int epl_expert_weight_grad(const epl_product_desc *p, const uint16_t *grad, cons
                            const int32_t *expert_start_loc, const int32_t *num_tokens_per_expert,
                            int accumulate, void *grad_weight, float *grad_bias, void *workspace,
                            void *stream);
+
+/* ---- rows and weights in 8 bits ------------------------------------------- */
+/* A row in 8 bits is C codes (e4m3, OCP "fn") and a scale for each group of
+ * 128 columns, S = ceil(C / 128) of them, the last group perhaps shorter; it
+ * stands for code * scale. The formats of the scales are those of the
+ * dispatch: EPL_SCALE_F32 [rows, S], EPL_SCALE_UE8M0 int32 [ceil(S / 4),
+ * rows] (bytes behind the last group's are written as 0) and
+ * EPL_SCALE_F32_RECT. A weight has one scale for each block of 128 x 128,
+ * [E, ceil(N / 128), ceil(K / 128)] for a weight [E, N, K]: fp32, or one byte
+ * of UE8M0 each.
+ *   fp32:   s = amax / 448, code = e4m3(v * (448 / amax))
+ *   UE8M0:  s = 2^k, the least with amax <= 448 s and k >= -126;
+ *           code = e4m3(v * 2^-k)
+ * in binary32 steps, rounded to nearest even; with fp32 scales those of
+ * epl_ll_dispatch. A group of zeros has scale 0 (UE8M0: 2^-126) and codes 0.
+ * A NaN becomes a NaN code and has no part in amax; an infinity becomes a NaN
+ * code and makes its group's scale infinite (UE8M0: NaN). */
+typedef struct epl_cast_desc {
+    int64_t num_rows;        /* 0 .. INT32_MAX - 1023                             */
+    int32_t num_experts;     /* blocks of rows, 0 .. 2048: 0 = all rows           */
+    int32_t cols;            /* C, 16 .. 2^20, C % 16 == 0                        */
+    int32_t value_type;      /* of the values: EPL_OUT_F32 or EPL_OUT_BF16        */
+    int32_t activation;      /* EPL_ACT_NONE, or (epl_quantize) EPL_ACT_SWIGLU    */
+    int32_t scale_format;    /* EPL_SCALE_F32, _UE8M0 or _F32_RECT                */
+    int32_t rows_per_expert; /* cap of _F32_RECT (num_rows % cap == 0), else 0    */
+    int32_t reserved;        /* must be 0                                         */
+    int32_t reserved2;       /* must be 0                                         */
+} epl_cast_desc;
+
+/* Host-only check of a description. Needs no GPU. */
+int epl_cast_validate(const epl_cast_desc *p);
+
+/* Rows to 8 bits. x [num_rows, C], or with EPL_ACT_SWIGLU [num_rows, 2C] whose
+ * silu(x[:, :C]) * x[:, C:] is cast. With num_experts > 0 only the rows of the
+ * experts' blocks (as in epl_expert_product) are cast and the others' codes
+ * and scales left as they were; without, both block pointers are ignored and
+ * all rows are. x and codes 16-byte aligned, the others 4. */
+int epl_quantize(const epl_cast_desc *p, const void *x, const int32_t *expert_start_loc,
+                 const int32_t *num_tokens_per_expert, uint8_t *codes, void *scale, void *stream);
+
+/* And back: y[p, c] = code * scale, one rounding. */
+int epl_dequantize(const epl_cast_desc *p, const uint8_t *codes, const void *scale,
+                   const int32_t *expert_start_loc, const int32_t *num_tokens_per_expert, void *y,
+                   void *stream);
+
+typedef struct epl_weight_cast_desc {
+    int32_t num_experts;     /* E, 1 <= E <= 2048                                 */
+    int32_t out_cols;        /* N, 1 .. 2^20                                      */
+    int32_t in_cols;         /* K, 16 .. 2^20, K % 16 == 0                        */
+    int32_t value_type;      /* of the weight: EPL_OUT_F32 or EPL_OUT_BF16        */
+    int32_t scale_format;    /* EPL_SCALE_F32 or EPL_SCALE_UE8M0 (bytes)          */
+    int32_t reserved;        /* must be 0                                         */
+} epl_weight_cast_desc;
+
+/* Host-only check of a description. Needs no GPU. */
+int epl_weight_cast_validate(const epl_weight_cast_desc *p);
+
+/* Weights to 8 bits: weight [E, N, K] -> codes [E, N, K] and scale [E,
+ * ceil(N / 128), ceil(K / 128)]. The scales' blocks lie the same way for both
+ * layouts of a product, so one array serves forwards and backwards. weight
+ * and codes 16-byte aligned; at most INT32_MAX blocks. */
+int epl_quantize_weight(const epl_weight_cast_desc *p, const void *weight, uint8_t *codes,
+                        void *scale, void *stream);
+
+typedef struct epl_product_fp8_desc {
+    int64_t num_rows;            /* as in epl_product_desc                        */
+    int64_t expected_rows;       /* as in epl_product_desc                        */
+    int32_t num_experts;         /* E, 1 <= E <= 2048                             */
+    int32_t in_cols;             /* K, 16 .. 2^20, K % 16 == 0                    */
+    int32_t out_cols;            /* N, 16 .. 2^20, N % 16 == 0, K * N <= 2^30     */
+    int32_t weight_layout;       /* EPL_WEIGHT_*                                  */
+    int32_t activation;          /* EPL_ACT_*                                     */
+    int32_t out_type;            /* y: EPL_OUT_F32 or EPL_OUT_BF16                */
+    int32_t scale_format;        /* of x: EPL_SCALE_F32, _UE8M0 or _F32_RECT      */
+    int32_t rows_per_expert;     /* cap of _F32_RECT (num_rows % cap == 0), else 0 */
+    int32_t weight_scale_format; /* EPL_SCALE_F32 or EPL_SCALE_UE8M0 (bytes)      */
+    int32_t codes_scale_format;  /* EPL_SCALE_NONE: the result is not cast;
+                                    EPL_SCALE_F32 or EPL_SCALE_UE8M0: it is, and
+                                    its columns (of the gated gradient those of
+                                    each half) are a multiple of 128              */
+    int32_t reserved;            /* must be 0                                     */
+    int32_t reserved2;           /* must be 0                                     */
+} epl_product_fp8_desc;
+
+/* Host-only check of a product description. Needs no GPU. */
+int epl_product_fp8_validate(const epl_product_fp8_desc *p);
+
+/* Bytes of device workspace of the call below, as epl_product_workspace_bytes. */
+size_t epl_product_fp8_workspace_bytes(const epl_product_fp8_desc *p);
+
+/* epl_expert_product on 8-bit rows and weights:
+ *   z[p, n] = sum over blocks b of 128 of x_scale[p, b] * weight_scale[n / 128, b]
+ *             * (sum over k in b of x[p, k] * weight[e][n, k]) + bias[e, n]
+ *   v[p, :] = act(z[p, :]) + residual[p, :]
+ * x codes [num_rows, K]; weight codes [E, N, K], or [E, K, N] with
+ * EPL_WEIGHT_IN_OUT, and its scales in blocks of that array. y, of out_type,
+ * receives v; codes [num_rows, columns of y] and codes_scale receive its cast
+ * (from the fp32 values): y may be NULL where the result is cast, and codes
+ * and codes_scale are NULL where it is not. Everything else (bias, residual,
+ * pre, the *_GRAD activations, blocks, rows of no expert) is as in
+ * epl_expert_product.
+ * Sums over blocks are kept in fp32; inside a block the 8-bit matrix
+ * instruction adds groups of 8 neighbouring k and drops of each product the
+ * bits below 2^-13 of the largest one's power of two: z is within 7 * 2^-13
+ * of the sum of the products' magnitudes (2^-16 of z for normal data), besides
+ * the fp32 sums. */
+int epl_expert_product_fp8(const epl_product_fp8_desc *p, const uint8_t *x, const void *x_scale,
+                           const uint8_t *weight, const void *weight_scale, const float *bias,
+                           const uint16_t *residual, const int32_t *expert_start_loc,
+                           const int32_t *num_tokens_per_expert, uint16_t *pre, void *y,
+                           uint8_t *codes, void *codes_scale, void *workspace, void *stream);
 
 /* ---- gradient of the combine ---------------------------------------------- */
 /* For y = epl_combine(expert_out, output_index, topk_weights):

@@ -36,6 +36,11 @@ __all__ = [
     "combine_backward", "dispatch_backward", "EPL_SCORE_SOFTMAX", "EPL_SCORE_SIGMOID",
     "EPL_ACT_NONE", "EPL_ACT_SILU", "EPL_ACT_GELU", "EPL_ACT_SWIGLU", "EPL_ACT_SILU_GRAD",
     "EPL_ACT_GELU_GRAD", "EPL_ACT_SWIGLU_GRAD", "EPL_WEIGHT_OUT_IN", "EPL_WEIGHT_IN_OUT",
+    "EPL_SCALE_F32_RECT", "Cast", "WeightCast", "ProductFp8", "epl_cast_validate",
+    "epl_weight_cast_validate", "epl_product_fp8_validate", "epl_product_fp8_workspace_bytes",
+    "epl_quantize", "epl_dequantize", "epl_quantize_weight", "epl_expert_product_fp8", "quantize",
+    "dequantize", "quantize_weight", "expert_product_fp8", "gated_block_fp8",
+    "gated_block_fp8_backward",
 ]
 
 EPL_OK = 0
@@ -48,6 +53,7 @@ EPL_OUT_BF16 = 1
 EPL_SCALE_NONE = 0
 EPL_SCALE_F32 = 1
 EPL_SCALE_UE8M0 = 2
+EPL_SCALE_F32_RECT = 3
 EPL_STATIC_WORKSPACE_BYTES = 8 << 20
 EPL_SCORE_SOFTMAX = 0
 EPL_SCORE_SIGMOID = 1
@@ -70,6 +76,9 @@ C_ENTRY_POINTS = (
     "epl_router_validate", "epl_route", "epl_route_backward", "epl_product_validate",
     "epl_expert_product", "epl_expert_weight_grad", "epl_combine_backward",
     "epl_product_workspace_bytes", "epl_weight_grad_workspace_bytes",
+    "epl_cast_validate", "epl_quantize", "epl_dequantize", "epl_weight_cast_validate",
+    "epl_quantize_weight", "epl_product_fp8_validate", "epl_product_fp8_workspace_bytes",
+    "epl_expert_product_fp8",
 )
 
 
@@ -147,6 +156,57 @@ class Product(ctypes.Structure):
         ("activation", ctypes.c_int32),
         ("out_type", ctypes.c_int32),
         ("reserved", ctypes.c_int32),
+    ]
+
+
+class Cast(ctypes.Structure):
+    """epl_cast_desc: sizes and formats of a cast of rows (see include/epl.h)."""
+
+    _fields_ = [
+        ("num_rows", ctypes.c_int64),
+        ("num_experts", ctypes.c_int32),
+        ("cols", ctypes.c_int32),
+        ("value_type", ctypes.c_int32),
+        ("activation", ctypes.c_int32),
+        ("scale_format", ctypes.c_int32),
+        ("rows_per_expert", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("reserved2", ctypes.c_int32),
+    ]
+
+
+class WeightCast(ctypes.Structure):
+    """epl_weight_cast_desc: sizes of a cast of weights (see include/epl.h)."""
+
+    _fields_ = [
+        ("num_experts", ctypes.c_int32),
+        ("out_cols", ctypes.c_int32),
+        ("in_cols", ctypes.c_int32),
+        ("value_type", ctypes.c_int32),
+        ("scale_format", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class ProductFp8(ctypes.Structure):
+    """epl_product_fp8_desc: sizes, formats and epilogue of an experts'
+    product on 8-bit rows (see include/epl.h)."""
+
+    _fields_ = [
+        ("num_rows", ctypes.c_int64),
+        ("expected_rows", ctypes.c_int64),
+        ("num_experts", ctypes.c_int32),
+        ("in_cols", ctypes.c_int32),
+        ("out_cols", ctypes.c_int32),
+        ("weight_layout", ctypes.c_int32),
+        ("activation", ctypes.c_int32),
+        ("out_type", ctypes.c_int32),
+        ("scale_format", ctypes.c_int32),
+        ("rows_per_expert", ctypes.c_int32),
+        ("weight_scale_format", ctypes.c_int32),
+        ("codes_scale_format", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("reserved2", ctypes.c_int32),
     ]
 
 
@@ -234,6 +294,20 @@ def load() -> ctypes.CDLL:
     for name in ("epl_product_workspace_bytes", "epl_weight_grad_workspace_bytes"):
         getattr(lib, name).argtypes = [pp]
         getattr(lib, name).restype = ctypes.c_size_t
+    pc, pw, p8 = ctypes.POINTER(Cast), ctypes.POINTER(WeightCast), ctypes.POINTER(ProductFp8)
+    for name, kind in (("epl_cast_validate", pc), ("epl_weight_cast_validate", pw),
+                       ("epl_product_fp8_validate", p8)):
+        getattr(lib, name).argtypes = [kind]
+        getattr(lib, name).restype = i32
+    for name in ("epl_quantize", "epl_dequantize"):
+        getattr(lib, name).argtypes = [pc, _P, _P, _P, _P, _P, _P]
+        getattr(lib, name).restype = i32
+    lib.epl_quantize_weight.argtypes = [pw, _P, _P, _P, _P]
+    lib.epl_quantize_weight.restype = i32
+    lib.epl_product_fp8_workspace_bytes.argtypes = [p8]
+    lib.epl_product_fp8_workspace_bytes.restype = ctypes.c_size_t
+    lib.epl_expert_product_fp8.argtypes = [p8, *[_P] * 14]
+    lib.epl_expert_product_fp8.restype = i32
     lib.epl_combine_backward.argtypes = [_PP, i32, _P, _P, i64, _P, _P, _P, _P, _P, _P]
     lib.epl_combine_backward.restype = i32
     lib.epl_status.argtypes = [_P, _P]
@@ -801,6 +875,127 @@ def epl_expert_weight_grad(p: Product, grad, x, expert_start_loc, num_tokens_per
             _ptr(grad_weight), _ptr(grad_bias), _ptr(workspace))
 
 
+def epl_cast_validate(p: Cast) -> int:
+    return load().epl_cast_validate(ctypes.byref(p))
+
+
+def epl_weight_cast_validate(p: WeightCast) -> int:
+    return load().epl_weight_cast_validate(ctypes.byref(p))
+
+
+def epl_product_fp8_validate(p: ProductFp8) -> int:
+    return load().epl_product_fp8_validate(ctypes.byref(p))
+
+
+def epl_product_fp8_workspace_bytes(p: ProductFp8) -> int:
+    return int(load().epl_product_fp8_workspace_bytes(ctypes.byref(p)))
+
+
+def _groups(cols: int) -> int:
+    return (cols + 127) // 128
+
+
+def _need_row_scales(t, name, fmt, rows, groups, cap, dev):
+    """Scales of 8-bit rows in one of the EPL_SCALE_* formats."""
+    torch = _torch()
+    if fmt == EPL_SCALE_UE8M0:
+        _need_same(t, name, torch.int32, ((groups + 3) // 4, rows), dev)
+    elif fmt == EPL_SCALE_F32_RECT:
+        _need_same(t, name, torch.float32, (rows // max(cap, 1), groups, cap), dev)
+    else:
+        _need_same(t, name, torch.float32, (rows, groups), dev)
+
+
+def _need_weight_scales(t, fmt, E, rows, cols, dev):
+    _need_same(t, "weight_scale",
+               _torch().uint8 if fmt == EPL_SCALE_UE8M0 else _torch().float32,
+               (E, _groups(rows), _groups(cols)), dev)
+
+
+def _cast_args(p: Cast, values, value_cols, codes, scale, expert_start_loc,
+               num_tokens_per_expert, where):
+    """The checks that both directions of a cast share; the device."""
+    torch = _torch()
+    _check(epl_cast_validate(p), where)
+    rows, C = p.num_rows, p.cols
+    dev = getattr(values, "device", None)
+    _need_same(values, "values", torch.bfloat16 if p.value_type == EPL_OUT_BF16 else torch.float32,
+               (rows, value_cols), dev)
+    _need_same(codes, "codes", torch.uint8, (rows, C), dev)
+    _need_row_scales(scale, "scale", p.scale_format, rows, _groups(C), p.rows_per_expert, dev)
+    if p.num_experts:
+        _blocks(p, expert_start_loc, num_tokens_per_expert, dev)
+    elif expert_start_loc is not None or num_tokens_per_expert is not None:
+        raise ValueError("blocks given but the cast has num_experts == 0")
+    return dev
+
+
+def epl_quantize(p: Cast, x, expert_start_loc, num_tokens_per_expert, codes, scale, stream=None):
+    dev = _cast_args(p, x, p.cols * (2 if p.activation == EPL_ACT_SWIGLU else 1), codes, scale,
+                     expert_start_loc, num_tokens_per_expert, "epl_quantize")
+    _launch("epl_quantize", dev, stream, ctypes.byref(p), _ptr(x), _ptr(expert_start_loc),
+            _ptr(num_tokens_per_expert), _ptr(codes), _ptr(scale))
+
+
+def epl_dequantize(p: Cast, codes, scale, expert_start_loc, num_tokens_per_expert, y, stream=None):
+    dev = _cast_args(p, y, p.cols, codes, scale, expert_start_loc, num_tokens_per_expert,
+                     "epl_dequantize")
+    _launch("epl_dequantize", dev, stream, ctypes.byref(p), _ptr(codes), _ptr(scale),
+            _ptr(expert_start_loc), _ptr(num_tokens_per_expert), _ptr(y))
+
+
+def epl_quantize_weight(p: WeightCast, weight, codes, scale, stream=None):
+    torch = _torch()
+    _check(epl_weight_cast_validate(p), "epl_quantize_weight")
+    E, N, K = p.num_experts, p.out_cols, p.in_cols
+    dev = getattr(weight, "device", None)
+    _need_same(weight, "weight", torch.bfloat16 if p.value_type == EPL_OUT_BF16 else torch.float32,
+               (E, N, K), dev)
+    _need_same(codes, "codes", torch.uint8, (E, N, K), dev)
+    _need_weight_scales(scale, p.scale_format, E, N, K, dev)
+    _launch("epl_quantize_weight", dev, stream, ctypes.byref(p), _ptr(weight), _ptr(codes),
+            _ptr(scale))
+
+
+def epl_expert_product_fp8(p: ProductFp8, x, x_scale, weight, weight_scale, bias, residual,
+                           expert_start_loc, num_tokens_per_expert, pre, y, codes=None,
+                           codes_scale=None, workspace=None, stream=None):
+    torch = _torch()
+    rows, E, K, N = p.num_rows, p.num_experts, p.in_cols, p.out_cols
+    bf16, u8 = torch.bfloat16, torch.uint8
+    dev = getattr(x, "device", None)
+    _need_same(x, "x", u8, (rows, K), dev)
+    _need_row_scales(x_scale, "x_scale", p.scale_format, rows, _groups(K), p.rows_per_expert, dev)
+    shape = (E, K, N) if p.weight_layout == EPL_WEIGHT_IN_OUT else (E, N, K)
+    _need_same(weight, "weight", u8, shape, dev)
+    _need_weight_scales(weight_scale, p.weight_scale_format, *shape, dev)
+    if bias is not None:
+        _need_same(bias, "bias", torch.float32, (E, N), dev)
+    grad = p.activation >= EPL_ACT_SILU_GRAD
+    cols = N // 2 if p.activation == EPL_ACT_SWIGLU else \
+        2 * N if p.activation == EPL_ACT_SWIGLU_GRAD else N
+    if residual is not None:
+        _need_same(residual, "residual", bf16, (rows, cols), dev)
+    if pre is not None or grad:
+        _need_same(pre, "pre", bf16, (rows, cols if grad else N), dev)
+    if y is not None or p.codes_scale_format == EPL_SCALE_NONE:
+        _need_same(y, "y", bf16 if p.out_type == EPL_OUT_BF16 else torch.float32, (rows, cols), dev)
+    if p.codes_scale_format != EPL_SCALE_NONE:
+        _need_same(codes, "codes", u8, (rows, cols), dev)
+        _need_row_scales(codes_scale, "codes_scale", p.codes_scale_format, rows, _groups(cols), 0,
+                         dev)
+    elif codes is not None or codes_scale is not None:
+        raise ValueError("codes given but the product has codes_scale_format == EPL_SCALE_NONE")
+    _blocks(p, expert_start_loc, num_tokens_per_expert, dev)
+    if workspace is not None:
+        _need_split_ws(workspace, dev, epl_product_fp8_workspace_bytes(p),
+                       "epl_expert_product_fp8")
+    _launch("epl_expert_product_fp8", dev, stream, ctypes.byref(p), _ptr(x), _ptr(x_scale),
+            _ptr(weight), _ptr(weight_scale), _ptr(bias), _ptr(residual), _ptr(expert_start_loc),
+            _ptr(num_tokens_per_expert), _ptr(pre), _ptr(y), _ptr(codes), _ptr(codes_scale),
+            _ptr(workspace))
+
+
 def epl_combine_backward(p: Problem, grad_y, expert_out, expert_rows, output_index, topk_weights,
                          grad_rows, grad_weights, workspace=None, stream=None):
     torch = _torch()
@@ -1156,6 +1351,255 @@ def expert_weight_grad(grad, x, expert_start_loc, num_tokens_per_expert, out=Non
     epl_expert_weight_grad(p, grad, x, expert_start_loc, num_tokens_per_expert, accumulate, out,
                            bias_grad, workspace)
     return out
+
+
+@functools.lru_cache(maxsize=256)
+def _cast_for(*fields) -> Cast:
+    p = Cast(*fields, 0, 0)
+    _check(epl_cast_validate(p), "epl_cast_validate")
+    return p
+
+
+@functools.lru_cache(maxsize=256)
+def _weight_cast_for(*fields) -> WeightCast:
+    p = WeightCast(*fields, 0)
+    _check(epl_weight_cast_validate(p), "epl_weight_cast_validate")
+    return p
+
+
+@functools.lru_cache(maxsize=256)
+def _product_fp8_for(*fields):
+    """A checked description and its workspace's bytes."""
+    p = ProductFp8(*fields, 0, 0)
+    _check(epl_product_fp8_validate(p), "epl_product_fp8_validate")
+    return p, epl_product_fp8_workspace_bytes(p)
+
+
+_FORMATS = {"f32": EPL_SCALE_F32, "ue8m0": EPL_SCALE_UE8M0}
+
+
+def _scale_kind(scale, rows: int, name: str):
+    """(format, rows per expert) of row scales, by their type and shape."""
+    torch = _torch()
+    if not isinstance(scale, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if scale.dtype == torch.int32:
+        return EPL_SCALE_UE8M0, 0
+    if scale.dtype != torch.float32:
+        raise TypeError(f"{name} must be torch.float32 or torch.int32, got {scale.dtype}")
+    if scale.dim() == 3:
+        return EPL_SCALE_F32_RECT, scale.shape[2]
+    return EPL_SCALE_F32, 0
+
+
+def _row_scales(fmt: int, rows: int, cols: int, device):
+    """A buffer for the scales of `rows` rows."""
+    torch = _torch()
+    S = _groups(cols)
+    if fmt == EPL_SCALE_UE8M0:
+        return torch.empty((S + 3) // 4, rows, dtype=torch.int32, device=device)
+    return torch.empty(rows, S, dtype=torch.float32, device=device)
+
+
+def _num_blocks(expert_start_loc, num_tokens_per_expert) -> int:
+    if expert_start_loc is None and num_tokens_per_expert is None:
+        return 0
+    _matrix(expert_start_loc, "expert_start_loc", 1)
+    if expert_start_loc.shape[0] == 0:
+        raise ValueError("expert_start_loc is empty")
+    return expert_start_loc.shape[0]
+
+
+def quantize(x, activation: str = "none", scale_format: str = "f32", expert_start_loc=None,
+             num_tokens_per_expert=None, out=None, out_scale=None, stream=None):
+    """(codes uint8 [rows, C], scales) of rows x [rows, C] (bf16 or fp32), a
+    scale for each 128 columns, as epl_quantize in include/epl.h: what
+    epl_dispatch_fp8 and expert_product_fp8 take. activation="swiglu" casts
+    silu(x[:, :C]) * x[:, C:] of x [rows, 2C]. scale_format "f32": fp32 [rows,
+    C / 128]; "ue8m0": powers of two, int32 [C / 512, rows]. With the experts'
+    blocks only their rows are cast: pass `out` and `out_scale` to choose what
+    the others hold."""
+    torch = _torch()
+    _matrix(x, "x", 2)
+    if stream is not None and x.is_cuda:
+        return _run_on(stream, x.device, quantize, x, activation, scale_format, expert_start_loc,
+                       num_tokens_per_expert, out, out_scale)
+    act = _named({k: _ACTIVATIONS[k] for k in ("none", "swiglu")}, activation, "activation")
+    rows, C = x.shape
+    if act == EPL_ACT_SWIGLU:
+        if C % 2:
+            raise ValueError(f"x must have an even number of columns, got {C}")
+        C //= 2
+    if out_scale is not None:
+        fmt, cap = _scale_kind(out_scale, rows, "out_scale")
+    else:
+        fmt, cap = _named(_FORMATS, scale_format, "scale format"), 0
+    p = _cast_for(rows, _num_blocks(expert_start_loc, num_tokens_per_expert), C,
+                  _type_code(x.dtype, "x"), act, fmt, cap)
+    if out is None:
+        out = torch.empty(rows, C, dtype=torch.uint8, device=x.device)
+    if out_scale is None:
+        out_scale = _row_scales(fmt, rows, C, x.device)
+    epl_quantize(p, x, expert_start_loc, num_tokens_per_expert, out, out_scale)
+    return out, out_scale
+
+
+def dequantize(codes, scale, expert_start_loc=None, num_tokens_per_expert=None, out=None,
+               out_dtype=None, stream=None):
+    """code * scale, bf16 or fp32 [rows, C], of 8-bit rows: codes uint8 [rows,
+    C] with scales of any format of the dispatch (fp32 [rows, C / 128], int32
+    [C / 512, rows], or the low-latency rectangle's fp32 [E, C / 128, cap] with
+    rows = E cap). With the experts' blocks only their rows are written: pass
+    `out` to choose what the others hold."""
+    torch = _torch()
+    _matrix(codes, "codes", 2)
+    if stream is not None and codes.is_cuda:
+        return _run_on(stream, codes.device, dequantize, codes, scale, expert_start_loc,
+                       num_tokens_per_expert, out, out_dtype)
+    rows, C = codes.shape
+    if out is not None:
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise ValueError(f"out is {out.dtype}, out_dtype {out_dtype}")
+    else:
+        out = torch.empty(rows, C, dtype=torch.bfloat16 if out_dtype is None else out_dtype,
+                          device=codes.device)
+    fmt, cap = _scale_kind(scale, rows, "scale")
+    p = _cast_for(rows, _num_blocks(expert_start_loc, num_tokens_per_expert), C,
+                  _type_code(out.dtype, "out"), EPL_ACT_NONE, fmt, cap)
+    epl_dequantize(p, codes, scale, expert_start_loc, num_tokens_per_expert, out)
+    return out
+
+
+def quantize_weight(weight, scale_format: str = "f32", out=None, out_scale=None, stream=None):
+    """(codes uint8 [E, N, K], scales [E, N / 128, K / 128]) of weights [E, N,
+    K] (bf16 or fp32), a scale for each 128 x 128 block: fp32, or with "ue8m0"
+    powers of two as uint8 exponents."""
+    torch = _torch()
+    _matrix(weight, "weight", 3)
+    if stream is not None and weight.is_cuda:
+        return _run_on(stream, weight.device, quantize_weight, weight, scale_format, out, out_scale)
+    E, N, K = weight.shape
+    fmt = _named(_FORMATS, scale_format, "scale format")
+    if out_scale is not None:
+        fmt = EPL_SCALE_UE8M0 if out_scale.dtype == torch.uint8 else EPL_SCALE_F32
+    p = _weight_cast_for(E, N, K, _type_code(weight.dtype, "weight"), fmt)
+    if out is None:
+        out = torch.empty(E, N, K, dtype=torch.uint8, device=weight.device)
+    if out_scale is None:
+        out_scale = torch.empty(E, _groups(N), _groups(K), device=weight.device,
+                                dtype=torch.uint8 if fmt == EPL_SCALE_UE8M0 else torch.float32)
+    epl_quantize_weight(p, weight, out, out_scale)
+    return out, out_scale
+
+
+def expert_product_fp8(x, x_scale, weight, weight_scale, expert_start_loc, num_tokens_per_expert,
+                       bias=None, activation: str = "none", residual=None, pre=None, out=None,
+                       out_dtype=None, quantized=None, transposed: bool = False,
+                       expected_rows: int = 0, workspace=None, stream=None):
+    """expert_product on 8-bit rows and weights, as epl_expert_product_fp8 in
+    include/epl.h: x codes uint8 [rows, K] with x_scale of any format of the
+    dispatch (see `dequantize`), weight codes uint8 [E, N, K] ([E, K, N] with
+    transposed=True) with weight_scale as `quantize_weight` makes them.
+
+    `quantized` asks for the result's cast: "f32" or "ue8m0", or the buffers
+    (codes, scales) that receive it. Returns the result (bf16, or `out_dtype`);
+    with `quantized` (codes, scales) alone, or (out, codes, scales) where `out`
+    or `out_dtype` asks for both."""
+    torch = _torch()
+    _matrix(x, "x", 2)
+    _matrix(weight, "weight", 3)
+    if stream is not None and x.is_cuda:
+        return _run_on(stream, x.device, expert_product_fp8, x, x_scale, weight, weight_scale,
+                       expert_start_loc, num_tokens_per_expert, bias, activation, residual, pre,
+                       out, out_dtype, quantized, transposed, expected_rows, workspace)
+    E, rows = weight.shape[0], x.shape[0]
+    N = weight.shape[2] if transposed else weight.shape[1]
+    act = _named(_ACTIVATIONS, activation, "activation")
+    cols = N // 2 if act == EPL_ACT_SWIGLU else 2 * N if act == EPL_ACT_SWIGLU_GRAD else N
+    if out is not None:
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise ValueError(f"out is {out.dtype}, out_dtype {out_dtype}")
+        out_dtype = out.dtype
+    elif out_dtype is None:
+        if quantized is None:
+            out_dtype = torch.bfloat16
+    codes = codes_scale = None
+    to = EPL_SCALE_NONE
+    if isinstance(quantized, tuple):
+        codes, codes_scale = quantized
+        to, cap = _scale_kind(codes_scale, rows, "quantized scales")
+        if to == EPL_SCALE_F32_RECT:
+            raise ValueError("quantized scales must be fp32 [rows, groups] or int32")
+    elif quantized is not None:
+        to = _named(_FORMATS, quantized, "scale format")
+    fmt, cap = _scale_kind(x_scale, rows, "x_scale")
+    w_fmt = EPL_SCALE_UE8M0 if getattr(weight_scale, "dtype", None) == torch.uint8 else EPL_SCALE_F32
+    p, ws_bytes = _product_fp8_for(
+        rows, int(expected_rows), E, x.shape[1], N,
+        EPL_WEIGHT_IN_OUT if transposed else EPL_WEIGHT_OUT_IN, act,
+        EPL_OUT_BF16 if out_dtype is None else _type_code(out_dtype, "out"), fmt, cap, w_fmt, to)
+    if out is None and out_dtype is not None:
+        out = torch.empty(rows, cols, dtype=out_dtype, device=x.device)
+    if to != EPL_SCALE_NONE and codes is None:
+        codes = torch.empty(rows, cols, dtype=torch.uint8, device=x.device)
+        codes_scale = _row_scales(to, rows, cols, x.device)
+    if workspace is None and x.is_cuda:
+        workspace = _split_ws(ws_bytes, x.device)
+    epl_expert_product_fp8(p, x, x_scale, weight, weight_scale, bias, residual, expert_start_loc,
+                           num_tokens_per_expert, pre, out, codes, codes_scale, workspace)
+    if codes is None:
+        return out
+    return (codes, codes_scale) if out is None else (out, codes, codes_scale)
+
+
+def gated_block_fp8(x, x_scale, w1, w1_scale, w2, w2_scale, expert_start_loc,
+                    num_tokens_per_expert, pre=None, out=None, expected_rows: int = 0,
+                    scale_format: str = "f32", stream=None):
+    """The experts' gated feed-forward block on 8-bit rows: h = silu(x W1g^T)
+    * (x W1u^T) and its cast in one product (w1 [E, 2F, H], gate rows first),
+    then h W2^T (w2 [E, H, F]), bf16 [rows, H]. F is a multiple of 128. x,
+    weights and their scales are as expert_product_fp8 takes them; h is cast
+    with `scale_format` scales. `pre` (bf16 [rows, 2F]) receives x W1^T for
+    gated_block_fp8_backward. Rows outside the experts' blocks are not
+    written."""
+    _matrix(x, "x", 2)
+    if stream is not None and x.is_cuda:
+        return _run_on(stream, x.device, gated_block_fp8, x, x_scale, w1, w1_scale, w2, w2_scale,
+                       expert_start_loc, num_tokens_per_expert, pre, out, expected_rows,
+                       scale_format)
+    h, h_scale = expert_product_fp8(x, x_scale, w1, w1_scale, expert_start_loc,
+                                    num_tokens_per_expert, activation="swiglu", pre=pre,
+                                    quantized=scale_format, expected_rows=expected_rows)
+    return expert_product_fp8(h, h_scale, w2, w2_scale, expert_start_loc, num_tokens_per_expert,
+                              out=out, expected_rows=expected_rows)
+
+
+def gated_block_fp8_backward(grad_y, pre, w1, w1_scale, w2, w2_scale, expert_start_loc,
+                             num_tokens_per_expert, grad_x=None, grad_pre=None,
+                             expected_rows: int = 0, scale_format: str = "f32", stream=None):
+    """Gradients of gated_block_fp8: (grad_x bf16 [rows, H], grad_pre bf16
+    [rows, 2F]) from grad_y (bf16 or fp32 [rows, H], e.g. of combine_backward) and the
+    `pre` it kept. grad_y is cast to 8 bits for the product with W2, and
+    grad_pre, whose cast leaves that product's epilogue too, for the one with
+    W1; expert_weight_grad takes grad_y and grad_pre as they are. Casts pass
+    gradients through. Rows outside the experts' blocks are not written."""
+    torch = _torch()
+    _matrix(grad_y, "grad_y", 2)
+    _matrix(w2, "w2", 3)
+    if stream is not None and grad_y.is_cuda:
+        return _run_on(stream, grad_y.device, gated_block_fp8_backward, grad_y, pre, w1, w1_scale,
+                       w2, w2_scale, expert_start_loc, num_tokens_per_expert, grad_x, grad_pre,
+                       expected_rows, scale_format)
+    dy, dy_scale = quantize(grad_y, scale_format=scale_format, expert_start_loc=expert_start_loc,
+                            num_tokens_per_expert=num_tokens_per_expert)
+    grad_pre, dz, dz_scale = expert_product_fp8(
+        dy, dy_scale, w2, w2_scale, expert_start_loc, num_tokens_per_expert,
+        activation="swiglu_grad", pre=pre, out=grad_pre, out_dtype=torch.bfloat16,
+        quantized=scale_format, transposed=True, expected_rows=expected_rows)
+    grad_x = expert_product_fp8(dz, dz_scale, w1, w1_scale, expert_start_loc,
+                                num_tokens_per_expert, out=grad_x, transposed=True,
+                                expected_rows=expected_rows)
+    return grad_x, grad_pre
 
 
 def combine_backward(grad_y, expert_out, output_index, topk_weights, grad_rows=None,

@@ -14,10 +14,14 @@ ROOT = os.path.dirname(PKG)
 INCLUDE = os.path.join(ROOT, "include")
 CSRC = os.path.join(PKG, "csrc")
 SOURCES = [os.path.join(CSRC, name) for name in
-           ("epl.hip", "epl_router.hip", "epl_product.hip", "epl_combine_backward.hip")]
+           ("epl.hip", "epl_router.hip", "epl_product.hip", "epl_combine_backward.hip",
+            "epl_cast.hip", "epl_product_fp8.hip")]
 DEPENDS = SOURCES + [os.path.join(CSRC, "epl_kernels.h"),
                      os.path.join(CSRC, "epl_router_kernels.h"),
-                     os.path.join(CSRC, "epl_product_kernels.h"), os.path.join(INCLUDE, "epl.h")]
+                     os.path.join(CSRC, "epl_product_kernels.h"),
+                     os.path.join(CSRC, "epl_cast_kernels.h"),
+                     os.path.join(CSRC, "epl_product_fp8_kernels.h"),
+                     os.path.join(INCLUDE, "epl.h")]
 LIB = os.path.join(PKG, "libepl.so")
 ARCH = "gfx950"
 

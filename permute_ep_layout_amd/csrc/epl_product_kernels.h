@@ -1,6 +1,6 @@
 // Device kernels of the experts' matrix products for gfx950 (CDNA4): the
-// product of each expert's block of rows with that expert's weight, its
-// gradients, and the column sums of the bias gradient.
+// product of each expert's block of rows with that expert's weight, and its
+// gradients.
 //
 // All of them are one contraction per expert,
 //     out[m, n] = sum_k P[m, k] * Q[n, k],   n contiguous in memory,
@@ -77,7 +77,8 @@ __device__ __forceinline__ void each(F &&f)
 }
 
 // An expert's block, cut to the buffer: [lo, lo + n).
-__device__ __forceinline__ int block_of(const Args &a, int e, int64_t &lo)
+template <typename A>
+__device__ __forceinline__ int block_of(const A &a, int e, int64_t &lo)
 {
     const int64_t s = a.start[e], c = a.count[e];
     lo = s < 0 ? 0 : s > a.rows ? a.rows : s;
@@ -415,17 +416,18 @@ enum Form { kForward, kDataGrad, kWeightGrad };
 
 // The m tiles of the experts before each expert, and of all of them: never
 // more than blocks apart from each other have, so that no sum overflows where
-// bad ones share rows.
-template <int BM, int THREADS>
-__device__ __forceinline__ void tile_prefix(const Args &a, int32_t *pre, int32_t *sums)
+// bad ones share rows. rows_of(e, first row) is an expert's number of rows.
+template <int BM, int THREADS, typename F>
+__device__ __forceinline__ void tile_prefix(int E, int64_t rows, F &&rows_of, int32_t *pre,
+                                            int32_t *sums)
 {
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-    const int most = (int)(a.rows / BM) + a.E;
+    const int most = (int)(rows / BM) + E;
     int base = 0;
-    for (int e0 = 0; e0 < a.E; e0 += THREADS) {
+    for (int e0 = 0; e0 < E; e0 += THREADS) {
         const int e = e0 + t;
         int64_t lo;
-        const int own = e < a.E ? (block_of(a, e, lo) + BM - 1) / BM : 0;
+        const int own = e < E ? (rows_of(e, lo) + BM - 1) / BM : 0;
         int up = own;
         for (int d = 1; d < 64; d <<= 1) {
             const int v = __shfl_up(up, d);
@@ -439,13 +441,33 @@ __device__ __forceinline__ void tile_prefix(const Args &a, int32_t *pre, int32_t
             before = min(before + (w < wave ? sums[w] : 0), most);
             base = min(base + sums[w], most);
         }
-        if (e < a.E)
+        if (e < E)
             pre[e] = min(before + up - own, most);
         __syncthreads();
     }
     if (t == 0)
-        pre[a.E] = base;
+        pre[E] = base;
     __syncthreads();
+}
+template <int BM, int THREADS>
+__device__ __forceinline__ void tile_prefix(const Args &a, int32_t *pre, int32_t *sums)
+{
+    tile_prefix<BM, THREADS>(
+        a.E, a.rows, [&](int e, int64_t &lo) { return block_of(a, e, lo); }, pre, sums);
+}
+
+// The last expert with pre[e] <= m tile `t`, the same for a whole wave.
+__device__ __forceinline__ int expert_of_tile(const int32_t *pre, int E, int t)
+{
+    int l = 0, h = E;
+    while (h - l > 1) {
+        const int mid = (l + h) >> 1;
+        if (pre[mid] <= t)
+            l = mid;
+        else
+            h = mid;
+    }
+    return __builtin_amdgcn_readfirstlane(l);
 }
 
 // Into how many parts to split the contraction of the `left` tiles of a round
@@ -1045,46 +1067,6 @@ __global__ __launch_bounds__(WAVES * 64, WAVES == 4 ? 2 : 4) void few_rows_kerne
             few_rows<WAVES, 1>(a, e, lo + m, cnt - m, nb, red);
         else
             few_rows<WAVES, 2>(a, e, lo + m, cnt - m, nb, red);
-    }
-}
-
-// --------------------------------------------------------- bias gradient --
-//
-// db[e, n] = sum over the expert's rows of d[p, n], in binary32. A workgroup
-// takes 64 columns (8 lanes of 8) of one expert; its 32 row lanes add rows
-// 32 apart and are added in order through LDS. 12288 rows over 64 experts, 2048
-// columns: 10 us. Rows are not shared over workgroups, so that one expert of
-// 16384 rows and 64 columns takes 142 us, four times its weight gradient.
-
-constexpr int kBiasThreads = 256;
-
-__global__ __launch_bounds__(kBiasThreads) void bias_grad_kernel(Args a, float *db)
-{
-    __shared__ float red[32][65];
-    const int e = blockIdx.y, tid = threadIdx.x, c = tid & 7, y = tid >> 3;
-    const int n = blockIdx.x * 64 + c * 8;
-    int64_t lo;
-    const int cnt = block_of(a, e, lo);
-    float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (n < a.N) {
-        for (int m = y; m < cnt; m += 32) {
-            float v[8];
-            load_bf16<8>(a.p + (lo + m) * a.N + n, v);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                s[i] += v[i];
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        red[y][c * 8 + i] = s[i];
-    __syncthreads();
-    if (tid < 64 && (int)blockIdx.x * 64 + tid < a.N) {
-        float t = 0;
-        for (int i = 0; i < 32; ++i)
-            t += red[i][tid];
-        float *out = db + (int64_t)e * a.N + blockIdx.x * 64 + tid;
-        *out = a.accumulate ? *out + t : t;
     }
 }
 
