@@ -19,6 +19,7 @@ SOURCES = [os.path.join(CSRC, name) for name in
 DEPENDS = SOURCES + [os.path.join(CSRC, "epl_kernels.h"),
                      os.path.join(CSRC, "epl_router_kernels.h"),
                      os.path.join(CSRC, "epl_product_kernels.h"),
+                     os.path.join(CSRC, "epl_product_host.h"),
                      os.path.join(CSRC, "epl_cast_kernels.h"),
                      os.path.join(CSRC, "epl_product_fp8_kernels.h"),
                      os.path.join(INCLUDE, "epl.h")]

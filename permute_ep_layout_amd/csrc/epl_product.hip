@@ -6,6 +6,7 @@
 #include <cstdint>
 
 #include "epl.h"
+#include "epl_product_host.h"
 #include "epl_product_kernels.h"
 
 namespace epl_product {
@@ -55,27 +56,15 @@ __global__ __launch_bounds__(kBiasThreads) void bias_grad_kernel(Args a, float *
 namespace {
 
 namespace P = epl_product;
+namespace H = epl_product_host;
 
-bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-int launch_status() { return hipGetLastError() == hipSuccess ? EPL_OK : EPL_EHIP; }
+using namespace H;
 
 // Rows an expert, on average, up to which the weights are read straight from
 // memory.
 constexpr int64_t kFewRows = 12;
 
-// Offsets within one expert's weight and within a tile are 32-bit.
-constexpr int32_t kMaxCols = 1 << 20;
-constexpr int64_t kMaxWeight = int64_t(1) << 29;
-
-// The kernels step through an expert's rows in 32-bit counts, by up to a tile
-// and the four rows read ahead of it.
-constexpr int64_t kMaxRows = INT32_MAX - 1023;
-
-bool is_grad(int act)
-{
-    return act == EPL_ACT_SILU_GRAD || act == EPL_ACT_GELU_GRAD || act == EPL_ACT_SWIGLU_GRAD;
-}
+constexpr int64_t kMaxWeight = int64_t(1) << 29;     // elements of an expert's
 
 bool desc_ok(const epl_product_desc *p)
 {
@@ -99,53 +88,19 @@ bool desc_ok(const epl_product_desc *p)
     return p->weight_layout == EPL_WEIGHT_OUT_IN || p->weight_layout == EPL_WEIGHT_IN_OUT;
 }
 
-// CUs that a launch counts on, at most (and those of an MI355X).
-constexpr int kCus = 256;
-
-int num_cus()
-{
-    int dev = 0, n = 0;
-    if (hipGetDevice(&dev) != hipSuccess ||
-        hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n < 1) {
-        (void)hipGetLastError();
-        return kCus;
-    }
-    return std::min(n, kCus);
-}
-
-// The kernel that a product takes: straight from memory for a few rows, or
-// tiles of 256 x 256 or 128 x 128. The counts are on the GPU, so the choice
-// goes by the rows that the caller expects an expert to have on average, however
-// unevenly they fall.
-enum Kind { kFew, kLarge, kSmall };
-
-int side_of(Kind k) { return k == kSmall ? 128 : 256; }
-
-// Parts that a contraction of `depth` is split into at most: of four stages
-// each at least.
-int max_parts(int64_t depth)
-{
-    return (int)std::min<int64_t>(P::kMaxParts, depth / (4 * P::kTileK));
-}
-
-int stages_of(int64_t depth) { return (int)((depth + P::kTileK - 1) / P::kTileK); }
-
-// About how long (us) `experts` products of m x n outputs, `depth` deep, take
-// with tiles of one kind. A round of large tiles takes 13 us and 1.55 a stage,
-// one of as many small ones as the GPU holds (half their outputs) 7 and 1.1:
-// large tiles read the operands half as often, small ones leave less idle
+// The costs of the bf16 tiles: a round of large tiles takes 13 us and 1.55 a
+// stage, one of as many small ones as the GPU holds (half their outputs) 7 and
+// 1.1: large tiles read the operands half as often, small ones leave less idle
 // where the last round is not full.
+constexpr Cost cost_of(Kind k) { return k == kLarge ? Cost{13.0, 1.55} : Cost{7.0, 1.1}; }
+
+int max_parts(int64_t depth) { return H::max_parts(depth, P::kTileK); }
+
+int stages_of(int64_t depth) { return H::stages_of(depth, P::kTileK); }
+
 double tiles_time(Kind k, int64_t m, int64_t n, int64_t experts, int64_t depth)
 {
-    const int side = side_of(k), round = kCus * P::tile_groups(side), stages = stages_of(depth);
-    const double start = k == kLarge ? 13.0 : 7.0, stage = k == kLarge ? 1.55 : 1.1;
-    const int64_t tiles = experts * ((m + side - 1) / side) * ((n + side - 1) / side);
-    const int left = (int)(tiles % round);
-    const int parts = P::parts_of(left, round, max_parts(depth), stages, side);
-    double t = (double)(tiles / round) * (start + stage * stages);
-    if (left > 0)
-        t += start + stage * stages / parts + (parts > 1 ? left * parts * stage / (k == kLarge ? 17 : 42) : 0.0);
-    return t;
+    return H::tiles_time(k, m, n, experts, depth, P::kTileK, cost_of(k));
 }
 
 // The faster kind by that. Measured (large, small), us: 8 experts of 4096
@@ -187,27 +142,9 @@ Kind grad_kind_of(const epl_product_desc &p)
     return tiles_for(p.out_cols, p.in_cols, p.num_experts, grad_depth(p));
 }
 
-// A workspace: what tile_kernel tells join_kernel, then the partial tiles.
-constexpr size_t kHeaderBytes = 256;
-
-size_t tile_workspace(Kind k, int64_t tiles, int parts)
-{
-    if (k == kFew || parts < 2)
-        return 0;
-    const int64_t slots = std::min<int64_t>(kCus * P::tile_groups(side_of(k)), tiles * parts);
-    return kHeaderBytes + (size_t)slots * side_of(k) * side_of(k) * sizeof(float);
-}
-
-void use_workspace(P::Args &a, void *workspace)
-{
-    a.header = static_cast<int *>(workspace);
-    a.ws = workspace ? reinterpret_cast<P::f32x4 *>(static_cast<char *>(workspace) + kHeaderBytes)
-                     : nullptr;
-}
-
 int64_t product_tiles(const epl_product_desc &p, Kind k)
 {
-    return (p.num_rows / side_of(k) + p.num_experts) * ((p.out_cols + side_of(k) - 1) / side_of(k));
+    return H::product_tiles(p.num_rows, p.num_experts, p.out_cols, k);
 }
 
 int64_t grad_tiles(const epl_product_desc &p, Kind k)
@@ -216,24 +153,18 @@ int64_t grad_tiles(const epl_product_desc &p, Kind k)
            ((p.in_cols + side_of(k) - 1) / side_of(k));
 }
 
-// `tiles`: how many there are, or at most are.
 template <int SIDE, P::Form FORM>
 int launch_tiles(const P::Args &a, int64_t tiles, hipStream_t s)
 {
-    // every workgroup that the CUs hold at once, striding over the tiles;
-    // also with fewer tiles where their contraction can be split
     const bool split = a.ws && a.max_parts > 1;
+    const int grid = tile_grid(a, tiles, SIDE, split);
     constexpr int threads = P::tile_threads(SIDE);
-    const int most = num_cus() * P::tile_groups(SIDE);
-    const int grid = (int)std::min<int64_t>(split ? tiles * a.max_parts : tiles, most);
     hipLaunchKernelGGL((P::tile_kernel<SIDE, SIDE, FORM>), dim3((unsigned)grid), dim3(threads), 0, s, a);
     int rc = launch_status();
     if (rc == EPL_OK && split) {
         constexpr int pieces = SIDE / P::kWavesM / 16;
-        const int64_t most_left = std::min<int64_t>(tiles, grid / 2);
-        hipLaunchKernelGGL((P::join_kernel<SIDE, SIDE, FORM>),
-                           dim3(pieces, (unsigned)std::max<int64_t>(1, most_left)), dim3(threads), 0, s,
-                           a, grid);
+        hipLaunchKernelGGL((P::join_kernel<SIDE, SIDE, FORM>), dim3(pieces, join_grid(tiles, grid)),
+                           dim3(threads), 0, s, a, grid);
         rc = launch_status();
     }
     return rc;

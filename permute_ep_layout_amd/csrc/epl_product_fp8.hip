@@ -7,25 +7,16 @@
 
 #include "epl.h"
 #include "epl_product_fp8_kernels.h"
+#include "epl_product_host.h"
 
 namespace {
 
 namespace P = epl_product8;
+namespace H = epl_product_host;
 
-bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+using namespace H;
 
-int launch_status() { return hipGetLastError() == hipSuccess ? EPL_OK : EPL_EHIP; }
-
-// Offsets within one expert's weight and within a tile are 32-bit, and so are
-// counts of rows, stepped through by up to a tile.
-constexpr int32_t kMaxCols = 1 << 20;
-constexpr int64_t kMaxWeight = int64_t(1) << 30;
-constexpr int64_t kMaxRows = INT32_MAX - 1023;
-
-bool is_grad(int act)
-{
-    return act == EPL_ACT_SILU_GRAD || act == EPL_ACT_GELU_GRAD || act == EPL_ACT_SWIGLU_GRAD;
-}
+constexpr int64_t kMaxWeight = int64_t(1) << 30;     // bytes of an expert's
 
 int out_cols(const epl_product_fp8_desc &p)
 {
@@ -67,6 +58,62 @@ bool desc_ok(const epl_product_fp8_desc *p)
            (p->scale_format == EPL_SCALE_F32 || p->scale_format == EPL_SCALE_UE8M0);
 }
 
+// Rows an expert, on average, up to which the weights are read straight from
+// memory.
+constexpr int64_t kFewRows = 12;
+
+constexpr Cost cost_of(Kind k) { return k == kLarge ? Cost{13.0, 1.55} : Cost{7.0, 1.1}; }
+
+int max_parts(int64_t depth) { return H::max_parts(depth, P::kGroup); }
+
+int64_t average_rows(const epl_product_fp8_desc &p)
+{
+    const int64_t rows = p.expected_rows > 0 ? std::min(p.expected_rows, p.num_rows) : p.num_rows;
+    return (rows + p.num_experts - 1) / p.num_experts;
+}
+
+Kind kind_of(const epl_product_fp8_desc &p)
+{
+    const int64_t avg = average_rows(p);
+    if (p.weight_layout == EPL_WEIGHT_OUT_IN && avg <= kFewRows)
+        return kFew;
+    // a small tile holds half a group of 128 columns of the gated activation
+    if (p.activation == EPL_ACT_SWIGLU && p.codes_scale_format != EPL_SCALE_NONE)
+        return kLarge;
+    auto time = [&](Kind k) {
+        return tiles_time(k, avg, p.out_cols, p.num_experts, p.in_cols, P::kGroup, cost_of(k));
+    };
+    return time(kLarge) <= time(kSmall) ? kLarge : kSmall;
+}
+
+int64_t tiles_of(const epl_product_fp8_desc &p, Kind k)
+{
+    return product_tiles(p.num_rows, p.num_experts, p.out_cols, k);
+}
+
+template <int SIDE, bool QT, bool CODES>
+int launch_tiles(const P::Args &a, int64_t tiles, hipStream_t s)
+{
+    const bool split = a.ws && a.max_parts > 1;
+    const int grid = tile_grid(a, tiles, SIDE, split);
+    constexpr int threads = P::tile_threads(SIDE);
+    hipLaunchKernelGGL((P::tile_kernel<SIDE, SIDE, QT, CODES>), dim3((unsigned)grid), dim3(threads), 0, s, a);
+    int rc = launch_status();
+    if (rc == EPL_OK && split) {
+        constexpr int pieces = SIDE / P::kWavesM / 16;
+        hipLaunchKernelGGL((P::join_kernel<SIDE, SIDE, CODES>), dim3(pieces, join_grid(tiles, grid)),
+                           dim3(threads), 0, s, a, grid);
+        rc = launch_status();
+    }
+    return rc;
+}
+
+template <bool QT, bool CODES>
+int launch_kind(Kind k, const P::Args &a, int64_t tiles, hipStream_t s)
+{
+    return k == kSmall ? launch_tiles<128, QT, CODES>(a, tiles, s) : launch_tiles<256, QT, CODES>(a, tiles, s);
+}
+
 }  // namespace
 
 extern "C" {
@@ -76,7 +123,13 @@ int epl_product_fp8_validate(const epl_product_fp8_desc *p)
     return desc_ok(p) ? EPL_OK : EPL_EINVAL;
 }
 
-size_t epl_product_fp8_workspace_bytes(const epl_product_fp8_desc *) { return 0; }
+size_t epl_product_fp8_workspace_bytes(const epl_product_fp8_desc *p)
+{
+    if (!desc_ok(p))
+        return 0;
+    const Kind k = kind_of(*p);
+    return tile_workspace(k, tiles_of(*p, k), max_parts(p->in_cols));
+}
 
 int epl_expert_product_fp8(const epl_product_fp8_desc *p, const uint8_t *x, const void *x_scale,
                            const uint8_t *weight, const void *weight_scale, const float *bias,
@@ -109,7 +162,7 @@ int epl_expert_product_fp8(const epl_product_fp8_desc *p, const uint8_t *x, cons
     a.w8 = weight;
     a.xs = P::Scales{const_cast<void *>(x_scale), p->scale_format, (p->in_cols + 127) / 128,
                      p->rows_per_expert, p->num_rows};
-    a.ws = weight_scale;
+    a.wscale = weight_scale;
     a.ws_bytes = p->weight_scale_format == EPL_SCALE_UE8M0;
     a.in_out = p->weight_layout == EPL_WEIGHT_IN_OUT;
     a.codes = codes;
@@ -127,14 +180,24 @@ int epl_expert_product_fp8(const epl_product_fp8_desc *p, const uint8_t *x, cons
     a.act = p->activation;
     a.out_f32 = p->out_type == EPL_OUT_F32;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const bool paired = p->activation == EPL_ACT_SWIGLU;
-    const int cols = paired ? a.N / 2 : a.N;
-    const dim3 grid((unsigned)((cols + 127) / 128), (unsigned)a.E);
-    if (paired)
-        hipLaunchKernelGGL((P::few_rows_kernel<true>), grid, dim3(P::kFewThreads), 0, s, a);
-    else
-        hipLaunchKernelGGL((P::few_rows_kernel<false>), grid, dim3(P::kFewThreads), 0, s, a);
-    return launch_status();
+    const Kind k = kind_of(*p);
+    if (k == kFew) {
+        const bool paired = p->activation == EPL_ACT_SWIGLU;
+        const int cols = paired ? a.N / 2 : a.N;
+        const dim3 grid((unsigned)((cols + 127) / 128), (unsigned)a.E);
+        if (paired)
+            hipLaunchKernelGGL((P::few_rows_kernel<true>), grid, dim3(P::kFewThreads), 0, s, a);
+        else
+            hipLaunchKernelGGL((P::few_rows_kernel<false>), grid, dim3(P::kFewThreads), 0, s, a);
+        return launch_status();
+    }
+    a.max_parts = max_parts(a.K);
+    a.stages = stages_of(a.K, P::kGroup);
+    use_workspace(a, a.max_parts > 1 ? workspace : nullptr);
+    const int64_t tiles = tiles_of(*p, k);
+    if (a.in_out)
+        return quantized ? launch_kind<true, true>(k, a, tiles, s) : launch_kind<true, false>(k, a, tiles, s);
+    return quantized ? launch_kind<false, true>(k, a, tiles, s) : launch_kind<false, false>(k, a, tiles, s);
 }
 
 }  // extern "C"

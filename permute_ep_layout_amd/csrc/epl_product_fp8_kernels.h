@@ -40,7 +40,7 @@ constexpr int kGroup = epl_cast::kGroup;
 struct Args : epl_product::Args {
     const uint8_t *x8, *w8;
     Scales xs;                // of x
-    const void *ws;           // of the weight: [E, blocks of out, blocks of in] as it lies
+    const void *wscale;       // of the weight: [E, blocks of out, blocks of in] as it lies
     int ws_bytes;             // exponents, one byte each, rather than fp32
     int in_out;               // weight [E, K, N]
     uint8_t *codes;           // the result as codes, or null
@@ -60,8 +60,8 @@ __device__ __forceinline__ float weight_scale(const Args &a, int e, int n, int b
 {
     const int nb = blocks_of(a.N), kb = blocks_of(a.K);
     const int64_t at = (int64_t)e * nb * kb + (a.in_out ? b * nb + n / kGroup : n / kGroup * kb + b);
-    return a.ws_bytes ? epl_cast::power_of(static_cast<const uint8_t *>(a.ws)[at])
-                      : static_cast<const float *>(a.ws)[at];
+    return a.ws_bytes ? epl_cast::power_of(static_cast<const uint8_t *>(a.wscale)[at])
+                      : static_cast<const float *>(a.wscale)[at];
 }
 
 // The finished values of C columns n .. of one row, from the product z: z is
@@ -135,6 +135,498 @@ __device__ __forceinline__ void store_codes(const Args &a, int64_t at, const flo
     for (int i = 0; i < C / 4; ++i)
         r[i] = w[i];
     *reinterpret_cast<vec *>(a.codes + at) = r;
+}
+
+// ----------------------------------------------------------- tile kernel --
+//
+// The tile kernel of the bf16 products on bytes: a workgroup of 8 (or 4) waves
+// computes BM x BN outputs, one block of 128 of the contraction at a time, from
+// two LDS stages that buffer loads fill while the other is multiplied. The
+// weight is the matrix instruction's A operand and the rows its B operand, so
+// that a lane's quad (i, j) holds row 16 i + r of the wave's rows (lane 16 q +
+// r) and columns 16 j + 4 q .. + 3: one scale of x for the quad, and one of the
+// weight. A lane's 32 k of an instruction are the 16-byte pieces q and q + 4 of
+// the block, for both operands alike.
+//
+// LDS: a contiguous operand as there (128 bytes a row, pieces swizzled by row);
+// a strided weight [128][BN] with piece c of row k at c ^ swz_t8(k), read with
+// ds_read_b64_tr_b8, which hands lane r of 16 column r of 8 rows, so that the 8
+// rows of two such groups fall on different banks.
+//
+// The scales of a block (of BM rows and of BN / 8 pieces of 8 columns) come
+// through registers: a thread loads one of them two stages ahead, and writes it
+// to LDS, as a number, before the barrier that ends the wait for it.
+//
+// Columns of the gated activation alternate by 16, gate and up.
+
+using epl_product::at;
+using epl_product::dma;
+using epl_product::each;
+using epl_product::landed;
+using epl_product::Plan;
+using epl_product::put;
+using epl_product::rsrc;
+using epl_product::swz;
+using epl_product::take;
+using epl_product::Tile;
+using epl_product::tile_threads;
+using epl_product::waves_n;
+
+typedef int i32x2 __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) i32x2 lds_i32x2;
+
+constexpr int kWavesM = epl_product::kWavesM;
+
+template <int BN>
+__device__ __forceinline__ int swz_t8(int k)
+{
+    return BN == 256 ? (k & 7) | ((k >> 4 & 1) << 3) : (k >> 1 & 3) | ((k >> 4 & 1) << 2);
+}
+
+// Column of the product (in [0, N) or beyond) of column c of tile tn.
+template <int BN>
+__device__ __forceinline__ int column_of(const Args &a, int tn, int c)
+{
+    return a.act == EPL_ACT_SWIGLU ? tn * (BN / 2) + (c >> 5) * 16 + (c & 15) + (c >> 4 & 1) * (a.N / 2)
+                                   : tn * BN + c;
+}
+
+// 32 codes of one column from a strided weight's stage [128][BN].
+template <int BN>
+__device__ __forceinline__ i32x8 read_tr8(const uint16_t *at)
+{
+    const uint8_t *p = reinterpret_cast<const uint8_t *>(at);
+    const i32x2 a = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2 *)p);
+    const i32x2 b = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2 *)(p + 8 * BN));
+    const i32x2 c = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2 *)(p + 64 * BN));
+    const i32x2 d = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2 *)(p + 72 * BN));
+    return i32x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// The epilogue of ROWS rows of 64 columns that a wave holds in its part of LDS
+// (as epl_product::emit_rows): a lane takes 8 neighbouring columns of y. m0:
+// the first row in the tile's block. With CODES every wave of the workgroup
+// comes here together, and the values stay in registers until the waves that
+// share a group of 128 columns have exchanged their largest.
+template <int BN, int ROWS, bool CODES, bool PAIRED>
+__device__ __forceinline__ void emit_rows(const Args &a, const Tile &x, const float *mine, int m0,
+                                          int lane, int wm, int wn, float *most)
+{
+    constexpr int LANES = PAIRED ? 4 : 8, STEP = 64 / LANES, TURNS = ROWS / STEP;
+    constexpr int WN = waves_n(BN), SHARE = PAIRED ? 4 : 2;        // waves of a group
+    const int c = lane % LANES * 8;
+    const int n = PAIRED ? x.tn * (BN / 2) + wn * 32 + c : x.tn * BN + wn * 64 + c;
+    const int at = PAIRED ? (c >> 4) * 32 + (c & 15) : c;          // column in LDS
+    const int F = PAIRED ? a.N / 2 : a.N, cols = out_cols(a);
+    const bool in = n < F, two = !PAIRED && a.act == EPL_ACT_SWIGLU_GRAD;
+    if (!CODES && !in)
+        return;
+    float b[8] = {}, bu[8] = {};
+    if (in) {
+        bias_of<8>(a, x.e, n, b);
+        if (PAIRED)
+            bias_of<8>(a, x.e, F + n, bu);
+    }
+    constexpr int AHEAD = CODES ? TURNS : TURNS < 4 ? TURNS : 4;
+#pragma unroll 1
+    for (int t0 = 0; t0 < TURNS; t0 += AHEAD) {
+        Side<8> s[AHEAD];
+        float v[AHEAD][8], u[AHEAD][8];
+        if (in) {
+#pragma unroll
+            for (int t = 0; t < AHEAD; ++t)
+                s[t] = side_of<8>(a, x.lo + min(m0 + (t0 + t) * STEP + lane / LANES, x.cnt - 1), n);
+        }
+#pragma unroll
+        for (int t = 0; t < AHEAD; ++t) {
+            const int row = (t0 + t) * STEP + lane / LANES;
+            const int64_t p = x.lo + m0 + row;
+            const bool live = in && m0 + row < x.cnt;
+            take<8>(mine, row, at, v[t]);
+            if (PAIRED)
+                take<8>(mine, row, at + 16, u[t]);
+            if (live) {
+                finish<8>(a, p, n, b, bu, s[t], v[t], u[t]);
+                if (a.y) {
+                    epl_product::store_out<8>(a, p * cols + n, v[t]);
+                    if (two)
+                        epl_product::store_out<8>(a, p * cols + F + n, u[t]);
+                }
+            }
+            if (CODES) {
+                for (int h = 0; h < (two ? 2 : 1); ++h) {
+                    float m = largest(h ? u[t] : v[t]);
+#pragma unroll
+                    for (int d = 1; d < LANES; d <<= 1)
+                        m = fmaxf(m, __shfl_xor(m, d));
+                    if (lane % LANES == 0)
+                        most[((h * kWavesM + wm) * ROWS + row) * WN + wn] = m;
+                }
+            }
+        }
+        if (CODES) {
+            __syncthreads();
+#pragma unroll
+            for (int t = 0; t < AHEAD; ++t) {
+                const int row = (t0 + t) * STEP + lane / LANES;
+                const int64_t p = x.lo + m0 + row;
+                for (int h = 0; h < (two ? 2 : 1); ++h) {
+                    const float *of = most + ((h * kWavesM + wm) * ROWS + row) * WN + wn / SHARE * SHARE;
+                    float m = fmaxf(of[0], of[1]);
+                    if (PAIRED)
+                        m = fmaxf(m, fmaxf(of[2], of[3]));
+                    const Factor f = epl_cast::factor_of(m, a.cs.format == EPL_SCALE_UE8M0);
+                    if (in && m0 + row < x.cnt) {
+                        store_codes<8>(a, p * cols + h * F + n, h ? u[t] : v[t], f);
+                        if (wn % SHARE == 0 && lane % LANES == 0)
+                            epl_cast::store_scale(a.cs, p, (h * F + n) / kGroup, f);
+                    }
+                }
+            }
+            __syncthreads();                   // the next rows' maxima overwrite these
+        }
+    }
+}
+
+template <int BN, int ROWS, bool CODES>
+__device__ __forceinline__ void emit_any(const Args &a, const Tile &x, const float *mine, int m0,
+                                         int lane, int wm, int wn, float *most)
+{
+    if (a.act == EPL_ACT_SWIGLU) {
+        if constexpr (!CODES || BN == 256)
+            emit_rows<BN, ROWS, CODES, true>(a, x, mine, m0, lane, wm, wn, most);
+    } else {
+        emit_rows<BN, ROWS, CODES, false>(a, x, mine, m0, lane, wm, wn, most);
+    }
+}
+
+// acc + by * sum, each rounded once.
+__device__ __forceinline__ f32x4 scaled(f32x4 sum, float by, f32x4 acc)
+{
+    return __builtin_elementwise_fma(sum, f32x4{by, by, by, by}, acc);
+}
+
+// Rows of a wave that the epilogue takes at a time.
+template <bool CODES>
+constexpr int epilogue_rows(int bm) { return bm / kWavesM / (CODES && bm == 256 ? 4 : 2); }
+
+template <int BM, int BN, bool QT, bool CODES>
+__global__ __launch_bounds__(tile_threads(BN), 2) void tile_kernel(Args a)
+{
+    constexpr int WN = waves_n(BN), WM = kWavesM, WAVES = WM * WN;
+    constexpr int IP = BM / WM / 16;                     // 16-row pieces of x a wave
+    constexpr int ROWS = WAVES * 8;                      // rows of a contiguous operand a DMA
+    constexpr int ISP = BM / ROWS, ISQ = BN / ROWS;      // DMAs a stage
+    constexpr int KQ = WAVES * 1024 / BN;                // rows of a strided one
+    constexpr int BYTES = 128;                           // of a row in a stage
+    constexpr int SCALES = BM + BN / 8;
+    constexpr int EROWS = epilogue_rows<CODES>(BM);
+    __shared__ __align__(1024) uint16_t sp0[BM * 64], sp1[BM * 64];
+    __shared__ __align__(1024) uint16_t sq0[BN * 64], sq1[BN * 64];
+    __shared__ float sc0[SCALES], sc1[SCALES];
+    __shared__ float most[CODES ? 2 * WM * EROWS * WN : 1];
+    __shared__ int32_t pre[epl_product::kMaxExperts + 1];
+    __shared__ int32_t sums[8];
+
+    const int tid = threadIdx.x;
+    const int lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / WN, wn = wave % WN, r = lane & 15, q = lane >> 4;
+
+    // the lane's LDS offsets (bytes) of its first pieces
+    int aq[2], ap[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int n = wn * 64 + r, m = wm * (BM / WM) + r, k = q * 16 + (r >> 1);
+        aq[h] = QT ? k * BN + ((wn * 4) ^ swz_t8<BN>(k)) * 16 + (r & 1) * 8
+                   : n * BYTES + ((h * 4 + q) ^ swz(n)) * 16;
+        ap[h] = m * BYTES + ((h * 4 + q) ^ swz(m)) * 16;
+    }
+    const int asx = wm * (BM / WM) + r, asw = BM + wn * 8 + (q >> 1);
+
+    const int ntn = (a.N + BN - 1) / BN;
+    epl_product::tile_prefix<BM, WAVES * 64>(a, pre, sums);
+    const int64_t total = (int64_t)pre[a.E] * ntn;
+
+    // workgroups of one XCD (every eighth) take neighbouring tiles
+    const int grid = gridDim.x;
+    int64_t first = blockIdx.x;
+    if (grid % epl_product::kNumXcd == 0)
+        first = (first % epl_product::kNumXcd) * (grid / epl_product::kNumXcd) + first / epl_product::kNumXcd;
+    const Plan plan = epl_product::plan_of<BM>(a, total, grid);
+    const int64_t items = plan.whole + plan.left * plan.parts;
+    if (a.ws && blockIdx.x == 0 && tid == 0)
+        a.header[0] = plan.left;
+
+    for (int64_t item = first; item < items; item += grid) {
+        const bool split = item >= plan.whole;
+        const int o = split ? (int)(item - plan.whole) : 0;
+        const int part = split ? o / plan.left : 0, rest = split ? o % plan.left : 0;
+        const Tile x = epl_product::locate<epl_product::kForward>(a, pre, split ? plan.whole + rest : item,
+                                                                  0, ntn);
+        const int e = x.e, cnt = x.cnt, tm = x.tm, tn = x.tn;
+        const int64_t lo = x.lo;
+
+        // opaque: what is derived from the lane for one tile is not kept for the next
+        int own = tid;
+        asm volatile("" : "+v"(own));
+        const int steps = blocks_of(a.K);
+        const int s0 = split ? steps * part / plan.parts : 0;
+        const int s1 = split ? steps * (part + 1) / plan.parts : steps;
+        // experts start at different places of the contraction (epl_product::tile_kernel)
+        const int turns = s1 - s0;
+        const int rot = turns > 0 ? (int)((uint32_t)(e * 13) % (uint32_t)turns) : 0;
+        const char *bp, *bq;
+        uint32_t op, oq;
+        int np, nq = 0, kp, kq = 0;
+        const int ip = ROWS * a.K;
+        const int iq = QT ? KQ * a.N : (a.act == EPL_ACT_SWIGLU ? ROWS / 2 : ROWS) * a.K;
+        {
+            const int row = own >> 3, c = (own & 7) ^ swz(row);
+            op = (uint32_t)row * a.K + c * 16;
+            kp = c * 16;
+            bp = reinterpret_cast<const char *>(a.x8 + (lo + (int64_t)tm * BM) * a.K);
+            np = min(cnt - tm * BM, BM) * a.K;
+        }
+        bq = reinterpret_cast<const char *>(a.w8 + (int64_t)e * a.K * a.N);
+        if (QT) {
+            const int k = own * 16 / BN, c = (own * 16 % BN / 16) ^ swz_t8<BN>(k);
+            oq = (uint32_t)k * a.N + column_of<BN>(a, tn, c * 16);
+        } else {
+            const int row = own >> 3, c = (own & 7) ^ swz(row);
+            oq = (uint32_t)column_of<BN>(a, tn, row) * a.K + c * 16;
+            kq = c * 16;
+            nq = a.N * a.K;
+        }
+        // the thread's scale: of row tm BM + tid, or of 8 columns
+        const bool of_x = wave < BM / 64;    // (the same for a wave)
+        const char *scale = nullptr;
+        bool small = false;                  // an exponent byte
+        int64_t per_block = 0;               // bytes to the next block's, or 4 blocks'
+        if (of_x) {
+            const int64_t p = lo + min(tm * BM + own, cnt - 1);
+            const char *base = static_cast<const char *>(a.xs.at);
+            if (a.xs.format == EPL_SCALE_UE8M0) {
+                scale = base + p * 4;
+                per_block = a.rows * 4;
+                small = true;
+            } else {
+                scale = base + epl_cast::scale_index(a.xs, p, 0) * 4;
+                per_block = a.xs.format == EPL_SCALE_F32_RECT ? (int64_t)a.xs.cap * 4 : 4;
+            }
+        } else if (own < SCALES) {
+            const int n = min(column_of<BN>(a, tn, (own - BM) * 8), a.N - 1);
+            const int nb = blocks_of(a.N), kb = blocks_of(a.K), size = a.ws_bytes ? 1 : 4;
+            scale = static_cast<const char *>(a.wscale) +
+                    ((int64_t)e * nb * kb + (int64_t)(n / kGroup) * (QT ? 1 : kb)) * size;
+            per_block = (QT ? nb : 1) * size;
+            small = a.ws_bytes;
+        }
+
+        f32x4 acc[IP * 4];
+        each<IP * 4>([&](auto i) { acc[i] = f32x4{0, 0, 0, 0}; });
+
+        struct Stage {
+            __amdgpu_buffer_rsrc_t rp, rq;
+            uint32_t op, oq;
+        };
+        auto block_at = [&](int s) { const int v = s + rot; return v < s1 ? v : v - turns; };
+        auto stage = [&](int s) {
+            const int k0 = block_at(s) * kGroup;
+            const int left = s < s1 ? min(a.K - k0, kGroup) : 0;
+            Stage f;
+            f.rp = rsrc(bp + k0, np - k0);
+            f.rq = QT ? rsrc(bq + (int64_t)k0 * a.N, left * a.N) : rsrc(bq + k0, nq - k0);
+            f.op = kp >= left ? op | 0x80000000u : op;
+            f.oq = !QT && kq >= left ? oq | 0x80000000u : oq;
+            return f;
+        };
+        auto fetch_one = [&](const Stage &f, uint16_t *lp, uint16_t *lq, auto i) {
+            if constexpr (i < ISP)
+                dma(f.rp, f.op + i * ip, lp + i * WAVES * 512 + wave * 512);
+            else
+                dma(f.rq, f.oq + (i - ISP) * iq, lq + (i - ISP) * WAVES * 512 + wave * 512);
+        };
+        auto fetch = [&](int s, uint16_t *lp, uint16_t *lq) {
+            const Stage f = stage(s);
+            each<ISP + ISQ>([&](auto i) { fetch_one(f, lp, lq, i); });
+        };
+        auto load_scale = [&](int s) {
+            uint32_t v = 0;
+            if (scale && s < s1) {
+                const int b = block_at(s);
+                if (small && of_x)
+                    v = *reinterpret_cast<const uint8_t *>(scale + (b >> 2) * per_block + (b & 3));
+                else if (small)
+                    v = *reinterpret_cast<const uint8_t *>(scale + b * per_block);
+                else
+                    v = *reinterpret_cast<const uint32_t *>(scale + b * per_block);
+            }
+            return v;
+        };
+        auto write_scale = [&](float *sc, uint32_t v) {
+            if (own < SCALES)
+                sc[own] = small ? epl_cast::power_of(v) : __uint_as_float(v);
+        };
+
+        i32x8 fq[4], fp[2];
+        float sx[2], sw[4];
+        f32x4 sum[4];                        // blocks' sums on their way, and their scales
+        float by[4];
+        each<4>([&](auto i) { sum[i] = f32x4{0, 0, 0, 0}, by[i] = 0.0f; });
+        auto pair = [&](const uint16_t *l, const int (&o2)[2], int rows) {
+            const i32x4 l0 = *reinterpret_cast<const i32x4 *>(at(l, o2[0], rows * 64));
+            const i32x4 l1 = *reinterpret_cast<const i32x4 *>(at(l, o2[1], rows * 64));
+            return __builtin_shufflevector(l0, l1, 0, 1, 2, 3, 4, 5, 6, 7);
+        };
+        auto read_q = [&](const uint16_t *lq, auto j) {
+            if constexpr (QT)
+                fq[j] = read_tr8<BN>(at(lq, aq[0] ^ (j * 16), 0));
+            else
+                fq[j] = pair(lq, aq, j * 16);
+        };
+        auto read_p = [&](const uint16_t *lp, const float *sc, auto g) {
+            fp[g % 2] = pair(lp, ap, g * 16);
+            sx[g % 2] = sc[asx + g * 16];
+        };
+        // Quad t = 4 g + j of a block: its sum starts; the sum that started three
+        // instructions before, which is done by now, is added to its accumulators.
+        auto multiply = [&](auto t) {
+            constexpr int g = t / 4, j = t % 4, old = (t + 4 * IP - 3) % (4 * IP);
+            sum[t % 4] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                fq[j], fp[g % 2], f32x4{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
+            by[t % 4] = sx[g % 2] * sw[j];
+            acc[old] = scaled(sum[old % 4], by[old % 4], acc[old]);
+            // here, and not after the loop: the sums would have to wait in memory
+            asm volatile("" : "+v"(acc[old]));
+        };
+        // One block: IP groups of 4 products, one piece of x each. A group's
+        // reads of the next piece run under its products; one barrier a stage,
+        // before the last group: all of this stage has been read by then, and
+        // may be overwritten, and the next has landed. The last group's
+        // products free the weight's registers one by one for the next stage's.
+        uint32_t coming = 0;                 // the scale of the stage after the next
+        auto turn = [&](int s, uint16_t *cp, uint16_t *cq, float *cs, uint16_t *xp, uint16_t *xq,
+                        float *xs) {
+            constexpr int dmas = ISP + ISQ, per = (dmas + 3) / 4;
+            Stage f;
+            each<IP>([&](auto g) {
+                if constexpr (g + 1 < IP)
+                    read_p(cp, cs, std::integral_constant<int, g + 1>{});
+                if constexpr (g == IP - 1) {
+                    write_scale(xs, coming);
+                    landed();
+                    f = stage(s + 2);
+                    coming = load_scale(s + 2);
+                }
+                each<4>([&](auto j) {
+                    multiply(std::integral_constant<int, g * 4 + j>{});
+                    if constexpr (g == IP - 1) {
+                        read_q(xq, j);
+                        each<per>([&](auto i) {
+                            constexpr std::integral_constant<int, decltype(j)::value * per + decltype(i)::value> d{};
+                            if constexpr (d < dmas)
+                                fetch_one(f, cp, cq, d);
+                        });
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                });
+                if constexpr (g == IP - 1) {
+                    read_p(xp, xs, std::integral_constant<int, 0>{});
+                    each<4>([&](auto j) { sw[j] = xs[asw + j * 2]; });
+                }
+            });
+        };
+        coming = load_scale(s0);
+        fetch(s0, sp0, sq0);
+        write_scale(sc0, coming);
+        landed();
+        fetch(s0 + 1, sp1, sq1);
+        coming = load_scale(s0 + 1);
+        each<4>([&](auto j) {
+            read_q(sq0, j);
+            sw[j] = sc0[asw + j * 2];
+        });
+        read_p(sp0, sc0, std::integral_constant<int, 0>{});
+        for (int s = s0; s < s1; s += 2) {
+            turn(s, sp0, sq0, sc0, sp1, sq1, sc1);
+            turn(s + 1, sp1, sq1, sc1, sp0, sq0, sc0);
+        }
+        each<3>([&](auto i) {                // the last three sums
+            constexpr int old = 4 * IP - 3 + i;
+            acc[old] = scaled(sum[old % 4], by[old % 4], acc[old]);
+        });
+        landed();                            // (what was fetched past the end too)
+
+        own = tid & 63;
+        asm volatile("" : "+v"(own));
+        const int er = own & 15, eq = own >> 4;
+        if (split) {
+            // registers as they are; join_kernel reads them alike
+            f32x4 *slot = a.ws + (int64_t)(rest * plan.parts + part) * (BM * BN / 4);
+            each<IP * 4>([&](auto y) { slot[((y / 4 * WAVES + wave) * 4 + y % 4) * 64 + own] = acc[y]; });
+        } else {
+            // some of the wave's rows at a time through its part of the stages
+            constexpr int share = WAVES / 4;       // waves to a stage array
+            uint16_t *const stages = wave < share       ? sp0
+                                     : wave < 2 * share ? sp1
+                                     : wave < 3 * share ? sq0
+                                                        : sq1;
+            float *const mine = reinterpret_cast<float *>(stages) + wave % share * EROWS * 64;
+            constexpr int pieces = EROWS / 16;
+            each<IP / pieces>([&](auto h) {
+                each<pieces>([&](auto i) {
+                    each<4>([&](auto j) {
+                        put(mine, i * 16 + er, j * 4 + eq, acc[(h * pieces + i) * 4 + j]);
+                    });
+                });
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+                emit_any<BN, EROWS, CODES>(a, x, mine, tm * BM + wm * (BM / WM) + h * EROWS, own, wm, wn, most);
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+            });
+            __syncthreads();       // the next tile's stages overwrite the other waves' parts
+        }
+    }
+}
+
+// Adds the parts of the tiles that tile_kernel split, in order, and runs their
+// epilogue (as epl_product::join_kernel).
+template <int BM, int BN, bool CODES>
+__global__ __launch_bounds__(tile_threads(BN)) void join_kernel(Args a, int grid)
+{
+    constexpr int WN = waves_n(BN), WM = kWavesM, WAVES = WM * WN;
+    __shared__ __align__(16) float rows[WAVES * 16 * 64];
+    __shared__ float most[CODES ? 2 * WM * 16 * WN : 1];
+    __shared__ int32_t pre[epl_product::kMaxExperts + 1];
+    __shared__ int32_t sums[8];
+    const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, q = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave / WN, wn = wave % WN;
+    if (a.header[0] == 0)
+        return;
+    const int i = blockIdx.x, ntn = (a.N + BN - 1) / BN;
+    epl_product::tile_prefix<BM, WAVES * 64>(a, pre, sums);
+    const Plan plan = epl_product::plan_of<BM>(a, (int64_t)pre[a.E] * ntn, grid);
+    for (int l = blockIdx.y; l < plan.left; l += gridDim.y) {
+        const Tile x = epl_product::locate<epl_product::kForward>(a, pre, plan.whole + l, 0, ntn);
+        const f32x4 *slot = a.ws + (int64_t)l * plan.parts * (BM * BN / 4) + ((i * WAVES + wave) * 4) * 64 + lane;
+        f32x4 acc[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            acc[j] = slot[j * 64];
+        for (int p = 1; p < plan.parts; ++p) {
+            slot += BM * BN / 4;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                acc[j] += slot[j * 64];
+        }
+        float *mine = rows + wave * 16 * 64;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            put(mine, r, j * 4 + q, acc[j]);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+        emit_any<BN, 16, CODES>(a, x, mine, x.tm * BM + wm * (BM / WM) + i * 16, lane, wm, wn, most);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+    }
 }
 
 // ------------------------------------------------------ few-rows kernel --
