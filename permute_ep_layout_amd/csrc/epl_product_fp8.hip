@@ -91,6 +91,14 @@ int64_t tiles_of(const epl_product_fp8_desc &p, Kind k)
     return product_tiles(p.num_rows, p.num_experts, p.out_cols, k);
 }
 
+template <bool PAIRED, int G, int WAVES>
+void launch_few(const P::Args &a, hipStream_t s)
+{
+    const int groups = ((PAIRED ? a.N / 2 : a.N) + G * 16 - 1) / (G * 16);
+    hipLaunchKernelGGL((P::few_rows_kernel<PAIRED, G, WAVES>), dim3((unsigned)groups, (unsigned)a.E),
+                       dim3(P::few_threads<WAVES>()), 0, s, a);
+}
+
 template <int SIDE, bool QT, bool CODES>
 int launch_tiles(const P::Args &a, int64_t tiles, hipStream_t s)
 {
@@ -182,13 +190,12 @@ int epl_expert_product_fp8(const epl_product_fp8_desc *p, const uint8_t *x, cons
     hipStream_t s = static_cast<hipStream_t>(stream);
     const Kind k = kind_of(*p);
     if (k == kFew) {
-        const bool paired = p->activation == EPL_ACT_SWIGLU;
-        const int cols = paired ? a.N / 2 : a.N;
-        const dim3 grid((unsigned)((cols + 127) / 128), (unsigned)a.E);
-        if (paired)
-            hipLaunchKernelGGL((P::few_rows_kernel<true>), grid, dim3(P::kFewThreads), 0, s, a);
+        if (p->activation == EPL_ACT_SWIGLU)
+            launch_few<true, 8, 16>(a, s);
+        else if (quantized)
+            launch_few<false, 8, 16>(a, s);
         else
-            hipLaunchKernelGGL((P::few_rows_kernel<false>), grid, dim3(P::kFewThreads), 0, s, a);
+            launch_few<false, 2, 8>(a, s);
         return launch_status();
     }
     a.max_parts = max_parts(a.K);

@@ -55,26 +55,22 @@ __device__ __forceinline__ int out_cols(const Args &a)
     return a.act == EPL_ACT_SWIGLU ? a.N / 2 : a.act == EPL_ACT_SWIGLU_GRAD ? 2 * a.N : a.N;
 }
 
-// The scale of column n's block and block b of the contraction.
-__device__ __forceinline__ float weight_scale(const Args &a, int e, int n, int b)
-{
-    const int nb = blocks_of(a.N), kb = blocks_of(a.K);
-    const int64_t at = (int64_t)e * nb * kb + (a.in_out ? b * nb + n / kGroup : n / kGroup * kb + b);
-    return a.ws_bytes ? epl_cast::power_of(static_cast<const uint8_t *>(a.wscale)[at])
-                      : static_cast<const float *>(a.wscale)[at];
-}
-
-// The finished values of C columns n .. of one row, from the product z: z is
+// The finished values of C columns n .. of one row, from z, product and bias: z is
 // column n of y, and u column N + n (gradient of the gated activation). Of the
 // gated activation z and u are the gate's and the up half's product, and z the
-// result.
+// result. kept: what the backward pass is left of both.
 template <int C>
-__device__ __forceinline__ void finish(const Args &a, int64_t row, int n, const float (&b)[C],
-                                       const float (&bu)[C], const Side<C> &s, float (&z)[C],
-                                       float (&u)[C])
+struct Kept {
+    typedef __bf16 vec __attribute__((ext_vector_type(C)));
+    vec z, u;
+};
+
+template <int C, bool PAIRED>
+__device__ __forceinline__ void finish(const Args &a, const Side<C> &s, float (&z)[C], float (&u)[C],
+                                       Kept<C> &kept)
 {
     using namespace epl_product;
-    if (a.act == EPL_ACT_SWIGLU_GRAD) {
+    if (!PAIRED && a.act == EPL_ACT_SWIGLU_GRAD) {
 #pragma unroll
         for (int i = 0; i < C; ++i) {
             u[i] = z[i] * silu((float)s.x[i]);
@@ -82,33 +78,57 @@ __device__ __forceinline__ void finish(const Args &a, int64_t row, int n, const 
         }
         return;
     }
-    if (a.act == EPL_ACT_SILU_GRAD || a.act == EPL_ACT_GELU_GRAD) {
+    if (!PAIRED && a.act >= EPL_ACT_SILU_GRAD) {
 #pragma unroll
         for (int i = 0; i < C; ++i)
             z[i] *= a.act == EPL_ACT_SILU_GRAD ? silu_slope((float)s.x[i]) : gelu_slope((float)s.x[i]);
         return;
     }
-    const bool paired = a.act == EPL_ACT_SWIGLU;
+    if (a.pre) {
 #pragma unroll
-    for (int i = 0; i < C; ++i) {
-        z[i] += b[i];
-        u[i] += bu[i];
+        for (int i = 0; i < C; ++i) {
+            kept.z[i] = (__bf16)z[i];
+            if (PAIRED)
+                kept.u[i] = (__bf16)u[i];
+        }
     }
-    if (a.pre) {                                   // read by the backward pass, much later
-        store_bf16<C, true>(a.pre + row * a.N + n, z);
-        if (paired)
-            store_bf16<C, true>(a.pre + row * a.N + a.N / 2 + n, u);
-    }
+    if (PAIRED) {
 #pragma unroll
-    for (int i = 0; i < C; ++i) {
-        if (paired)
+        for (int i = 0; i < C; ++i)
             z[i] = silu(z[i]) * u[i];
-        else if (a.act == EPL_ACT_SILU)
+    } else if (a.act == EPL_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < C; ++i)
             z[i] = silu(z[i]);
-        else if (a.act == EPL_ACT_GELU)
+    } else if (a.act == EPL_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < C; ++i)
             z[i] = gelu(z[i]);
-        if (a.residual)
+    }
+    if (a.residual) {
+#pragma unroll
+        for (int i = 0; i < C; ++i)
             z[i] += (float)s.x[i];
+    }
+}
+
+// What finish() leaves, to memory: the kept product past the caches (it is
+// read by the backward pass, much later), and y.
+template <int C, bool PAIRED>
+__device__ __forceinline__ void store_row(const Args &a, int64_t row, int n, const float (&z)[C],
+                                          const float (&u)[C], const Kept<C> &kept)
+{
+    typedef typename Kept<C>::vec vec;
+    if (a.pre && a.act <= EPL_ACT_SWIGLU) {
+        __builtin_nontemporal_store(kept.z, reinterpret_cast<vec *>(a.pre + row * a.N + n));
+        if (PAIRED)
+            __builtin_nontemporal_store(kept.u, reinterpret_cast<vec *>(a.pre + row * a.N + a.N / 2 + n));
+    }
+    if (a.y) {
+        const int64_t at = row * out_cols(a) + n;
+        epl_product::store_out<C>(a, at, z);
+        if (!PAIRED && a.act == EPL_ACT_SWIGLU_GRAD)
+            epl_product::store_out<C>(a, at + a.N, u);
     }
 }
 
@@ -246,12 +266,15 @@ __device__ __forceinline__ void emit_rows(const Args &a, const Tile &x, const fl
             if (PAIRED)
                 take<8>(mine, row, at + 16, u[t]);
             if (live) {
-                finish<8>(a, p, n, b, bu, s[t], v[t], u[t]);
-                if (a.y) {
-                    epl_product::store_out<8>(a, p * cols + n, v[t]);
-                    if (two)
-                        epl_product::store_out<8>(a, p * cols + F + n, u[t]);
+                Kept<8> kept;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    v[t][i] += b[i];
+                    if (PAIRED)
+                        u[t][i] += bu[i];
                 }
+                finish<8, PAIRED>(a, s[t], v[t], u[t], kept);
+                store_row<8, PAIRED>(a, p, n, v[t], u[t], kept);
             }
             if (CODES) {
                 for (int h = 0; h < (two ? 2 : 1); ++h) {
@@ -631,111 +654,195 @@ __global__ __launch_bounds__(tile_threads(BN)) void join_kernel(Args a, int grid
 
 // ------------------------------------------------------ few-rows kernel --
 //
-// A workgroup of 8 waves takes 128 columns of y for an expert, a wave 16 of
-// them (of the gated activation 16 of each half) over the whole contraction.
+// For experts with a few rows the weights' bytes are the cost: each is read
+// once for 16 or 32 rows, straight into the registers of the matrix
+// instruction. A workgroup takes G times 16 columns of y for an expert (of the
+// gated activation as many of each half), a wave 16 of them; the KS waves of
+// the same columns take every KS-th block of the contraction each and add
+// their sums through LDS in order. Workgroups start at different places of the
+// contraction and come round, as those of the bf16 products.
 
-constexpr int kFewThreads = 512;
+template <int WAVES>
+constexpr int few_threads() { return WAVES * 64; }
 
-// 32 codes of a row's or column's block at k: pieces q and q + 4 of it.
-__device__ __forceinline__ i32x8 piece(const uint8_t *row, int k, int q, int K)
+// The scales of `U` blocks as they lie: of a row, and of a lane's 4 columns.
+__device__ __forceinline__ uint32_t raw_scale(const char *at, bool byte)
 {
-    i32x4 lo = {}, hi = {};
-    if (k + q * 16 < K)
-        lo = *reinterpret_cast<const i32x4 *>(row + k + q * 16);
-    if (k + q * 16 + 64 < K)
-        hi = *reinterpret_cast<const i32x4 *>(row + k + q * 16 + 64);
-    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    return byte ? *reinterpret_cast<const uint8_t *>(at) : *reinterpret_cast<const uint32_t *>(at);
 }
 
-// The same of a column of a weight [K, N].
-__device__ __forceinline__ i32x8 column(const uint8_t *col, int k, int q, int K, int N)
+__device__ __forceinline__ float scale_value(uint32_t v, bool byte)
 {
-    i32x8 r = {};
-    for (int i = 0; i < 32; ++i) {
-        const int at = k + q * 16 + (i & 15) + (i >> 4) * 64;
-        if (at < K)
-            r[i / 4] |= (int)((uint32_t)col[(int64_t)at * N] << (8 * (i & 3)));
+    return byte ? epl_cast::power_of(v) : __uint_as_float(v);
+}
+
+template <bool PAIRED, int G, int WAVES, int MT>
+__device__ __forceinline__ void few_rows(const Args &a, int e, int64_t row0, int left, int nb, f32x4 *red,
+                                         float *most)
+{
+    constexpr int J = PAIRED ? 2 : 1, KS = WAVES / G, U = PAIRED || MT == 2 ? 2 : 4;
+    static_assert(KS >= MT, "a row tile's epilogue has waves of its own");
+    const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, q = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), g = wave % G, ks = wave / G;
+    const int F = PAIRED ? a.N / 2 : a.N, kb = blocks_of(a.K), nblocks = blocks_of(a.N);
+    const int n0 = (nb * G + g) * 16;                       // the wave's first column
+    const int nq = min(n0 + q * 4, F - 4);                  // first column of the lane's quad
+    const auto rw = rsrc(reinterpret_cast<const char *>(a.w8 + (int64_t)e * a.N * a.K), a.N * a.K);
+    const auto rx = rsrc(reinterpret_cast<const char *>(a.x8 + row0 * a.K), left * a.K);
+    uint32_t ow[J], ox[MT];
+    const char *pw[J], *px[MT];                             // scales
+    const bool wbyte = a.ws_bytes, xbyte = a.xs.format == EPL_SCALE_UE8M0;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        ow[j] = (uint32_t)(min(n0 + r, F - 1) + j * F) * a.K + q * 16;
+        pw[j] = static_cast<const char *>(a.wscale) +
+                ((int64_t)e * nblocks * kb + (int64_t)((j * F + nq) / kGroup) * kb) * (wbyte ? 1 : 4);
     }
-    return r;
+    // (rows beyond the block: zeros, and the last row's scales)
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        const int64_t p = row0 + min(i * 16 + r, left - 1);
+        ox[i] = i * 16 + r < left ? (uint32_t)(i * 16 + r) * a.K + q * 16 : 0x80000000u;
+        px[i] = static_cast<const char *>(a.xs.at) + (xbyte ? p : epl_cast::scale_index(a.xs, p, 0)) * 4;
+    }
+    const int64_t x_step = xbyte ? a.xs.rows * 4 : a.xs.format == EPL_SCALE_F32_RECT ? (int64_t)a.xs.cap * 4 : 4;
+    f32x4 acc[MT][J];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+            acc[i][j] = f32x4{0, 0, 0, 0};
+
+    const int start = (int)((uint32_t)(e * 13 + nb * 3) % (uint32_t)kb);
+    for (int p = ks; p < kb; p += KS * U) {
+        i32x4 fw[U][J][2], fx[U][MT][2];
+        uint32_t sw[U][J], sx[U][MT];
+        int at[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int v = p + u * KS, b = v + start < kb ? v + start : v + start - kb, k = b * kGroup;
+            at[u] = v < kb ? b : 0;
+            const bool lo = v < kb && k + q * 16 < a.K, hi = v < kb && k + q * 16 + 64 < a.K;
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                fw[u][j][0] = __builtin_bit_cast(
+                    i32x4, __builtin_amdgcn_raw_buffer_load_b128(rw, (int)(lo ? ow[j] : 0x80000000u), k, 0));
+                fw[u][j][1] = __builtin_bit_cast(
+                    i32x4, __builtin_amdgcn_raw_buffer_load_b128(rw, (int)(hi ? ow[j] + 64 : 0x80000000u), k, 0));
+            }
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                fx[u][i][0] = __builtin_bit_cast(
+                    i32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, (int)(lo ? ox[i] : 0x80000000u), k, 0));
+                fx[u][i][1] = __builtin_bit_cast(
+                    i32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, (int)(hi ? ox[i] + 64 : 0x80000000u), k, 0));
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+                sx[u][i] = raw_scale(px[i] + (xbyte ? (at[u] >> 2) * x_step + (at[u] & 3) : at[u] * x_step), xbyte);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                sw[u][j] = raw_scale(pw[j] + at[u] * (wbyte ? 1 : 4), wbyte);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                const i32x8 x = __builtin_shufflevector(fx[u][i][0], fx[u][i][1], 0, 1, 2, 3, 4, 5, 6, 7);
+#pragma unroll
+                for (int j = 0; j < J; ++j) {
+                    const i32x8 w = __builtin_shufflevector(fw[u][j][0], fw[u][j][1], 0, 1, 2, 3, 4, 5, 6, 7);
+                    const f32x4 part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                        w, x, f32x4{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
+                    acc[i][j] = scaled(part, scale_value(sx[u][i], xbyte) * scale_value(sw[u][j], wbyte), acc[i][j]);
+                }
+            }
+        }
+    }
+
+    __syncthreads();           // red and most may still be read for the rows before
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+            red[((ks * MT + i) * J + j) * G * 64 + g * 64 + lane] = acc[i][j];
+    __syncthreads();
+    // waves ks = 0 .. MT - 1 finish a row tile each
+    const int row_in = ks * 16 + r;
+    const int64_t row = row0 + min(row_in, left - 1);
+    const bool live = ks < MT && row_in < left && n0 + q * 4 < F;
+    const bool two = !PAIRED && a.act == EPL_ACT_SWIGLU_GRAD;
+    const int cols = out_cols(a);
+    float z[4] = {}, u[4] = {};
+    if (ks < MT) {
+        f32x4 sum[J];
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            sum[j] = red[(ks * J + j) * G * 64 + g * 64 + lane];
+#pragma unroll
+            for (int o = 1; o < KS; ++o)
+                sum[j] += red[((o * MT + ks) * J + j) * G * 64 + g * 64 + lane];
+        }
+        float b[4], bu[4];
+        bias_of<4>(a, e, nq, b);
+        bias_of<4>(a, e, PAIRED ? F + nq : nq, bu);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            z[i] = sum[0][i] + b[i];
+            if (PAIRED)
+                u[i] = sum[J - 1][i] + bu[i];
+        }
+        Kept<4> kept;
+        finish<4, PAIRED>(a, side_of<4>(a, row, nq), z, u, kept);
+        if (live)
+            store_row<4, PAIRED>(a, row, nq, z, u, kept);
+    }
+    if constexpr (G == 8) {
+        if (!a.codes)
+            return;
+        if (ks < MT) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float v = largest(h ? u : z);
+                v = fmaxf(v, __shfl_xor(v, 16));
+                v = fmaxf(v, __shfl_xor(v, 32));
+                if (q == 0)
+                    most[((h * MT + ks) * G + g) * 16 + r] = v;
+            }
+        }
+        __syncthreads();
+        if (live) {
+            for (int h = 0; h < (two ? 2 : 1); ++h) {
+                float v = 0.0f;
+#pragma unroll
+                for (int i = 0; i < G; ++i)
+                    v = fmaxf(v, most[((h * MT + ks) * G + i) * 16 + r]);
+                const Factor f = epl_cast::factor_of(v, a.cs.format == EPL_SCALE_UE8M0);
+                store_codes<4>(a, row * cols + h * F + nq, h ? u : z, f);
+                if (g == 0 && q == 0)
+                    epl_cast::store_scale(a.cs, row, (h * F + nq) / kGroup, f);
+            }
+        }
+    }
 }
 
-template <bool PAIRED>
-__global__ __launch_bounds__(kFewThreads) void few_rows_kernel(Args a)
+template <bool PAIRED, int G, int WAVES>
+__global__ __launch_bounds__(few_threads<WAVES>(), 4) void few_rows_kernel(Args a)
 {
-    __shared__ float most[2][8][16];
+    __shared__ f32x4 red[WAVES * 2 * (PAIRED ? 2 : 1) * 64];
+    __shared__ float most[G == 8 ? 2 * 2 * G * 16 : 1];
     const int e = blockIdx.y, nb = blockIdx.x;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, q = lane >> 4;
-    const int F = PAIRED ? a.N / 2 : a.N;
-    const int n = nb * kGroup + wave * 16;           // first column of the wave
-    constexpr int J = PAIRED ? 2 : 1;
     int64_t lo;
     const int cnt = block_of(a, e, lo);
-    const int nq = min(n + q * 4, F - 4);            // first column of the lane's quad
-    const bool in = n + q * 4 < F;
-    const uint8_t *w[J];
-    for (int j = 0; j < J; ++j) {
-        const int64_t c = min(n + r, F - 1) + j * F;
-        w[j] = a.w8 + (int64_t)e * a.N * a.K + (a.in_out ? c : c * a.K);
-    }
-    float b[4], bu[4] = {0, 0, 0, 0};
-    bias_of<4>(a, e, nq, b);
-    if (PAIRED)
-        bias_of<4>(a, e, F + nq, bu);
-    for (int m = 0; m < cnt; m += 16) {
-        const int64_t row = lo + min(m + r, cnt - 1);
-        const bool live = m + r < cnt && in;
-        f32x4 acc[J];
-        for (int j = 0; j < J; ++j)
-            acc[j] = f32x4{0, 0, 0, 0};
-        for (int g = 0; g < blocks_of(a.K); ++g) {
-            const i32x8 fx = piece(a.x8 + row * a.K, g * kGroup, q, a.K);
-            const float sx = epl_cast::load_scale(a.xs, row, g);
-            for (int j = 0; j < J; ++j) {
-                const i32x8 fw = a.in_out ? column(w[j], g * kGroup, q, a.K, a.N)
-                                          : piece(w[j], g * kGroup, q, a.K);
-                const f32x4 part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                    fw, fx, f32x4{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
-                const float s = sx * weight_scale(a, e, j * F + nq, g);
-                for (int i = 0; i < 4; ++i)
-                    acc[j][i] = fmaf(part[i], s, acc[j][i]);
-            }
-        }
-        float z[4], u[4] = {0, 0, 0, 0};
-        for (int i = 0; i < 4; ++i) {
-            z[i] = acc[0][i];
-            if (PAIRED)
-                u[i] = acc[J - 1][i];
-        }
-        const bool two = a.act == EPL_ACT_SWIGLU_GRAD;
-        const int cols = out_cols(a);
-        if (live) {
-            finish<4>(a, row, nq, b, bu, side_of<4>(a, row, nq), z, u);
-            if (a.y) {
-                epl_product::store_out<4>(a, row * cols + nq, z);
-                if (two)
-                    epl_product::store_out<4>(a, row * cols + F + nq, u);
-            }
-        }
-        if (!a.codes)
-            continue;
-        for (int h = 0; h < (two ? 2 : 1); ++h) {
-            float v = in ? largest(h ? u : z) : 0.0f;
-            v = fmaxf(v, __shfl_xor(v, 16));
-            v = fmaxf(v, __shfl_xor(v, 32));
-            most[h][wave][r] = v;
-        }
-        __syncthreads();
-        for (int h = 0; h < (two ? 2 : 1); ++h) {
-            float v = 0.0f;
-            for (int i = 0; i < 8; ++i)
-                v = fmaxf(v, most[h][i][r]);
-            const Factor f = epl_cast::factor_of(v, a.cs.format == EPL_SCALE_UE8M0);
-            if (live)
-                store_codes<4>(a, row * cols + h * F + nq, h ? u : z, f);
-            if (live && wave == 0 && q == 0)
-                epl_cast::store_scale(a.cs, row, (h * F + n) / kGroup, f);
-        }
-        __syncthreads();
+    for (int m = 0; m < cnt; m += 32) {
+        if (cnt - m <= 16)
+            few_rows<PAIRED, G, WAVES, 1>(a, e, lo + m, cnt - m, nb, red, most);
+        else
+            few_rows<PAIRED, G, WAVES, 2>(a, e, lo + m, min(cnt - m, 32), nb, red, most);
     }
 }
 
