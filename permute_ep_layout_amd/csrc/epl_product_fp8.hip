@@ -195,7 +195,7 @@ int epl_expert_product_fp8(const epl_product_fp8_desc *p, const uint8_t *x, cons
         else if (quantized)
             launch_few<false, 8, 16>(a, s);
         else
-            launch_few<false, 2, 8>(a, s);
+            launch_few<false, 4, 8>(a, s);
         return launch_status();
     }
     a.max_parts = max_parts(a.K);

@@ -55,6 +55,15 @@ __device__ __forceinline__ int out_cols(const Args &a)
     return a.act == EPL_ACT_SWIGLU ? a.N / 2 : a.act == EPL_ACT_SWIGLU_GRAD ? 2 * a.N : a.N;
 }
 
+// The scale of block nb of an expert's columns and block b of the contraction
+// (weight [E, N, K]).
+__device__ __forceinline__ float weight_scale(const Args &a, int e, int nb, int b)
+{
+    const int64_t at = ((int64_t)e * blocks_of(a.N) + nb) * blocks_of(a.K) + b;
+    return a.ws_bytes ? epl_cast::power_of(static_cast<const uint8_t *>(a.wscale)[at])
+                      : static_cast<const float *>(a.wscale)[at];
+}
+
 // The finished values of C columns n .. of one row, from z, product and bias: z is
 // column n of y, and u column N + n (gradient of the gated activation). Of the
 // gated activation z and u are the gate's and the up half's product, and z the
@@ -659,53 +668,50 @@ __global__ __launch_bounds__(tile_threads(BN)) void join_kernel(Args a, int grid
 // instruction. A workgroup takes G times 16 columns of y for an expert (of the
 // gated activation as many of each half), a wave 16 of them; the KS waves of
 // the same columns take every KS-th block of the contraction each and add
-// their sums through LDS in order. Workgroups start at different places of the
+// their sums through LDS in order. The rows and all scales come through LDS,
+// where the G waves share them (from memory into each wave's registers 8 x 8
+// rows, 7168 -> 4096 took 61 us, 8 x 1 48: their bytes are few but go through
+// the same caches G times). Workgroups start at different places of the
 // contraction and come round, as those of the bf16 products.
 
 template <int WAVES>
 constexpr int few_threads() { return WAVES * 64; }
 
-// The scales of `U` blocks as they lie: of a row, and of a lane's 4 columns.
-__device__ __forceinline__ uint32_t raw_scale(const char *at, bool byte)
-{
-    return byte ? *reinterpret_cast<const uint8_t *>(at) : *reinterpret_cast<const uint32_t *>(at);
-}
+// Blocks of the contraction that LDS holds the rows of at a time: 128 KB of
+// them, or 64 KB where two workgroups share a CU.
+template <int WAVES, int MT>
+constexpr int few_blocks() { return (WAVES == 16 ? 64 : 32) / MT; }
 
-__device__ __forceinline__ float scale_value(uint32_t v, bool byte)
-{
-    return byte ? epl_cast::power_of(v) : __uint_as_float(v);
-}
+struct FewShared {
+    uint8_t *x;               // [blocks][16 MT][128], pieces swizzled by row
+    float *sx, *sw;           // [blocks][16 MT], [blocks][4]
+    f32x4 *red;               // in x, when that has been read
+    float *most;
+};
 
 template <bool PAIRED, int G, int WAVES, int MT>
-__device__ __forceinline__ void few_rows(const Args &a, int e, int64_t row0, int left, int nb, f32x4 *red,
-                                         float *most)
+__device__ __forceinline__ void few_rows(const Args &a, int e, int64_t row0, int left, int nb, const FewShared &l)
 {
-    constexpr int J = PAIRED ? 2 : 1, KS = WAVES / G, U = PAIRED || MT == 2 ? 2 : 4;
+    constexpr int J = PAIRED ? 2 : 1, KS = WAVES / G, U = PAIRED ? 2 : 4, M = 16 * MT;
+    constexpr int SEG = few_blocks<WAVES, MT>();
     static_assert(KS >= MT, "a row tile's epilogue has waves of its own");
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), g = wave % G, ks = wave / G;
     const int F = PAIRED ? a.N / 2 : a.N, kb = blocks_of(a.K), nblocks = blocks_of(a.N);
     const int n0 = (nb * G + g) * 16;                       // the wave's first column
     const int nq = min(n0 + q * 4, F - 4);                  // first column of the lane's quad
+    f32x4 *const red = l.red;
+    float *const most = l.most;
     const auto rw = rsrc(reinterpret_cast<const char *>(a.w8 + (int64_t)e * a.N * a.K), a.N * a.K);
     const auto rx = rsrc(reinterpret_cast<const char *>(a.x8 + row0 * a.K), left * a.K);
-    uint32_t ow[J], ox[MT];
-    const char *pw[J], *px[MT];                             // scales
-    const bool wbyte = a.ws_bytes, xbyte = a.xs.format == EPL_SCALE_UE8M0;
+    uint32_t ow[J];
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
+    for (int j = 0; j < J; ++j)
         ow[j] = (uint32_t)(min(n0 + r, F - 1) + j * F) * a.K + q * 16;
-        pw[j] = static_cast<const char *>(a.wscale) +
-                ((int64_t)e * nblocks * kb + (int64_t)((j * F + nq) / kGroup) * kb) * (wbyte ? 1 : 4);
-    }
-    // (rows beyond the block: zeros, and the last row's scales)
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        const int64_t p = row0 + min(i * 16 + r, left - 1);
-        ox[i] = i * 16 + r < left ? (uint32_t)(i * 16 + r) * a.K + q * 16 : 0x80000000u;
-        px[i] = static_cast<const char *>(a.xs.at) + (xbyte ? p : epl_cast::scale_index(a.xs, p, 0)) * 4;
-    }
-    const int64_t x_step = xbyte ? a.xs.rows * 4 : a.xs.format == EPL_SCALE_F32_RECT ? (int64_t)a.xs.cap * 4 : 4;
+    // scales of the weight: of the workgroup's block of columns, and of the two
+    // that the up half's columns may lie in
+    const int wb0 = nb * G * 16 / kGroup, ub0 = (F + nb * G * 16) / kGroup;
+    const int at_u = PAIRED ? 1 + (F + nq) / kGroup - ub0 : 0;
     f32x4 acc[MT][J];
 #pragma unroll
     for (int i = 0; i < MT; ++i)
@@ -714,57 +720,79 @@ __device__ __forceinline__ void few_rows(const Args &a, int e, int64_t row0, int
             acc[i][j] = f32x4{0, 0, 0, 0};
 
     const int start = (int)((uint32_t)(e * 13 + nb * 3) % (uint32_t)kb);
-    for (int p = ks; p < kb; p += KS * U) {
-        i32x4 fw[U][J][2], fx[U][MT][2];
-        uint32_t sw[U][J], sx[U][MT];
-        int at[U];
+    auto block_at = [&](int v) { return v + start < kb ? v + start : v + start - kb; };
+    struct Chunk {
+        i32x4 w[U][J][2];
+    };
+    for (int v0 = 0; v0 < kb; v0 += SEG) {
+        const int v1 = min(v0 + SEG, kb);
+        // weights of the positions p, p + KS, .. of this segment
+        auto load = [&](int p) {
+            Chunk c;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int v = p + u * KS, b = v + start < kb ? v + start : v + start - kb, k = b * kGroup;
-            at[u] = v < kb ? b : 0;
-            const bool lo = v < kb && k + q * 16 < a.K, hi = v < kb && k + q * 16 + 64 < a.K;
-#pragma unroll
-            for (int j = 0; j < J; ++j) {
-                fw[u][j][0] = __builtin_bit_cast(
-                    i32x4, __builtin_amdgcn_raw_buffer_load_b128(rw, (int)(lo ? ow[j] : 0x80000000u), k, 0));
-                fw[u][j][1] = __builtin_bit_cast(
-                    i32x4, __builtin_amdgcn_raw_buffer_load_b128(rw, (int)(hi ? ow[j] + 64 : 0x80000000u), k, 0));
-            }
-#pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                fx[u][i][0] = __builtin_bit_cast(
-                    i32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, (int)(lo ? ox[i] : 0x80000000u), k, 0));
-                fx[u][i][1] = __builtin_bit_cast(
-                    i32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, (int)(hi ? ox[i] + 64 : 0x80000000u), k, 0));
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-                sx[u][i] = raw_scale(px[i] + (xbyte ? (at[u] >> 2) * x_step + (at[u] & 3) : at[u] * x_step), xbyte);
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int j = 0; j < J; ++j)
-                sw[u][j] = raw_scale(pw[j] + at[u] * (wbyte ? 1 : 4), wbyte);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-#pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                const i32x8 x = __builtin_shufflevector(fx[u][i][0], fx[u][i][1], 0, 1, 2, 3, 4, 5, 6, 7);
+            for (int u = 0; u < U; ++u) {
+                const int v = p + u * KS, k = block_at(min(v, kb - 1)) * kGroup;
+                const bool lo = v < v1 && k + q * 16 < a.K, hi = v < v1 && k + q * 16 + 64 < a.K;
 #pragma unroll
                 for (int j = 0; j < J; ++j) {
-                    const i32x8 w = __builtin_shufflevector(fw[u][j][0], fw[u][j][1], 0, 1, 2, 3, 4, 5, 6, 7);
-                    const f32x4 part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                        w, x, f32x4{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
-                    acc[i][j] = scaled(part, scale_value(sx[u][i], xbyte) * scale_value(sw[u][j], wbyte), acc[i][j]);
+                    c.w[u][j][0] = __builtin_bit_cast(
+                        i32x4, __builtin_amdgcn_raw_buffer_load_b128(rw, (int)(lo ? ow[j] : 0x80000000u), k, 0));
+                    c.w[u][j][1] = __builtin_bit_cast(
+                        i32x4, __builtin_amdgcn_raw_buffer_load_b128(rw, (int)(hi ? ow[j] + 64 : 0x80000000u), k, 0));
                 }
             }
+            return c;
+        };
+        auto multiply = [&](const Chunk &c, int p) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int at = min(p + u * KS, v1 - 1) - v0;
+                const float *sw = l.sw + at * 4;
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    const uint8_t *row = l.x + (at * M + i * 16 + r) * 128;
+                    const i32x4 x0 = *reinterpret_cast<const i32x4 *>(row + (q ^ swz(r)) * 16);
+                    const i32x4 x1 = *reinterpret_cast<const i32x4 *>(row + ((4 + q) ^ swz(r)) * 16);
+                    const i32x8 x = __builtin_shufflevector(x0, x1, 0, 1, 2, 3, 4, 5, 6, 7);
+                    const float sx = l.sx[at * M + i * 16 + r];
+#pragma unroll
+                    for (int j = 0; j < J; ++j) {
+                        const i32x8 w = __builtin_shufflevector(c.w[u][j][0], c.w[u][j][1], 0, 1, 2, 3, 4, 5, 6, 7);
+                        const f32x4 part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                            w, x, f32x4{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
+                        acc[i][j] = scaled(part, sx * sw[j ? at_u : 0], acc[i][j]);
+                    }
+                }
+            }
+        };
+        Chunk c = load(v0 + ks);
+        __syncthreads();                     // the segment, and the rows, before have been read
+        for (int i = wave; i < (v1 - v0) * (M / 8); i += WAVES) {
+            const int v = i / (M / 8), row = i % (M / 8) * 8 + (lane >> 3), p = (lane & 7) ^ swz(row);
+            const int k = block_at(v0 + v) * kGroup;
+            dma(rx, k + p * 16 < a.K ? (uint32_t)row * a.K + k + p * 16 : 0x80000000u,
+                reinterpret_cast<uint16_t *>(l.x + i * 1024));
         }
+        for (int i = tid; i < (v1 - v0) * M; i += WAVES * 64)
+            l.sx[i] = i % M < left ? epl_cast::load_scale(a.xs, row0 + i % M, block_at(v0 + i / M)) : 0.0f;
+        for (int i = tid; i < (v1 - v0) * 4; i += WAVES * 64) {
+            const int n = i % 4 == 0 ? wb0 : ub0 + i % 4 - 1;
+            if (i % 4 < (PAIRED ? 3 : 1) && n < nblocks)
+                l.sw[i] = weight_scale(a, e, n, block_at(v0 + i / 4));
+        }
+        landed();
+        int p = v0 + ks;
+        for (; p + KS * U < v1; p += 2 * KS * U) {
+            const Chunk d = load(p + KS * U);
+            multiply(c, p);
+            c = load(p + 2 * KS * U);
+            multiply(d, p + KS * U);
+        }
+        if (p < v1)
+            multiply(c, p);
     }
 
-    __syncthreads();           // red and most may still be read for the rows before
+    __syncthreads();           // red lies where other waves may still read x
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -833,16 +861,21 @@ __device__ __forceinline__ void few_rows(const Args &a, int e, int64_t row0, int
 template <bool PAIRED, int G, int WAVES>
 __global__ __launch_bounds__(few_threads<WAVES>(), 4) void few_rows_kernel(Args a)
 {
-    __shared__ f32x4 red[WAVES * 2 * (PAIRED ? 2 : 1) * 64];
+    constexpr int SEG = few_blocks<WAVES, 1>();
+    __shared__ __align__(1024) uint8_t x[SEG * 16 * 128];
+    __shared__ float sx[SEG * 16], sw[SEG * 4];
+    static_assert(sizeof(x) >= WAVES * 2 * (PAIRED ? 2 : 1) * 64 * sizeof(f32x4), "the sums fit x");
+    f32x4 *const red = reinterpret_cast<f32x4 *>(x);
     __shared__ float most[G == 8 ? 2 * 2 * G * 16 : 1];
     const int e = blockIdx.y, nb = blockIdx.x;
+    const FewShared l{x, sx, sw, red, most};
     int64_t lo;
     const int cnt = block_of(a, e, lo);
     for (int m = 0; m < cnt; m += 32) {
         if (cnt - m <= 16)
-            few_rows<PAIRED, G, WAVES, 1>(a, e, lo + m, cnt - m, nb, red, most);
+            few_rows<PAIRED, G, WAVES, 1>(a, e, lo + m, cnt - m, nb, l);
         else
-            few_rows<PAIRED, G, WAVES, 2>(a, e, lo + m, min(cnt - m, 32), nb, red, most);
+            few_rows<PAIRED, G, WAVES, 2>(a, e, lo + m, min(cnt - m, 32), nb, l);
     }
 }
 
