@@ -91,12 +91,46 @@ int64_t tiles_of(const epl_product_fp8_desc &p, Kind k)
     return product_tiles(p.num_rows, p.num_experts, p.out_cols, k);
 }
 
-template <bool PAIRED, int G, int WAVES>
-void launch_few(const P::Args &a, hipStream_t s)
+// Columns of y of a workgroup of the few-rows kernel: a whole group where the
+// result is cast, else half of one.
+int few_columns(const epl_product_fp8_desc &p) { return p.codes_scale_format != EPL_SCALE_NONE ? 128 : 64; }
+
+int64_t few_groups(const epl_product_fp8_desc &p)
 {
-    const int groups = ((PAIRED ? a.N / 2 : a.N) + G * 16 - 1) / (G * 16);
-    hipLaunchKernelGGL((P::few_rows_kernel<PAIRED, G, WAVES>), dim3((unsigned)groups, (unsigned)a.E),
-                       dim3(P::few_threads<WAVES>()), 0, s, a);
+    const int cols = p.activation == EPL_ACT_SWIGLU ? p.out_cols / 2 : p.out_cols;
+    return (cols + few_columns(p) - 1) / few_columns(p);
+}
+
+// Parts that its contraction is shared out to: so many that every CU has a
+// workgroup, of eight blocks each at least.
+int few_parts(const epl_product_fp8_desc &p)
+{
+    const int64_t groups = few_groups(p) * p.num_experts, blocks = (p.in_cols + 127) / 128;
+    return (int)std::max<int64_t>(1, std::min<int64_t>(kCus / std::max<int64_t>(groups, 1), blocks / 8));
+}
+
+size_t few_workspace(const epl_product_fp8_desc &p)
+{
+    const int parts = few_parts(p);
+    const int paired = p.activation == EPL_ACT_SWIGLU ? 2 : 1;
+    return parts < 2 ? 0
+                     : kHeaderBytes + (size_t)parts * p.num_experts * few_groups(p) * P::kFewMost *
+                                          few_columns(p) * paired * sizeof(float);
+}
+
+template <bool PAIRED, int G>
+int launch_few(const P::Args &a, unsigned groups, int parts, hipStream_t s)
+{
+    constexpr int waves = 2 * G;
+    const dim3 grid(groups, (unsigned)a.E);
+    hipLaunchKernelGGL((P::few_rows_kernel<PAIRED, G, waves>), dim3(groups, (unsigned)a.E, (unsigned)parts),
+                       dim3(P::few_threads<waves>()), 0, s, a);
+    int rc = launch_status();
+    if (rc == EPL_OK && parts > 1) {
+        hipLaunchKernelGGL((P::few_join_kernel<PAIRED, G>), grid, dim3(G * 128), 0, s, a, parts);
+        rc = launch_status();
+    }
+    return rc;
 }
 
 template <int SIDE, bool QT, bool CODES>
@@ -136,7 +170,7 @@ size_t epl_product_fp8_workspace_bytes(const epl_product_fp8_desc *p)
     if (!desc_ok(p))
         return 0;
     const Kind k = kind_of(*p);
-    return tile_workspace(k, tiles_of(*p, k), max_parts(p->in_cols));
+    return k == kFew ? few_workspace(*p) : tile_workspace(k, tiles_of(*p, k), max_parts(p->in_cols));
 }
 
 int epl_expert_product_fp8(const epl_product_fp8_desc *p, const uint8_t *x, const void *x_scale,
@@ -190,13 +224,12 @@ int epl_expert_product_fp8(const epl_product_fp8_desc *p, const uint8_t *x, cons
     hipStream_t s = static_cast<hipStream_t>(stream);
     const Kind k = kind_of(*p);
     if (k == kFew) {
+        use_workspace(a, workspace);
+        const unsigned groups = (unsigned)few_groups(*p);
+        const int parts = workspace ? few_parts(*p) : 1;
         if (p->activation == EPL_ACT_SWIGLU)
-            launch_few<true, 8, 16>(a, s);
-        else if (quantized)
-            launch_few<false, 8, 16>(a, s);
-        else
-            launch_few<false, 4, 8>(a, s);
-        return launch_status();
+            return quantized ? launch_few<true, 8>(a, groups, parts, s) : launch_few<true, 4>(a, groups, parts, s);
+        return quantized ? launch_few<false, 8>(a, groups, parts, s) : launch_few<false, 4>(a, groups, parts, s);
     }
     a.max_parts = max_parts(a.K);
     a.stages = stages_of(a.K, P::kGroup);

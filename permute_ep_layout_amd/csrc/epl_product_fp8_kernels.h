@@ -673,14 +673,22 @@ __global__ __launch_bounds__(tile_threads(BN)) void join_kernel(Args a, int grid
 // rows, 7168 -> 4096 took 61 us, 8 x 1 48: their bytes are few but go through
 // the same caches G times). Workgroups start at different places of the
 // contraction and come round, as those of the bf16 products.
+//
+// A CU reads no more than some 35 GB/s in this way. Where the columns are too
+// few for a workgroup on every CU, `parts` workgroups share the contraction,
+// and few_join_kernel adds their sums in order.
 
 template <int WAVES>
 constexpr int few_threads() { return WAVES * 64; }
 
 // Blocks of the contraction that LDS holds the rows of at a time: 128 KB of
-// them, or 64 KB where two workgroups share a CU.
+// them, or 64 KB where two workgroups share a CU. A thread loads one scale of
+// the rows for each time.
 template <int WAVES, int MT>
-constexpr int few_blocks() { return (WAVES == 16 ? 64 : 32) / MT; }
+constexpr int few_blocks() { return WAVES * 4 / MT; }
+
+// Rows of an expert up to which its contraction is shared.
+constexpr int kFewMost = 32;
 
 struct FewShared {
     uint8_t *x;               // [blocks][16 MT][128], pieces swizzled by row
@@ -689,8 +697,83 @@ struct FewShared {
     float *most;
 };
 
+// All loads are done but the last N that this wave began.
+template <int N>
+__device__ __forceinline__ void all_but()
+{
+    static_assert(N < 64, "the counter's width");
+    __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4) << 14 | 0x0070);       // (and lgkmcnt(0))
+}
+
+// The epilogue of row tile i (16 rows from row0 + 16 i on) by the G waves of a
+// workgroup that hold its sums. All waves of the workgroup come here; `mine`:
+// this one holds sums.
+template <bool PAIRED, int G, int MT>
+__device__ __forceinline__ void few_finish(const Args &a, int e, int64_t row0, int left, int nb, int g, int i,
+                                           bool mine, const f32x4 (&sum)[PAIRED ? 2 : 1], float *most)
+{
+    const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+    const int F = PAIRED ? a.N / 2 : a.N, n0 = (nb * G + g) * 16, nq = min(n0 + q * 4, F - 4);
+    const int64_t row = row0 + min(i * 16 + r, left - 1);
+    const bool live = mine && i * 16 + r < left && n0 + q * 4 < F;
+    const bool two = !PAIRED && a.act == EPL_ACT_SWIGLU_GRAD;
+    const int cols = out_cols(a);
+    float z[4] = {}, u[4] = {};
+    if (mine) {
+        float b[4], bu[4];
+        bias_of<4>(a, e, nq, b);
+        bias_of<4>(a, e, PAIRED ? F + nq : nq, bu);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            z[k] = sum[0][k] + b[k];
+            if (PAIRED)
+                u[k] = sum[PAIRED ? 1 : 0][k] + bu[k];
+        }
+        Kept<4> kept;
+        finish<4, PAIRED>(a, side_of<4>(a, row, nq), z, u, kept);
+        if (live)
+            store_row<4, PAIRED>(a, row, nq, z, u, kept);
+    }
+    if constexpr (G == 8) {
+        if (!a.codes)
+            return;
+        if (mine) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float v = largest(h ? u : z);
+                v = fmaxf(v, __shfl_xor(v, 16));
+                v = fmaxf(v, __shfl_xor(v, 32));
+                if (q == 0)
+                    most[((h * MT + i) * G + g) * 16 + r] = v;
+            }
+        }
+        __syncthreads();
+        if (live) {
+            for (int h = 0; h < (two ? 2 : 1); ++h) {
+                float v = 0.0f;
+#pragma unroll
+                for (int k = 0; k < G; ++k)
+                    v = fmaxf(v, most[((h * MT + i) * G + k) * 16 + r]);
+                const Factor f = epl_cast::factor_of(v, a.cs.format == EPL_SCALE_UE8M0);
+                store_codes<4>(a, row * cols + h * F + nq, h ? u : z, f);
+                if (g == 0 && q == 0)
+                    epl_cast::store_scale(a.cs, row, (h * F + nq) / kGroup, f);
+            }
+        }
+    }
+}
+
+// Where the sums of a shared contraction wait: quad j of the wave of columns g,
+// row tile i, of part z.
+template <int J, int G>
+__device__ __forceinline__ f32x4 *few_slot(const Args &a, int z, int e, int nb, int groups, int i, int g)
+{
+    return a.ws + (((((int64_t)z * a.E + e) * groups + nb) * 2 + i) * G + g) * J * 64;
+}
+
 template <bool PAIRED, int G, int WAVES, int MT>
-__device__ __forceinline__ void few_rows(const Args &a, int e, int64_t row0, int left, int nb, const FewShared &l)
+__device__ __forceinline__ void few_rows(const Args &a, int e, int64_t row0, int left, int nb, bool shared,
+                                         const FewShared &l)
 {
     constexpr int J = PAIRED ? 2 : 1, KS = WAVES / G, U = PAIRED ? 2 : 4, M = 16 * MT;
     constexpr int SEG = few_blocks<WAVES, MT>();
@@ -701,7 +784,6 @@ __device__ __forceinline__ void few_rows(const Args &a, int e, int64_t row0, int
     const int n0 = (nb * G + g) * 16;                       // the wave's first column
     const int nq = min(n0 + q * 4, F - 4);                  // first column of the lane's quad
     f32x4 *const red = l.red;
-    float *const most = l.most;
     const auto rw = rsrc(reinterpret_cast<const char *>(a.w8 + (int64_t)e * a.N * a.K), a.N * a.K);
     const auto rx = rsrc(reinterpret_cast<const char *>(a.x8 + row0 * a.K), left * a.K);
     uint32_t ow[J];
@@ -719,19 +801,22 @@ __device__ __forceinline__ void few_rows(const Args &a, int e, int64_t row0, int
         for (int j = 0; j < J; ++j)
             acc[i][j] = f32x4{0, 0, 0, 0};
 
-    const int start = (int)((uint32_t)(e * 13 + nb * 3) % (uint32_t)kb);
-    auto block_at = [&](int v) { return v + start < kb ? v + start : v + start - kb; };
+    // this workgroup's part of the blocks
+    const int z = shared ? (int)blockIdx.z : 0, parts = shared ? (int)gridDim.z : 1;
+    const int first = kb * z / parts, own = kb * (z + 1) / parts - first;
+    const int start = (int)((uint32_t)(e * 13 + nb * 3) % (uint32_t)max(own, 1));
+    auto block_at = [&](int v) { return first + (v + start < own ? v + start : v + start - own); };
     struct Chunk {
         i32x4 w[U][J][2];
     };
-    for (int v0 = 0; v0 < kb; v0 += SEG) {
-        const int v1 = min(v0 + SEG, kb);
+    for (int v0 = 0; v0 < own; v0 += SEG) {
+        const int v1 = min(v0 + SEG, own);
         // weights of the positions p, p + KS, .. of this segment
         auto load = [&](int p) {
             Chunk c;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int v = p + u * KS, k = block_at(min(v, kb - 1)) * kGroup;
+                const int v = p + u * KS, k = block_at(min(v, own - 1)) * kGroup;
                 const bool lo = v < v1 && k + q * 16 < a.K, hi = v < v1 && k + q * 16 + 64 < a.K;
 #pragma unroll
                 for (int j = 0; j < J; ++j) {
@@ -765,7 +850,6 @@ __device__ __forceinline__ void few_rows(const Args &a, int e, int64_t row0, int
                 }
             }
         };
-        Chunk c = load(v0 + ks);
         __syncthreads();                     // the segment, and the rows, before have been read
         for (int i = wave; i < (v1 - v0) * (M / 8); i += WAVES) {
             const int v = i / (M / 8), row = i % (M / 8) * 8 + (lane >> 3), p = (lane & 7) ^ swz(row);
@@ -773,23 +857,30 @@ __device__ __forceinline__ void few_rows(const Args &a, int e, int64_t row0, int
             dma(rx, k + p * 16 < a.K ? (uint32_t)row * a.K + k + p * 16 : 0x80000000u,
                 reinterpret_cast<uint16_t *>(l.x + i * 1024));
         }
-        for (int i = tid; i < (v1 - v0) * M; i += WAVES * 64)
-            l.sx[i] = i % M < left ? epl_cast::load_scale(a.xs, row0 + i % M, block_at(v0 + i / M)) : 0.0f;
-        for (int i = tid; i < (v1 - v0) * 4; i += WAVES * 64) {
-            const int n = i % 4 == 0 ? wb0 : ub0 + i % 4 - 1;
-            if (i % 4 < (PAIRED ? 3 : 1) && n < nblocks)
-                l.sw[i] = weight_scale(a, e, n, block_at(v0 + i / 4));
+        float sx = 0.0f, sw = 0.0f;
+        if (tid / M < v1 - v0 && tid % M < left)
+            sx = epl_cast::load_scale(a.xs, row0 + tid % M, block_at(v0 + tid / M));
+        if (tid / 4 < v1 - v0) {
+            const int n = tid % 4 == 0 ? wb0 : ub0 + tid % 4 - 1;
+            if (tid % 4 < (PAIRED ? 3 : 1) && n < nblocks)
+                sw = weight_scale(a, e, n, block_at(v0 + tid / 4));
         }
-        landed();
+        // the first weights are on their way while the rows are waited for
         int p = v0 + ks;
-        for (; p + KS * U < v1; p += 2 * KS * U) {
-            const Chunk d = load(p + KS * U);
+        Chunk c = load(p), d = load(p + KS * U);
+        l.sx[tid] = sx;
+        if (tid < SEG * 4)
+            l.sw[tid] = sw;
+        all_but<4 * U * J>();
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+        for (; p < v1; p += 2 * KS * U) {
             multiply(c, p);
             c = load(p + 2 * KS * U);
             multiply(d, p + KS * U);
+            d = load(p + 3 * KS * U);
         }
-        if (p < v1)
-            multiply(c, p);
     }
 
     __syncthreads();           // red lies where other waves may still read x
@@ -800,14 +891,8 @@ __device__ __forceinline__ void few_rows(const Args &a, int e, int64_t row0, int
             red[((ks * MT + i) * J + j) * G * 64 + g * 64 + lane] = acc[i][j];
     __syncthreads();
     // waves ks = 0 .. MT - 1 finish a row tile each
-    const int row_in = ks * 16 + r;
-    const int64_t row = row0 + min(row_in, left - 1);
-    const bool live = ks < MT && row_in < left && n0 + q * 4 < F;
-    const bool two = !PAIRED && a.act == EPL_ACT_SWIGLU_GRAD;
-    const int cols = out_cols(a);
-    float z[4] = {}, u[4] = {};
+    f32x4 sum[J] = {};
     if (ks < MT) {
-        f32x4 sum[J];
 #pragma unroll
         for (int j = 0; j < J; ++j) {
             sum[j] = red[(ks * J + j) * G * 64 + g * 64 + lane];
@@ -815,47 +900,17 @@ __device__ __forceinline__ void few_rows(const Args &a, int e, int64_t row0, int
             for (int o = 1; o < KS; ++o)
                 sum[j] += red[((o * MT + ks) * J + j) * G * 64 + g * 64 + lane];
         }
-        float b[4], bu[4];
-        bias_of<4>(a, e, nq, b);
-        bias_of<4>(a, e, PAIRED ? F + nq : nq, bu);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            z[i] = sum[0][i] + b[i];
-            if (PAIRED)
-                u[i] = sum[J - 1][i] + bu[i];
-        }
-        Kept<4> kept;
-        finish<4, PAIRED>(a, side_of<4>(a, row, nq), z, u, kept);
-        if (live)
-            store_row<4, PAIRED>(a, row, nq, z, u, kept);
     }
-    if constexpr (G == 8) {
-        if (!a.codes)
-            return;
+    if (shared) {
         if (ks < MT) {
+            f32x4 *const to = few_slot<J, G>(a, z, e, nb, gridDim.x, ks, g) + lane;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float v = largest(h ? u : z);
-                v = fmaxf(v, __shfl_xor(v, 16));
-                v = fmaxf(v, __shfl_xor(v, 32));
-                if (q == 0)
-                    most[((h * MT + ks) * G + g) * 16 + r] = v;
-            }
+            for (int j = 0; j < J; ++j)
+                to[j * 64] = sum[j];
         }
-        __syncthreads();
-        if (live) {
-            for (int h = 0; h < (two ? 2 : 1); ++h) {
-                float v = 0.0f;
-#pragma unroll
-                for (int i = 0; i < G; ++i)
-                    v = fmaxf(v, most[((h * MT + ks) * G + i) * 16 + r]);
-                const Factor f = epl_cast::factor_of(v, a.cs.format == EPL_SCALE_UE8M0);
-                store_codes<4>(a, row * cols + h * F + nq, h ? u : z, f);
-                if (g == 0 && q == 0)
-                    epl_cast::store_scale(a.cs, row, (h * F + nq) / kGroup, f);
-            }
-        }
+        return;
     }
+    few_finish<PAIRED, G, MT>(a, e, row0, left, nb, g, ks, ks < MT, sum, l.most);
 }
 
 template <bool PAIRED, int G, int WAVES>
@@ -865,18 +920,46 @@ __global__ __launch_bounds__(few_threads<WAVES>(), 4) void few_rows_kernel(Args 
     __shared__ __align__(1024) uint8_t x[SEG * 16 * 128];
     __shared__ float sx[SEG * 16], sw[SEG * 4];
     static_assert(sizeof(x) >= WAVES * 2 * (PAIRED ? 2 : 1) * 64 * sizeof(f32x4), "the sums fit x");
-    f32x4 *const red = reinterpret_cast<f32x4 *>(x);
     __shared__ float most[G == 8 ? 2 * 2 * G * 16 : 1];
     const int e = blockIdx.y, nb = blockIdx.x;
-    const FewShared l{x, sx, sw, red, most};
+    const FewShared l{x, sx, sw, reinterpret_cast<f32x4 *>(x), most};
     int64_t lo;
     const int cnt = block_of(a, e, lo);
+    const bool shared = gridDim.z > 1 && cnt <= kFewMost;
+    if (!shared && blockIdx.z > 0)
+        return;                              // (an expert of many rows: the first part takes it all)
     for (int m = 0; m < cnt; m += 32) {
         if (cnt - m <= 16)
-            few_rows<PAIRED, G, WAVES, 1>(a, e, lo + m, cnt - m, nb, l);
+            few_rows<PAIRED, G, WAVES, 1>(a, e, lo + m, cnt - m, nb, shared, l);
         else
-            few_rows<PAIRED, G, WAVES, 2>(a, e, lo + m, min(cnt - m, 32), nb, l);
+            few_rows<PAIRED, G, WAVES, 2>(a, e, lo + m, min(cnt - m, 32), nb, shared, l);
     }
+}
+
+// Adds the parts of shared contractions, in order, and runs their epilogue: a
+// workgroup of 2 G waves takes what one of few_rows_kernel's takes.
+template <bool PAIRED, int G>
+__global__ __launch_bounds__(G * 128) void few_join_kernel(Args a, int parts)
+{
+    constexpr int J = PAIRED ? 2 : 1;
+    __shared__ float most[G == 8 ? 2 * 2 * G * 16 : 1];
+    const int e = blockIdx.y, nb = blockIdx.x, lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = wave % G, i = wave / G;
+    int64_t lo;
+    const int cnt = block_of(a, e, lo);
+    if (cnt == 0 || cnt > kFewMost)
+        return;
+    const bool mine = i * 16 < cnt;
+    f32x4 sum[J] = {};
+    if (mine) {
+        for (int z = 0; z < parts; ++z) {
+            const f32x4 *from = few_slot<J, G>(a, z, e, nb, gridDim.x, i, g) + lane;
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                sum[j] += from[j * 64];
+        }
+    }
+    few_finish<PAIRED, G, 2>(a, e, lo, cnt, nb, g, i, mine, sum, most);
 }
 
 }  // namespace epl_product8
