@@ -913,10 +913,9 @@ def _need_weight_scales(t, fmt, E, rows, cols, dev):
 
 
 def _cast_args(p: Cast, values, value_cols, codes, scale, expert_start_loc,
-               num_tokens_per_expert, where):
+               num_tokens_per_expert):
     """The checks that both directions of a cast share; the device."""
     torch = _torch()
-    _check(epl_cast_validate(p), where)
     rows, C = p.num_rows, p.cols
     dev = getattr(values, "device", None)
     _need_same(values, "values", torch.bfloat16 if p.value_type == EPL_OUT_BF16 else torch.float32,
@@ -932,21 +931,19 @@ def _cast_args(p: Cast, values, value_cols, codes, scale, expert_start_loc,
 
 def epl_quantize(p: Cast, x, expert_start_loc, num_tokens_per_expert, codes, scale, stream=None):
     dev = _cast_args(p, x, p.cols * (2 if p.activation == EPL_ACT_SWIGLU else 1), codes, scale,
-                     expert_start_loc, num_tokens_per_expert, "epl_quantize")
+                     expert_start_loc, num_tokens_per_expert)
     _launch("epl_quantize", dev, stream, ctypes.byref(p), _ptr(x), _ptr(expert_start_loc),
             _ptr(num_tokens_per_expert), _ptr(codes), _ptr(scale))
 
 
 def epl_dequantize(p: Cast, codes, scale, expert_start_loc, num_tokens_per_expert, y, stream=None):
-    dev = _cast_args(p, y, p.cols, codes, scale, expert_start_loc, num_tokens_per_expert,
-                     "epl_dequantize")
+    dev = _cast_args(p, y, p.cols, codes, scale, expert_start_loc, num_tokens_per_expert)
     _launch("epl_dequantize", dev, stream, ctypes.byref(p), _ptr(codes), _ptr(scale),
             _ptr(expert_start_loc), _ptr(num_tokens_per_expert), _ptr(y))
 
 
 def epl_quantize_weight(p: WeightCast, weight, codes, scale, stream=None):
     torch = _torch()
-    _check(epl_weight_cast_validate(p), "epl_quantize_weight")
     E, N, K = p.num_experts, p.out_cols, p.in_cols
     dev = getattr(weight, "device", None)
     _need_same(weight, "weight", torch.bfloat16 if p.value_type == EPL_OUT_BF16 else torch.float32,
@@ -1376,6 +1373,7 @@ def _product_fp8_for(*fields):
 
 
 _FORMATS = {"f32": EPL_SCALE_F32, "ue8m0": EPL_SCALE_UE8M0}
+_CAST_ACTIVATIONS = {"none": EPL_ACT_NONE, "swiglu": EPL_ACT_SWIGLU}
 
 
 def _scale_kind(scale, rows: int, name: str):
@@ -1424,7 +1422,7 @@ def quantize(x, activation: str = "none", scale_format: str = "f32", expert_star
     if stream is not None and x.is_cuda:
         return _run_on(stream, x.device, quantize, x, activation, scale_format, expert_start_loc,
                        num_tokens_per_expert, out, out_scale)
-    act = _named({k: _ACTIVATIONS[k] for k in ("none", "swiglu")}, activation, "activation")
+    act = _named(_CAST_ACTIVATIONS, activation, "activation")
     rows, C = x.shape
     if act == EPL_ACT_SWIGLU:
         if C % 2:

@@ -59,8 +59,11 @@ bool desc_ok(const epl_product_fp8_desc *p)
 }
 
 // Rows an expert, on average, up to which the weights are read straight from
-// memory.
-constexpr int64_t kFewRows = 12;
+// memory, once for every 32 rows of an expert. Measured (this way, tiles), us: 8
+// experts of 24 rows, 7168 -> 4096: 52, 64, gated with its cast 54, 82; of 32, none
+// of them more: 53, 63; but where counts scatter about 32 half of the experts'
+// weights are read twice.
+constexpr int64_t kFewRows = 24;
 
 constexpr Cost cost_of(Kind k) { return k == kLarge ? Cost{13.0, 1.55} : Cost{7.0, 1.1}; }
 
@@ -102,11 +105,16 @@ int64_t few_groups(const epl_product_fp8_desc &p)
 }
 
 // Parts that its contraction is shared out to: so many that every CU has a
-// workgroup, of eight blocks each at least.
+// workgroup, of eight blocks each at least, and where a workgroup's weights, at
+// 35 KB a us, would take so much longer that the join's launch (5 us) pays: 1 expert
+// of one row, 7168 -> 4096, gated: 19 us in 8 parts, 55 whole; 2048 -> 7168: 17 in
+// two, 14 whole.
 int few_parts(const epl_product_fp8_desc &p)
 {
     const int64_t groups = few_groups(p) * p.num_experts, blocks = (p.in_cols + 127) / 128;
-    return (int)std::max<int64_t>(1, std::min<int64_t>(kCus / std::max<int64_t>(groups, 1), blocks / 8));
+    const int64_t parts = std::min<int64_t>(kCus / std::max<int64_t>(groups, 1), blocks / 8);
+    const int64_t bytes = (int64_t)few_columns(p) * (p.activation == EPL_ACT_SWIGLU ? 2 : 1) * p.in_cols;
+    return parts > 1 && bytes - bytes / parts > 5 * 35000 ? (int)parts : 1;
 }
 
 size_t few_workspace(const epl_product_fp8_desc &p)

@@ -775,7 +775,10 @@ template <bool PAIRED, int G, int WAVES, int MT>
 __device__ __forceinline__ void few_rows(const Args &a, int e, int64_t row0, int left, int nb, bool shared,
                                          const FewShared &l)
 {
-    constexpr int J = PAIRED ? 2 : 1, KS = WAVES / G, U = PAIRED ? 2 : 4, M = 16 * MT;
+    constexpr int J = PAIRED ? 2 : 1, KS = WAVES / G, M = 16 * MT;
+    // blocks at a time, two times of them on their way: more spill (8 x 24 rows,
+    // 7168 -> 4096: 56 us with 4, 52 with 2; gated and cast 64 with 2, 54 with 1)
+    constexpr int U = PAIRED ? 1 : MT == 2 ? 2 : 4;
     constexpr int SEG = few_blocks<WAVES, MT>();
     static_assert(KS >= MT, "a row tile's epilogue has waves of its own");
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, q = lane >> 4;
