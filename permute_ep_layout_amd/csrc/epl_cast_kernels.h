@@ -140,8 +140,7 @@ struct Args {
 
 // A workgroup of 4 waves takes tiles of kRows rows by kCols columns: 8 lanes to
 // a group of 128 columns, 16 each, so that a wave reads and writes whole lines
-// of up to 8 groups, and 4 of them are on their way before the first is
-// rounded.
+// of up to 8 groups.
 constexpr int kThreads = 256;
 constexpr int kRows = 16;
 constexpr int kCols = 8 * kGroup;
@@ -214,9 +213,11 @@ __device__ __forceinline__ void each_group(const Args &a, F &&item)
         const int m0 = (mt - pre[e]) * kRows;
         const int rows = min(cnt - m0, kRows), groups = min(S - chunk * 8, 8);
         const int items = rows * groups;
+        const int by = 65536 / groups + 1;     // i / groups = i * by >> 16, i < 128, groups <= 8
+#pragma unroll 2
         for (int i0 = team; i0 < ((items + 31) & ~31); i0 += 32) {
-            const int i = min(i0, items - 1);
-            item(lo + m0 + i / groups, chunk * 8 + i % groups, lane, i0 < items);
+            const int i = min(i0, items - 1), row = i * by >> 16;
+            item(lo + m0 + row, chunk * 8 + i - row * groups, lane, i0 < items);
         }
     }
 }

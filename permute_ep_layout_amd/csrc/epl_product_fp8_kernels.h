@@ -702,7 +702,7 @@ constexpr int kFewMost = 32;
 
 struct FewShared {
     uint8_t *x;               // [blocks][16 MT][128], pieces swizzled by row
-    float *sx, *sw;           // [blocks][16 MT], [blocks][4]
+    float *sx, *sw;           // [blocks + 1][16 MT], [blocks + 1][4], zeros last
     f32x4 *red;               // in x, when that has been read
     float *most;
 };
@@ -844,15 +844,17 @@ __device__ __forceinline__ void few_rows(const Args &a, int e, int64_t row0, int
         auto multiply = [&](const Chunk &c, int p) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int at = min(p + u * KS, v1 - 1) - v0;
-                const float *sw = l.sw + at * 4;
+                // beyond the segment: no weights and no scales (an infinite one times
+                // nothing would be NaN)
+                const int at = min(p + u * KS, v1 - 1) - v0, as = p + u * KS < v1 ? at : SEG;
+                const float *sw = l.sw + as * 4;
 #pragma unroll
                 for (int i = 0; i < MT; ++i) {
                     const uint8_t *row = l.x + (at * M + i * 16 + r) * 128;
                     const i32x4 x0 = *reinterpret_cast<const i32x4 *>(row + (q ^ swz(r)) * 16);
                     const i32x4 x1 = *reinterpret_cast<const i32x4 *>(row + ((4 + q) ^ swz(r)) * 16);
                     const i32x8 x = __builtin_shufflevector(x0, x1, 0, 1, 2, 3, 4, 5, 6, 7);
-                    const float sx = l.sx[at * M + i * 16 + r];
+                    const float sx = l.sx[as * M + i * 16 + r];
 #pragma unroll
                     for (int j = 0; j < J; ++j) {
                         const i32x8 w = __builtin_shufflevector(c.w[u][j][0], c.w[u][j][1], 0, 1, 2, 3, 4, 5, 6, 7);
@@ -878,12 +880,21 @@ __device__ __forceinline__ void few_rows(const Args &a, int e, int64_t row0, int
             if (tid % 4 < (PAIRED ? 3 : 1) && n < nblocks)
                 sw = weight_scale(a, e, n, block_at(v0 + tid / 4));
         }
-        // the first weights are on their way while the rows are waited for
+        // the first weights are on their way while the rows are waited for: they are
+        // the last loads that begin before the wait, and none of them begins after
         int p = v0 + ks;
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
         Chunk c = load(p), d = load(p + KS * U);
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
         l.sx[tid] = sx;
         if (tid < SEG * 4)
             l.sw[tid] = sw;
+        if (tid < M)
+            l.sx[SEG * M + tid] = 0.0f;
+        if (tid < 4)
+            l.sw[SEG * 4 + tid] = 0.0f;
         all_but<4 * U * J>();
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
         __builtin_amdgcn_s_barrier();
@@ -931,7 +942,7 @@ __global__ __launch_bounds__(few_threads<WAVES>(), 4) void few_rows_kernel(Args 
 {
     constexpr int SEG = few_blocks<WAVES, 1>();
     __shared__ __align__(1024) uint8_t x[SEG * 16 * 128];
-    __shared__ float sx[SEG * 16], sw[SEG * 4];
+    __shared__ float sx[SEG * 16 + 32], sw[SEG * 4 + 4];
     static_assert(sizeof(x) >= WAVES * 2 * (PAIRED ? 2 : 1) * 64 * sizeof(f32x4), "the sums fit x");
     __shared__ float most[G == 8 ? 2 * 2 * G * 16 : 1];
     const int e = blockIdx.y, nb = blockIdx.x;
