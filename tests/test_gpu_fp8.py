@@ -669,3 +669,104 @@ def test_two_streams_at_once():
         torch.cuda.current_stream().wait_stream(s)
     for g in got:
         assert torch.equal(g, want)
+
+
+@pytest.mark.parametrize("act,K,N,quantized,out", [
+    ("none", 8240, 48, None, torch.bfloat16), ("swiglu", 4096, 80, None, torch.float32),
+    ("swiglu", 4240, 400, None, torch.bfloat16), ("swiglu", 4096, 256, "f32", torch.float32),
+    ("swiglu_grad", 4112, 128, "ue8m0", torch.float32), ("gelu", 6160, 128, "f32", None),
+])
+@pytest.mark.parametrize("split", [False, True])
+def test_product_few_rows_long_contraction(act, K, N, quantized, out, split):
+    """The contraction shared by workgroups and joined, but for the expert of
+    more than 32 rows; without a workspace, taken in segments of it."""
+    counts, grad = [1, 40, 0, 17, 32], act.endswith("_grad")
+    p = epl.ProductFp8(sum(counts) + 5, 0, 5, K, N, 0, ACTS[act], 1, 1, 0, 1,
+                       FORMATS[quantized] if quantized else 0, 0, 0)
+    assert epl.epl_product_fp8_workspace_bytes(p) > 256
+    check_product(counts, K, N, act=act, quantized=quantized, out=out, split=split, gap=1,
+                  bias=not grad, residual=not grad, pre=not grad)
+
+
+@pytest.mark.parametrize("counts", [[3], [24], [150]])
+@pytest.mark.parametrize("blocks_of_k", [1, 3, 8])
+def test_product_infinite_scales(counts, blocks_of_k):
+    """An infinite scale over finite codes of one sign: infinities, and none of
+    them times a padded zero."""
+    K, rows = 128 * blocks_of_k, counts[0]
+    one = torch.full((rows, K), 0x38, dtype=torch.uint8, device=DEV)
+    scale = torch.ones(rows, blocks_of_k, device=DEV)
+    scale[1, blocks_of_k - 1], scale[2, 0] = math.inf, math.inf
+    w = torch.full((1, 144, K), 0x38, dtype=torch.uint8, device=DEV)
+    ws = torch.ones(1, 2, blocks_of_k, device=DEV)
+    want = torch.full((rows, 144), float(K))
+    want[1:3] = math.inf
+    assert torch.equal(epl.expert_product_fp8(one, scale, w, ws, i32([0]), i32(counts)).cpu(),
+                       want.bfloat16())
+    ws[0, 1, 0] = math.inf
+    want[:, 128:] = math.inf
+    assert torch.equal(epl.expert_product_fp8(one, scale, w, ws, i32([0]), i32(counts)).cpu(),
+                       want.bfloat16())
+
+
+@pytest.mark.parametrize("rows", [5, 150])
+def test_product_exponents_at_their_ends(rows):
+    """A byte of 255 makes its row, or its block's columns, NaN; 0 is 2^-127."""
+    K = 256
+    one = torch.full((rows, K), 0x38, dtype=torch.uint8, device=DEV)
+    w = torch.full((1, 256, K), 0x38, dtype=torch.uint8, device=DEV)
+    power = torch.full((rows, 4), 127, dtype=torch.uint8)
+    power[:, 2:] = 0
+    power[1, 1], power[2, :2] = 255, 0
+    scale = power.view(torch.int32).t().contiguous().to(DEV)
+    ws = torch.full((1, 2, 2), 127, dtype=torch.uint8, device=DEV)
+    ws[0, 1, 0] = 255
+    y = epl.expert_product_fp8(one, scale, w, ws, i32([0]), i32([rows]),
+                               out_dtype=torch.float32).cpu()
+    want = torch.full((rows, 256), 256.0)
+    want[2] = 256 * 2.0 ** -127
+    want[1], want[:, 128:] = math.nan, math.nan
+    assert torch.equal(torch.isnan(y), torch.isnan(want))
+    # 2^-119 is a normal number, and every step to it is exact
+    assert torch.equal(torch.nan_to_num(y), torch.nan_to_num(want))
+
+
+def test_no_rows():
+    none = torch.zeros(0, 256, dtype=torch.bfloat16, device=DEV)
+    w1 = epl.quantize_weight(randn(2, 512, 256, seed=0).to(DEV))
+    w2 = epl.quantize_weight(randn(2, 256, 256, seed=1).to(DEV))
+    at = i32([0, 0])
+    for fmt in ("f32", "ue8m0"):
+        codes, scale = epl.quantize(none, scale_format=fmt)
+        assert epl.dequantize(codes, scale).shape == (0, 256)
+        assert epl.expert_product_fp8(codes, scale, *w1, at, at).shape == (0, 512)
+        assert epl.gated_block_fp8(codes, scale, *w1, *w2, at, at).shape == (0, 256)
+    dx, dz = epl.gated_block_fp8_backward(none, torch.zeros(0, 512, dtype=torch.bfloat16, device=DEV),
+                                          *w1, *w2, at, at)[:2]
+    assert dx.shape == (0, 256) and dz.shape == (0, 512)
+
+
+def test_two_captured_graphs_share_a_workspace():
+    """Replayed in turn, in one stream's order: neither finds what the other left."""
+    made = []
+    for counts, K, N, act, seed in [([1, 20, 9], 4096, 256, "swiglu", 0), ([130, 0, 260], 1040, 144, "none", 3)]:
+        args = list(check_product(counts, K, N, act=act, seed=seed))
+        made.append((args, args[10].clone()))
+    size = max(a[13].numel() for a, _ in made)
+    shared = torch.full((size,), 0xA5, dtype=torch.uint8, device=DEV)
+    graphs = []
+    for args, _ in made:
+        args[13] = shared
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            epl.epl_expert_product_fp8(*args)
+        graphs.append(g)
+    for k in range(6):
+        for (args, want), g in zip(made, graphs):
+            args[10].zero_()
+            g.replay()
+            assert torch.equal(args[10], want)
+        shared.fill_(0x11 * k)                          # the program's own work between
+        torch.cuda.synchronize()
