@@ -1414,7 +1414,8 @@ def quantize(x, activation: str = "none", scale_format: str = "f32", expert_star
     scale for each 128 columns, as epl_quantize in include/epl.h: what
     epl_dispatch_fp8 and expert_product_fp8 take. activation="swiglu" casts
     silu(x[:, :C]) * x[:, C:] of x [rows, 2C]. scale_format "f32": fp32 [rows,
-    C / 128]; "ue8m0": powers of two, int32 [C / 512, rows]. With the experts'
+    C / 128]; "ue8m0": powers of two, int32 [C / 512, rows]; `out_scale` has its format
+    by itself (also the low-latency rectangle's fp32 [E, C / 128, cap]). With the experts'
     blocks only their rows are cast: pass `out` and `out_scale` to choose what
     the others hold."""
     torch = _torch()
@@ -1471,7 +1472,7 @@ def dequantize(codes, scale, expert_start_loc=None, num_tokens_per_expert=None, 
 def quantize_weight(weight, scale_format: str = "f32", out=None, out_scale=None, stream=None):
     """(codes uint8 [E, N, K], scales [E, N / 128, K / 128]) of weights [E, N,
     K] (bf16 or fp32), a scale for each 128 x 128 block: fp32, or with "ue8m0"
-    powers of two as uint8 exponents."""
+    (or a uint8 `out_scale`) powers of two as uint8 exponents."""
     torch = _torch()
     _matrix(weight, "weight", 3)
     if stream is not None and weight.is_cuda:

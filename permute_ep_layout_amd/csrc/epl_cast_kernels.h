@@ -5,7 +5,10 @@
 //     UE8M0         s = 2^k, the least with amax <= 448 s (k >= -126),
 //                   code = e4m3(x * 2^-k)
 // in binary32 steps, e4m3 to nearest even. Both directions are bound by the
-// bytes of the rows: nothing is read twice.
+// bytes of the rows: nothing is read twice. Measured: 32768 gated rows of 2 x 2048
+// to codes 74 us, 29765 rows of 7168 back 141 us (4.5 TB/s both, a copy of 2 GiB
+// 4.8-5.0), 8 weights of 4096 x 7168 135 us (5.2 TB/s). Few rows are a launch and
+// two dependent reads: one row of 7168 3.5 us.
 #pragma once
 
 #include <hip/hip_runtime.h>
