@@ -770,3 +770,55 @@ def test_two_captured_graphs_share_a_workspace():
             assert torch.equal(args[10], want)
         shared.fill_(0x11 * k)                          # the program's own work between
         torch.cuda.synchronize()
+
+
+def close_to_product(y, xc, xs, wc, ws):
+    """A bf16 result against the sums and their bound (fp8_reference.product)."""
+    z, tol = ref.product(xc, xs, wc, ref.weight_scales(ws[None], *wc.shape)[0][:, ::128])
+    assert ((y.cpu().double() - z).abs() <= tol + 2.0 ** -8 * (z.abs() + tol)).all()
+
+
+@pytest.mark.parametrize("fmt", ["f32", "ue8m0"])
+def test_rows_past_32_bits(fmt):
+    rows, K = 300_001, 7168                              # 2.15e9 codes
+    x = torch.zeros(rows, K, dtype=torch.bfloat16, device=DEV)
+    x[-200:] = randn(200, K, seed=0).to(DEV)
+    codes, scale = epl.quantize(x, scale_format=fmt)
+    last = x[-200:].cpu().float()
+    want, want_scale = ref.cast_rows(last, fmt)
+    same_codes(codes[-200:], want)
+    got_scale = by_row(scale[:, -200:] if fmt == "ue8m0" else scale[-200:], fmt, K)
+    assert torch.equal(raw(got_scale), raw(want_scale))
+    assert not codes[:-200].any()
+    x.fill_(1)
+    epl.dequantize(codes, scale, out=x)
+    wide = (ref.decode(want) * ref.numbers(want_scale).repeat_interleave(128, 1)).float().bfloat16()
+    assert torch.equal(raw(x[-200:]), raw(wide)) and not x[:-200].any()
+    del x
+    wc, ws = ref.cast_weight(randn(1, 48, K, seed=1, std=K ** -0.5), "f32")
+    for count in (3, 200):
+        y = epl.expert_product_fp8(codes, scale, wc.to(DEV), ws.to(DEV), i32([rows - count]),
+                                   i32([count]), expected_rows=count)
+        close_to_product(y[-count:], want[-count:], ref.numbers(want_scale)[-count:], wc[0], ws[0])
+
+
+def test_weights_past_32_bits():
+    E, N, K = 2048, 1024, 1040                           # 2.18e9 codes
+    w = torch.zeros(E, N, K, dtype=torch.bfloat16, device=DEV)
+    w[-1] = randn(N, K, seed=0, std=K ** -0.5).to(DEV)
+    codes, scale = epl.quantize_weight(w)
+    want, want_scale = ref.cast_weight(w[-1:].cpu().float(), "f32")
+    del w
+    same_codes(codes[-1:], want)
+    assert torch.equal(raw(scale[-1:]), raw(want_scale)) and not codes[:-1].any()
+    counts = [0] * (E - 1) + [150]
+    for transposed in (False, True):
+        xc, xs = ref.cast_rows(randn(150, N if transposed else K, seed=1), "f32")
+        y = epl.expert_product_fp8(xc.to(DEV), xs.to(DEV), codes, scale, i32([0] * E), i32(counts),
+                                   transposed=transposed)
+        if transposed:
+            full = ref.weight_scales(want_scale, N, K)[0].t()
+            z, tol = ref.product(xc, ref.numbers(xs), want[0].t().contiguous(), full[:, ::128])
+            assert ((y.cpu().double() - z).abs() <= tol + 2.0 ** -8 * (z.abs() + tol)).all()
+        else:
+            close_to_product(y, xc, ref.numbers(xs), want[0], want_scale[0])
