@@ -188,8 +188,8 @@ __device__ __forceinline__ void store_codes(const Args &a, int64_t at, const flo
 //
 // Columns of the gated activation alternate by 16, gate and up.
 //
-// Measured: 8 x 4096 rows, 7168 -> 4096, 1060-1090 us, 1.8 PFLOP/s (gated and cast
-// 1000, powers of two as scales 945-990), where a library's product with one scale
+// Measured: 8 x 4096 rows, 7168 -> 4096, 1045-1070 us, 1.8 PFLOP/s (gated and cast
+// 930, powers of two as scales 915-925), where a library's product with one scale
 // reaches 2.5-2.7: a tile of 56 blocks 135 us, of 16 44. The matrix units are busy for
 // 45% of the cycles at 2.1 GHz. Without its loads it takes 800, with all of them in L2
 // 950, without its epilogue 1000 (8 to 10 us a tile). What bounds it is a stage's loads,
@@ -341,6 +341,28 @@ __device__ __forceinline__ void emit_any(const Args &a, const Tile &x, const flo
     }
 }
 
+// All loads are done but the last N that this wave began.
+template <int N>
+__device__ __forceinline__ void all_but()
+{
+    static_assert(N < 64, "the counter's width");
+    __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4) << 14 | 0x0070);       // (and lgkmcnt(0))
+}
+
+// All waves of the workgroup have come here, and (N >= 0) what each loaded into LDS
+// but its last N loads has landed, and what it wrote. (A fence would wait for
+// all loads.)
+template <int N = -1>
+__device__ __forceinline__ void met()
+{
+    asm volatile("" ::: "memory");
+    if constexpr (N >= 0)
+        all_but<N>();
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
 // acc + by * sum, each rounded once.
 __device__ __forceinline__ f32x4 scaled(f32x4 sum, float by, f32x4 acc)
 {
@@ -468,29 +490,25 @@ __global__ __launch_bounds__(tile_threads(BN), 2) void tile_kernel(Args a)
         each<IP * 4>([&](auto i) { acc[i] = f32x4{0, 0, 0, 0}; });
 
         struct Stage {
-            __amdgpu_buffer_rsrc_t rp, rq;
-            uint32_t op, oq;
+            __amdgpu_buffer_rsrc_t r;
+            uint32_t o;
         };
         auto block_at = [&](int s) { const int v = s + rot; return v < s1 ? v : v - turns; };
-        auto stage = [&](int s) {
-            const int k0 = block_at(s) * kGroup;
-            const int left = s < s1 ? min(a.K - k0, kGroup) : 0;
-            Stage f;
-            f.rp = rsrc(bp + k0, np - k0);
-            f.rq = QT ? rsrc(bq + (int64_t)k0 * a.N, left * a.N) : rsrc(bq + k0, nq - k0);
-            f.op = kp >= left ? op | 0x80000000u : op;
-            f.oq = !QT && kq >= left ? oq | 0x80000000u : oq;
-            return f;
+        auto stage_p = [&](int s) {
+            const int k0 = block_at(s) * kGroup, left = s < s1 ? min(a.K - k0, kGroup) : 0;
+            return Stage{rsrc(bp + k0, np - k0), kp >= left ? op | 0x80000000u : op};
         };
-        auto fetch_one = [&](const Stage &f, uint16_t *lp, uint16_t *lq, auto i) {
-            if constexpr (i < ISP)
-                dma(f.rp, f.op + i * ip, lp + i * WAVES * 512 + wave * 512);
-            else
-                dma(f.rq, f.oq + (i - ISP) * iq, lq + (i - ISP) * WAVES * 512 + wave * 512);
+        auto stage_q = [&](int s) {
+            const int k0 = block_at(s) * kGroup, left = s < s1 ? min(a.K - k0, kGroup) : 0;
+            if (QT)
+                return Stage{rsrc(bq + (int64_t)k0 * a.N, left * a.N), oq};
+            return Stage{rsrc(bq + k0, nq - k0), kq >= left ? oq | 0x80000000u : oq};
         };
-        auto fetch = [&](int s, uint16_t *lp, uint16_t *lq) {
-            const Stage f = stage(s);
-            each<ISP + ISQ>([&](auto i) { fetch_one(f, lp, lq, i); });
+        auto fetch_p = [&](const Stage &f, uint16_t *l, auto i) {
+            dma(f.r, f.o + i * ip, l + i * WAVES * 512 + wave * 512);
+        };
+        auto fetch_q = [&](const Stage &f, uint16_t *l, auto i) {
+            dma(f.r, f.o + i * iq, l + i * WAVES * 512 + wave * 512);
         };
         auto load_scale = [&](int s) {
             uint32_t v = 0;
@@ -542,34 +560,45 @@ __global__ __launch_bounds__(tile_threads(BN), 2) void tile_kernel(Args a)
             asm volatile("" : "+v"(acc[old]));
         };
         // One block: IP groups of 4 products, one piece of x each. A group's
-        // reads of the next piece run under its products; one barrier a stage,
-        // before the last group: all of this stage has been read by then, and
-        // may be overwritten, and the next has landed. The last group's
-        // products free the weight's registers one by one for the next stage's.
-        // The loads of the stage after the next start there too, kNow of them, and
-        // the rest over the next block's first groups: all of them at once wait for
-        // each other before the products go on (8 x 4096 rows, 7168 -> 4096: 1080 us,
-        // all at once 1120; 2048 -> 7168: 600, 640).
-        constexpr int dmas = ISP + ISQ, kNow = 2, kLater = IP - 1 < 3 ? IP - 1 : 3;
-        constexpr int per = (dmas - kNow + kLater - 1) / kLater;
-        Stage after;                         // the next stage but one, and the
-        uint32_t coming = 0;                 // thread's scale of it
+        // reads of the next piece run under its products. The weight's part of a
+        // stage has been read by all waves when they meet in the second group
+        // (its codes wait in registers), and loads of the next stage but one
+        // begin to overwrite it there; x's has when they meet before the last
+        // group, where the next stage has landed too. The last group's products
+        // free the weight's registers one by one for the next stage's. So weights
+        // have nearly two blocks' products to arrive under, and x one (8 x 4096
+        // rows, 7168 -> 4096, gated and cast: 930 us; both begun before and after the
+        // last group, with one meeting, 970; all of them there 1000).
+        constexpr int kNow = ISP / 2, per = (ISQ + IP - 4) / (IP - 3);
+        static_assert((IP - 2) * per >= ISQ, "all of the weight's loads begin before the last group");
+        Stage afterp;                        // the next stage's x
+        uint32_t coming = 0;                 // the thread's scale of the next stage
         auto turn = [&](int s, uint16_t *cp, uint16_t *cq, float *cs, uint16_t *xp, uint16_t *xq,
                         float *xs) {
+            Stage afterq;
             each<IP>([&](auto g) {
                 if constexpr (g + 1 < IP)
                     read_p(cp, cs, std::integral_constant<int, g + 1>{});
                 if constexpr (g == IP - 1) {
                     write_scale(xs, coming);
-                    landed();
-                    after = stage(s + 2);
+                    met<ISQ>();
+                    afterp = stage_p(s + 2);
                     coming = load_scale(s + 2);
-                } else if constexpr (g < kLater) {
+                }
+                if constexpr (g == 0)
+                    each<ISP - kNow>([&](auto i) {
+                        fetch_p(afterp, xp, std::integral_constant<int, kNow + decltype(i)::value>{});
+                    });
+                if constexpr (g == 1) {
+                    met();
+                    afterq = stage_q(s + 2);
+                }
+                if constexpr (g >= 1 && g < IP - 1) {
                     each<per>([&](auto i) {
                         constexpr std::integral_constant<
-                            int, kNow + decltype(g)::value * per + decltype(i)::value> d{};
-                        if constexpr (d < dmas)
-                            fetch_one(after, xp, xq, d);
+                            int, (decltype(g)::value - 1) * per + decltype(i)::value> d{};
+                        if constexpr (d < ISQ)
+                            fetch_q(afterq, cq, d);
                     });
                 }
                 each<4>([&](auto j) {
@@ -577,7 +606,7 @@ __global__ __launch_bounds__(tile_threads(BN), 2) void tile_kernel(Args a)
                     if constexpr (g == IP - 1) {
                         read_q(xq, j);
                         if constexpr (j < kNow)
-                            fetch_one(after, cp, cq, j);
+                            fetch_p(afterp, cp, j);
                     }
                     __builtin_amdgcn_sched_barrier(0);
                 });
@@ -588,11 +617,19 @@ __global__ __launch_bounds__(tile_threads(BN), 2) void tile_kernel(Args a)
             });
         };
         coming = load_scale(s0);
-        fetch(s0, sp0, sq0);
+        {
+            const Stage p0 = stage_p(s0), q0 = stage_q(s0);
+            each<ISP>([&](auto i) { fetch_p(p0, sp0, i); });
+            each<ISQ>([&](auto i) { fetch_q(q0, sq0, i); });
+        }
         write_scale(sc0, coming);
         landed();
-        after = stage(s0 + 1);
-        each<kNow>([&](auto i) { fetch_one(after, sp1, sq1, i); });
+        {
+            const Stage q1 = stage_q(s0 + 1);
+            each<ISQ>([&](auto i) { fetch_q(q1, sq1, i); });
+        }
+        afterp = stage_p(s0 + 1);
+        each<kNow>([&](auto i) { fetch_p(afterp, sp1, i); });
         coming = load_scale(s0 + 1);
         each<4>([&](auto j) {
             read_q(sq0, j);
@@ -718,14 +755,6 @@ struct FewShared {
     f32x4 *red;               // in x, when that has been read
     float *most;
 };
-
-// All loads are done but the last N that this wave began.
-template <int N>
-__device__ __forceinline__ void all_but()
-{
-    static_assert(N < 64, "the counter's width");
-    __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4) << 14 | 0x0070);       // (and lgkmcnt(0))
-}
 
 // The epilogue of row tile i (16 rows from row0 + 16 i on) by the G waves of a
 // workgroup that hold its sums. All waves of the workgroup come here; `mine`:
