@@ -60,16 +60,16 @@ bool desc_ok(const epl_product_fp8_desc *p)
 
 // Rows an expert, on average, up to which the weights are read straight from
 // memory, once for every 32 rows of an expert. Measured (this way, tiles), us: 8
-// experts of 24 rows, 7168 -> 4096: 52, 64, gated with its cast 54, 82; of 32, none
-// of them more: 53, 63; but where counts scatter about 32 half of the experts'
-// weights are read twice.
+// experts of 24 rows, 7168 -> 4096: 52, 63, gated with its cast 55, 76; 64 of 24,
+// 4096 -> 2048: 108, 106; 8 of 32, none of them more, 7168 -> 4096: 53, 63; but where
+// counts scatter about 32 half of the experts' weights are read twice.
 constexpr int64_t kFewRows = 24;
 
-// Large tiles take 2.3 us a stage for four times what a small one, two of them on
-// a CU, takes 1.45 for. Measured (large, small), us: 8 experts of 4096 rows, 7168 ->
-// 4096: 1083, 1356; of 512: 133, 178; of 256: 97, 89; 64 of 192, 4096 -> 2048: 166,
-// 222; of 128: 155, 144; 1 of 4096, 2048 -> 2048: 50, 35.
-constexpr Cost cost_of(Kind k) { return k == kLarge ? Cost{7.0, 2.3} : Cost{4.0, 1.45}; }
+// Large tiles take 2.2 us a stage for four times what a small one, two of them on
+// a CU, takes 1.4 for. Measured (large, small), us: 8 experts of 4096 rows, 7168 ->
+// 4096: 1056, 1330; of 512: 124, 161; of 256: 93, 83; 64 of 192, 4096 -> 2048: 159,
+// 204; of 128: 149, 135; 1 of 4096, 2048 -> 2048: 51, 36.
+constexpr Cost cost_of(Kind k) { return k == kLarge ? Cost{7.0, 2.2} : Cost{4.0, 1.4}; }
 
 int max_parts(int64_t depth) { return H::max_parts(depth, P::kGroup); }
 

@@ -190,12 +190,13 @@ __device__ __forceinline__ void store_codes(const Args &a, int64_t at, const flo
 //
 // Measured: 8 x 4096 rows, 7168 -> 4096, 1045-1070 us, 1.8 PFLOP/s (gated and cast
 // 930, powers of two as scales 915-925), where a library's product with one scale
-// reaches 2.5-2.7: a tile of 56 blocks 135 us, of 16 44. The matrix units are busy for
-// 45% of the cycles at 2.1 GHz. Without its loads it takes 800, with all of them in L2
-// 950, without its epilogue 1000 (8 to 10 us a tile). What bounds it is a stage's loads,
-// which have about one block's products to arrive under; LDS holds no third stage of
-// 64 KB, and smaller tiles load more. Loads of a further block into L2 alone gained 2%;
-// the epilogue's passes as one loop (less code, but spilled sums) lost 5 to 9%.
+// reaches 2.5-2.7: a tile of 56 blocks 131 us, of 16 43. The matrix units are busy for
+// 45% of the cycles at 2.1 GHz. What bounds it is x's loads, with one block's products
+// to arrive under, and the epilogue, 8 to 10 us a tile: before weights were loaded early
+// it took 1080 us, then without its loads 800, with all of them in L2 950, without its
+// epilogue 1000. LDS holds no third stage of 64 KB, and smaller tiles load more. Loads
+// of a further block into L2 alone gained 2% then, starts of the XCDs 10 to 20 us apart
+// nothing; the epilogue's passes as one loop (less code, but spilled sums) lost 5 to 9%.
 
 using epl_product::at;
 using epl_product::dma;
