@@ -39,6 +39,11 @@ bool cast_ok(const epl_cast_desc *p)
            (p->scale_format == EPL_SCALE_F32 || p->scale_format == EPL_SCALE_UE8M0);
 }
 
+int64_t weight_blocks(const epl_weight_cast_desc &p)
+{
+    return (int64_t)p.num_experts * ((p.in_cols + 127) / 128) * ((p.out_cols + 127) / 128);
+}
+
 bool weight_ok(const epl_weight_cast_desc *p)
 {
     if (!p || p->reserved != 0 || p->num_experts < 1 || p->num_experts > epl_product::kMaxExperts)
@@ -46,8 +51,7 @@ bool weight_ok(const epl_weight_cast_desc *p)
     if (p->in_cols < 16 || p->in_cols % 16 != 0 || p->in_cols > kMaxCols || p->out_cols < 1 ||
         p->out_cols > kMaxCols || !type_ok(p->value_type))
         return false;
-    const int64_t blocks = (int64_t)p->num_experts * ((p->in_cols + 127) / 128) * ((p->out_cols + 127) / 128);
-    return blocks <= INT32_MAX &&
+    return weight_blocks(*p) <= INT32_MAX &&
            (p->scale_format == EPL_SCALE_F32 || p->scale_format == EPL_SCALE_UE8M0);
 }
 
@@ -148,13 +152,13 @@ int epl_quantize_weight(const epl_weight_cast_desc *p, const void *weight, uint8
     if (!weight || !aligned(weight, 16) || !codes || !aligned(codes, 16) || !scale ||
         !aligned(scale, power ? 1 : 4))
         return EPL_EINVAL;
-    const C::WeightArgs a{weight, codes, scale, p->out_cols, p->in_cols, power};
-    const unsigned blocks = (unsigned)p->num_experts * ((p->in_cols + 127) / 128) * ((p->out_cols + 127) / 128);
+    const C::WeightArgs a{weight, codes, scale, p->out_cols, p->in_cols, power, weight_blocks(*p)};
+    const dim3 grid((unsigned)std::min<int64_t>(a.blocks, C::kWeightGrid)), threads(C::kThreads);
     hipStream_t s = static_cast<hipStream_t>(stream);
     if (p->value_type == EPL_OUT_F32)
-        hipLaunchKernelGGL((C::quantize_weight_kernel<float>), dim3(blocks), dim3(C::kThreads), 0, s, a);
+        hipLaunchKernelGGL((C::quantize_weight_kernel<float>), grid, threads, 0, s, a);
     else
-        hipLaunchKernelGGL((C::quantize_weight_kernel<__bf16>), dim3(blocks), dim3(C::kThreads), 0, s, a);
+        hipLaunchKernelGGL((C::quantize_weight_kernel<__bf16>), grid, threads, 0, s, a);
     return launch_status();
 }
 

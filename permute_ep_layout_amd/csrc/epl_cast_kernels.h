@@ -284,22 +284,24 @@ __global__ __launch_bounds__(kThreads) void dequantize_kernel(Args a)
 
 // -------------------------------------------------------------- weights --
 //
-// A workgroup takes a block of 128 x 128, which its registers hold between
-// the maximum and the rounding.
+// A workgroup takes blocks of 128 x 128, which its registers hold between the
+// maximum and the rounding: one block, but where there are more of them than a
+// launch may have workgroups (2^32 threads), as of 2048 weights of 2^20 columns.
 
 struct WeightArgs {
     const void *w;            // [E, N, K]
     uint8_t *codes;
     void *scale;              // [E, N / 128, K / 128] fp32 or uint8
     int N, K, power;
+    int64_t blocks;
 };
 
+constexpr int kWeightGrid = 1 << 23;   // workgroups at most
+
 template <typename T>
-__global__ __launch_bounds__(kThreads) void quantize_weight_kernel(WeightArgs a)
+__device__ __forceinline__ void quantize_block(const WeightArgs &a, int b, float *most)
 {
-    __shared__ float most[4];
     const int kb = (a.K + kGroup - 1) / kGroup, nb = (a.N + kGroup - 1) / kGroup;
-    const int b = blockIdx.x;
     const int64_t e = b / (nb * kb);
     const int n0 = b / kb % nb * kGroup, k0 = b % kb * kGroup;
     const int tid = threadIdx.x, k = k0 + (tid & 7) * 16, n = n0 + (tid >> 3);
@@ -340,6 +342,17 @@ __global__ __launch_bounds__(kThreads) void quantize_weight_kernel(WeightArgs a)
             static_cast<uint8_t *>(a.scale)[b] = (uint8_t)f.byte;
         else
             static_cast<float *>(a.scale)[b] = f.scale;
+    }
+}
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void quantize_weight_kernel(WeightArgs a)
+{
+    __shared__ float most[4];
+    for (int64_t b = blockIdx.x; b < a.blocks; b += gridDim.x) {
+        if (b != blockIdx.x)
+            __syncthreads();           // the block before has been rounded
+        quantize_block<T>(a, (int)b, most);
     }
 }
 
