@@ -580,7 +580,11 @@ size_t epl_product_fp8_workspace_bytes(const epl_product_fp8_desc *p);
  * than itself; one whose exponents sum to E - 7 or more loses nothing. Besides the
  * fp32 sums, z is so within 7 * 2^-13 of the sum of the products' magnitudes where
  * no code is subnormal, and within 7 * 2^-10 of it where some are (2^-16 of z for
- * normal data). */
+ * normal data).
+ * A block's two scales are multiplied before its sum is, in binary32. Where their
+ * product is below 2^-126 it is rounded to a multiple of 2^-149, which the bounds
+ * above do not count; where it is beyond binary32 it is an infinity, also for sums
+ * that would bring it back, and a sum of zero becomes NaN. */
 int epl_expert_product_fp8(const epl_product_fp8_desc *p, const uint8_t *x, const void *x_scale,
                            const uint8_t *weight, const void *weight_scale, const float *bias,
                            const uint16_t *residual, const int32_t *expert_start_loc,

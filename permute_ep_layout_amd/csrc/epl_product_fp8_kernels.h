@@ -368,7 +368,9 @@ __device__ __forceinline__ void met()
     __builtin_amdgcn_sched_barrier(0);
 }
 
-// acc + by * sum, each rounded once.
+// acc + by * sum, each rounded once. (by, a row's scale times a weight's, comes
+// first: by * sum with the scales in turn would be three more instructions a quad,
+// and where one order leaves binary32 the other may too.)
 __device__ __forceinline__ f32x4 scaled(f32x4 sum, float by, f32x4 acc)
 {
     return __builtin_elementwise_fma(sum, f32x4{by, by, by, by}, acc);

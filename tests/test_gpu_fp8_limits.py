@@ -96,3 +96,28 @@ def test_product_bits_lost_next_to_subnormal_codes(rows):
     lost = 0.5 + seven - unit_product(x, w)
     assert (lost == seven).all()
     assert 7 * 2.0 ** -13 * (0.5 + seven) < seven <= 7 * 2.0 ** -10 * (0.5 + seven)
+
+
+@pytest.mark.parametrize("rows", [2, 90])                # few rows, tiles
+@pytest.mark.parametrize("transposed", [False, True])
+def test_product_of_scales_at_the_ends_of_binary32(rows, transposed):
+    """The product of a block's scales is rounded to binary32 before the block's sum is
+    multiplied by it: subnormal ones are kept to multiples of 2^-149, not flushed, and
+    beyond the largest number they are infinite, NaN where the sum is zero."""
+    x = torch.full((rows, 128), 0x78, dtype=torch.uint8, device=DEV)     # 256
+    w = torch.full((1, 128, 128), 0x78, dtype=torch.uint8, device=DEV)
+    x[1] = 0                                             # sums: 2^23, and 0 in row 1
+
+    def made(sx, sw):
+        return epl.expert_product_fp8(
+            x, torch.full((rows, 1), sx, device=DEV), w, torch.full((1, 1, 1), sw, device=DEV),
+            i32([0]), i32([rows]), out_dtype=torch.float32, transposed=transposed).cpu().double()
+
+    for sx, sw, by in ((2.0 ** -70, 2.0 ** -70, 2.0 ** -140),
+                       (1.5 * 2.0 ** -75, 1.25 * 2.0 ** -74, 2.0 ** -148),   # 1.875 2^-149
+                       (2.0 ** -100, 2.0 ** -60, 0.0), (2.0 ** 50, 2.0 ** 54, 2.0 ** 104)):
+        y = made(sx, sw)
+        assert (y[0] == by * 2.0 ** 23).all() and (y[2:] == by * 2.0 ** 23).all()
+        assert (y[1] == 0).all()
+    y = made(2.0 ** 80, 2.0 ** 48)
+    assert (y[0] == float("inf")).all() and torch.isnan(y[1]).all()
