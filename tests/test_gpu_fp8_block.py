@@ -172,3 +172,79 @@ def test_layer_hands_every_row_on():
     dx = epl.dispatch_backward(drows, oi)
     each = drows.double()[slots]
     assert ((dx.double() - each.sum(1)).abs() <= 4 * U * each.abs().sum(1)).all()
+
+
+def silu(z):
+    return z * torch.sigmoid(z)
+
+
+def silu_slope(z):
+    p = torch.sigmoid(z)
+    return p + z * p * torch.sigmoid(-z)
+
+
+def in_64_bits(w):
+    return ref.decode(w[0]) * ref.weight_scales(w[1], *w[0].shape[1:])
+
+
+@pytest.mark.parametrize("fmt", ["f32", "ue8m0"])
+@pytest.mark.parametrize("counts", [[3, 0, 2], [90, 50]])       # few rows, tiles
+def test_block_gradient_against_differences_of_the_block(counts, fmt):
+    """gated_block_fp8_backward against central differences of the block in 64 bits. Rows, weights
+    and dy are positive, so that nothing cancels and relative errors pass through sums as they
+    are; dy is its own cast."""
+    H = F = 128
+    E, total = len(counts), sum(counts)
+    starts = [sum(counts[:e]) for e in range(E)]
+    owner = torch.repeat_interleave(torch.arange(E), torch.tensor(counts))
+    w_fmt = "ue8m0" if fmt == "ue8m0" else "f32"
+    xc, xs = ref.cast_rows(randn(total, H, seed=0, std=0.25).abs(), fmt)
+    w1 = ref.cast_weight(randn(E, 2 * F, H, seed=1, std=0.1).abs(), w_fmt)
+    w2 = ref.cast_weight(randn(E, H, F, seed=2, std=0.1).abs(), w_fmt)
+    dyc = torch.randint(0x30, 0x7F, (total, H), generator=torch.Generator().manual_seed(3),
+                        dtype=torch.uint8)
+    dyc[:, 7] = 0x7E                                           # 448: the scale is 1
+    dy = ref.decode(dyc)
+    w = [t.to(DEV) for t in (*w1, *w2)]
+    at, n = i32(starts), i32(counts)
+    pre = torch.empty(total, 2 * F, dtype=torch.bfloat16, device=DEV)
+    epl.gated_block_fp8(xc.to(DEV), ref.lay(xs, fmt).to(DEV), *w, at, n, pre=pre, scale_format=fmt)
+    gx, gz = epl.gated_block_fp8_backward(dy.bfloat16().to(DEV), pre, *w, at, n, scale_format=fmt)
+
+    v1, v2 = in_64_bits(w1)[owner], in_64_bits(w2)[owner]      # a row's own weights
+    x = ref.decode(xc) * ref.numbers(xs)
+
+    def value(z):
+        g, u = z.chunk(2, 1)
+        return ((v2 * (silu(g) * u)[:, None]).sum(2) * dy).sum(1)          # of each row
+
+    def project(rows):
+        return (v1 * rows[:, None]).sum(2)
+
+    step = 1e-5
+    v = randn(total, H, seed=4).abs().double() + 0.1
+    slope = (value(project(x + step * v)) - value(project(x - step * v))) / (2 * step)
+    z = project(x)
+    vz = randn(total, 2 * F, seed=5).abs().double() + 0.1
+    slope_z = (value(z + step * vz) - value(z - step * vz)) / (2 * step)
+
+    # dz = [dh u silu'(g), dh silu(g)]: dh and z within 7 2^-10 each (bits inside a block; all
+    # terms are positive), z rounded to bf16 (2^-8); silu(g) passes a relative error of g on at most
+    # 2 times and silu'(g) at most half (g > 0); binary32 below 2^-16; dz in bf16 2^-8.
+    # The differences: 1e-6.
+    assert (z > 0).all()
+    bits, half = 7 * 2.0 ** -10, 2.0 ** -8
+    of_z = (1 + bits) * (1 + half) - 1
+    of_dz = (1 + bits) * (1 + 2 * of_z) * (1 + 2.0 ** -16) - 1
+    slope_of = lambda g, d: (g.cpu().double() * d).sum(1)  # noqa: E731
+    err_z = (slope_of(gz, vz) - slope_z).abs()
+    assert (err_z <= ((1 + of_dz) * (1 + half) - 1 + 1e-6) * slope_z).all()
+    # dx: dz cast (2^-4, and 2^-10 of its scale near zero), its product and bf16 again
+    g, u = z.chunk(2, 1)
+    dh = (v2 * dy[:, :, None]).sum(1)
+    dz = torch.cat([dh * u * silu_slope(g), dh * silu(g)], 1)
+    scale = dz.view(total, 2, 128).amax(2) * (1 + of_dz) / 448 * (2 if fmt == "ue8m0" else 1)
+    low = (v1 * (2.0 ** -10 * scale).repeat_interleave(128, 1)[:, :, None]).sum(1)
+    rel = (1 + of_dz) * (1 + 2.0 ** -4) * (1 + bits) * (1 + half) - 1
+    err = (slope_of(gx, v) - slope).abs()
+    assert (err <= (rel + 1e-6) * slope + 1.02 * (low * v).sum(1)).all()
