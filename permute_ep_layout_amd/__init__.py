@@ -1580,8 +1580,11 @@ def gated_block_fp8_backward(grad_y, pre, w1, w1_scale, w2, w2_scale, expert_sta
     [rows, 2F]) from grad_y (bf16 or fp32 [rows, H], e.g. of combine_backward) and the
     `pre` it kept. grad_y is cast to 8 bits for the product with W2, and
     grad_pre, whose cast leaves that product's epilogue too, for the one with
-    W1; expert_weight_grad takes grad_y and grad_pre as they are. Casts pass
-    gradients through. Rows outside the experts' blocks are not written."""
+    W1. Casts pass gradients through. Rows outside the experts' blocks are not
+    written. The weights' gradients are expert_weight_grad(grad_pre, x) and
+    expert_weight_grad(grad_y, h) on bf16 rows: grad_pre and (bf16) grad_y as
+    they are, x by `dequantize`, and h, which the block does not keep, from
+    `pre`: dequantize(*quantize(pre, activation="swiglu", ..), ..)."""
     torch = _torch()
     _matrix(grad_y, "grad_y", 2)
     _matrix(w2, "w2", 3)

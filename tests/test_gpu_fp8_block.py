@@ -248,3 +248,56 @@ def test_block_gradient_against_differences_of_the_block(counts, fmt):
     rel = (1 + of_dz) * (1 + 2.0 ** -4) * (1 + bits) * (1 + half) - 1
     err = (slope_of(gx, v) - slope).abs()
     assert (err <= (rel + 1e-6) * slope + 1.02 * (low * v).sum(1)).all()
+
+
+def test_both_weight_gradients():
+    """dw2 and dw1 of the block, by expert_weight_grad: of w2 with the block's h cast and made
+    bf16 again from the kept z, of w1 with dz and x made bf16 again. Each element within the sum
+    of its terms' errors."""
+    counts, H, F, total = [40, 0, 7, 90], 400, 256, 150
+    starts = [2, 43, 43, 55]
+    E = len(counts)
+    owned = torch.zeros(total, dtype=torch.bool)
+    for s, m in zip(starts, counts):
+        owned[s:s + m] = True
+    xc, xs = ref.cast_rows(randn(total, H, seed=0), "f32")
+    xc[~owned] = 0x7F
+    w1 = ref.cast_weight(randn(E, 2 * F, H, seed=1, std=H ** -0.5), "f32")
+    w2 = ref.cast_weight(randn(E, H, F, seed=2, std=F ** -0.5), "f32")
+    dy = randn(total, H, seed=3).bfloat16()
+    dy[~owned] = float("nan")
+    rows = dict(expert_start_loc=i32(starts), num_tokens_per_expert=i32(counts))
+    w = [t.to(DEV) for t in (*w1, *w2)]
+    x = [xc.to(DEV), xs.to(DEV)]
+    pre = filled((total, 2 * F), torch.bfloat16)
+    epl.gated_block_fp8(*x, *w, **rows, pre=pre)
+    _, dz = epl.gated_block_fp8_backward(dy.to(DEV), pre, *w, **rows)
+    h = epl.dequantize(*epl.quantize(pre, activation="swiglu", **rows), **rows)
+    dw2 = epl.expert_weight_grad(dy.to(DEV), h, **rows, out_dtype=torch.float32)
+    dw1 = epl.expert_weight_grad(dz, epl.dequantize(*x, **rows), **rows, out_dtype=torch.float32)
+    assert dw2.shape == (E, H, F) and dw1.shape == (E, 2 * F, H)
+    dw2, dw1, dz = dw2.cpu().double(), dw1.cpu().double(), dz.cpu().double()
+    wide = ref.numbers(xs).repeat_interleave(128, 1)[:, :H]
+    for e, (s, m) in enumerate(zip(starts, counts)):
+        at = slice(s, s + m)
+        if m == 0:
+            assert not dw2[e].any() and not dw1[e].any()
+            continue
+        s1 = ref.weight_scales(w1[1], 2 * F, H)[e][:, ::128]
+        z, tol = ref.product(xc[at], ref.numbers(xs)[at], w1[0][e], s1)
+        tol = tol + 2.0 ** -8 * (z.abs() + tol)                # kept in bf16
+        g, u = z.chunk(2, 1)
+        tg, tu = tol.chunk(2, 1)
+        v = silu(g) * u
+        tv = 1.13 * tg * (u.abs() + tu) + silu(g).abs() * tu + 32 * U * (1 + v.abs())
+        # its cast: half a step, 2^-4 of the value, or 2^-10 of its scale; then bf16
+        most = ((v.abs() + tv).view(m, -1, 128).amax(2) / 448).repeat_interleave(128, 1)
+        cast = tv + 2.0 ** -4 * (v.abs() + tv) + 2.0 ** -10 * most
+        cast = cast + 2.0 ** -8 * (v.abs() + cast)
+        d = dy[at].double()
+        sums = (m + 1) * 2.0 ** -23
+        lim = d.abs().t() @ cast + sums * (d.abs().t() @ (v.abs() + cast))
+        assert ((dw2[e] - d.t() @ v).abs() <= lim).all()
+        xv = ref.decode(xc[at]) * wide[at]
+        mag = dz[at].abs().t() @ xv.abs()
+        assert ((dw1[e] - dz[at].t() @ xv).abs() <= (2.0 ** -8 + sums) * 1.01 * mag).all()
