@@ -301,3 +301,49 @@ def test_both_weight_gradients():
         xv = ref.decode(xc[at]) * wide[at]
         mag = dz[at].abs().t() @ xv.abs()
         assert ((dw1[e] - dz[at].t() @ xv).abs() <= (2.0 ** -8 + sums) * 1.01 * mag).all()
+
+
+@pytest.mark.parametrize("cap", [16, 48])
+def test_layer_in_a_rectangle(cap):
+    """The low-latency dispatch's rectangle through the block and back, as it lies: rows, results
+    and weight gradients are those of the same rows packed, kernels chosen by the routed rows."""
+    T, H, F, E, K = 40, 256, 128, 8, 2
+    idx = torch.stack([(torch.arange(T) * 3) % E, (torch.arange(T) * 3 + 1) % E], 1).to(DEV)
+    x = randn(T, H, seed=0).bfloat16().to(DEV)
+    p = epl.Problem.make(T, K, E, 1, H, H // 128)
+    e32 = lambda *s: torch.empty(*s, dtype=torch.int32, device=DEV)  # noqa: E731
+    out, scale, oi, cnt = filled((E, cap, H), torch.uint8), filled((E, H // 128, cap), torch.float32), \
+        e32(T, K), e32(E)
+    epl.epl_ll_dispatch(p, T, cap, idx, x, out, scale, cnt, e32(E, cap), e32(E, 1, 2), oi,
+                        torch.empty(epl.epl_ll_workspace_bytes(p, T), dtype=torch.uint8, device=DEV))
+    codes, routed = out.view(-1, H), idx.numel()
+    rows = dict(expert_start_loc=cap * torch.arange(E, dtype=torch.int32, device=DEV),
+                num_tokens_per_expert=cnt)
+    w = [t.to(DEV) for t in (*ref.cast_weight(randn(E, 2 * F, H, seed=1, std=H ** -0.5), "f32"),
+                             *ref.cast_weight(randn(E, H, F, seed=2, std=F ** -0.5), "f32"))]
+    wt = torch.rand(T, K, generator=torch.Generator().manual_seed(3)).to(DEV)
+    dy = randn(T, H, seed=4).to(DEV)
+
+    def layer(codes, scale, rows, oi):
+        """Forwards and back, as the documentation writes it."""
+        pre = torch.empty(codes.shape[0], 2 * F, dtype=torch.bfloat16, device=DEV)
+        o = epl.gated_block_fp8(codes, scale, *w, **rows, pre=pre, expected_rows=routed)
+        do, dweights = epl.combine_backward(dy, o, oi, wt)
+        dx, dz = epl.gated_block_fp8_backward(do, pre, *w, **rows, expected_rows=routed)
+        dw1 = epl.expert_weight_grad(dz, epl.dequantize(codes, scale, **rows), **rows,
+                                     out_dtype=torch.float32, expected_rows=routed)
+        h = epl.dequantize(*epl.quantize(pre, activation="swiglu", **rows), **rows)
+        dw2 = epl.expert_weight_grad(do, h, **rows, out_dtype=torch.float32, expected_rows=routed)
+        return epl.combine(o, oi, wt), dweights, epl.dispatch_backward(dx, oi), dw1, dw2
+
+    got = layer(codes, scale, rows, oi)
+    n = cnt.cpu()
+    starts = (torch.cumsum(n, 0) - n).to(DEV)
+    e = (oi // cap).long()
+    packed_oi = (starts[e] + oi % cap).int()
+    packed, packed_scale = (torch.cat([v[i, :m] for i, m in enumerate(n.tolist())])
+                            for v in (out, scale.transpose(1, 2)))
+    want = layer(packed.contiguous(), packed_scale.contiguous(),
+                 dict(expert_start_loc=starts.int(), num_tokens_per_expert=cnt), packed_oi)
+    for a, b in zip(got, want):
+        assert torch.isfinite(a.float()).all() and torch.equal(raw(a), raw(b))
