@@ -62,7 +62,8 @@ bool desc_ok(const epl_product_fp8_desc *p)
 // memory, once for every 32 rows of an expert. Measured (this way, tiles), us: 8
 // experts of 24 rows, 7168 -> 4096: 52, 63, gated with its cast 55, 76; 64 of 24,
 // 4096 -> 2048: 108, 106; 8 of 32, none of them more, 7168 -> 4096: 53, 63; but where
-// counts scatter about 32 half of the experts' weights are read twice.
+// counts scatter about 32 half of the experts' weights are read twice. The counts are on
+// the GPU: an uneven batch of few rows on average takes this way too, and longer.
 constexpr int64_t kFewRows = 24;
 
 // Large tiles take 2.2 us a stage for four times what a small one, two of them on

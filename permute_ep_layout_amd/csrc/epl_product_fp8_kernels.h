@@ -201,6 +201,9 @@ __device__ __forceinline__ void store_codes(const Args &a, int64_t at, const flo
 // epilogue 1000. LDS holds no third stage of 64 KB, and smaller tiles load more. Loads
 // of a further block into L2 alone gained 2% then, starts of the XCDs 10 to 20 us apart
 // nothing; the epilogue's passes as one loop (less code, but spilled sums) lost 5 to 9%.
+// Start, launch and epilogue of one round of large tiles (256 tiles, over 8 to 56 blocks,
+// extrapolated to none): 20 us, transposed 22, with a cast 45, gated gradient 34, and with
+// its cast 70.
 
 using epl_product::at;
 using epl_product::dma;
@@ -739,6 +742,10 @@ __global__ __launch_bounds__(tile_threads(BN)) void join_kernel(Args a, int grid
 //
 // Measured: 8 x 8 rows, 7168 -> 4096, gated, 47 us: 5.0 TB/s of weights (cast as well
 // 54); 64 x 1, 4096 -> 2048, 93 us, 5.8 TB/s; 8 x 24 as the first 55.
+//
+// An expert's rows are taken 32 at a time, in turn, by the same workgroup: 64 experts,
+// 4096 -> 2048, 1536 rows, 112 us evenly spread, 304 with half of them at one expert
+// (tiles 134).
 //
 // A CU reads no more than some 35 GB/s in this way. Where the columns are too
 // few for a workgroup on every CU, `parts` workgroups share the contraction,
