@@ -504,7 +504,9 @@ typedef struct epl_cast_desc {
 int epl_cast_validate(const epl_cast_desc *p);
 
 /* Rows to 8 bits. x [num_rows, C], or with EPL_ACT_SWIGLU [num_rows, 2C] whose
- * silu(x[:, :C]) * x[:, C:] is cast. With num_experts > 0 only the rows of the
+ * silu(x[:, :C]) * x[:, C:] is cast (silu within 32 * 2^-24 of the larger of its
+ * argument's magnitude and 1: a value next to a border may get the neighbouring
+ * code). With num_experts > 0 only the rows of the
  * experts' blocks (as in epl_expert_product) are cast and the others' codes
  * and scales left as they were; without, both block pointers are ignored and
  * all rows are. x and codes 16-byte aligned, the others 4. */

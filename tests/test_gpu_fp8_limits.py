@@ -121,3 +121,31 @@ def test_product_of_scales_at_the_ends_of_binary32(rows, transposed):
         assert (y[1] == 0).all()
     y = made(2.0 ** 80, 2.0 ** 48)
     assert (y[0] == float("inf")).all() and torch.isnan(y[1]).all()
+
+
+@pytest.mark.parametrize("transposed", [False, True])
+@pytest.mark.parametrize("N", [16, 48, 272, 304])
+@pytest.mark.parametrize("counts", [[5, 0, 11], [150, 0, 45]])
+def test_gated_product_of_halves_that_are_no_multiple_of_16(counts, N, transposed):
+    """Halves of 8, 24, 136 and 152 columns. Codes of small whole numbers: z is exact."""
+    K, E, total = 144, len(counts), sum(counts)
+    starts = [sum(counts[:e]) for e in range(E)]
+    pick = torch.tensor([0x00, 0x38, 0xB8, 0x40, 0xC0], dtype=torch.uint8)
+    g = torch.Generator().manual_seed(N)
+    x = pick[torch.randint(0, 5, (total, K), generator=g)]
+    shape = (E, K, N) if transposed else (E, N, K)
+    w = pick[torch.randint(0, 5, shape, generator=g)]
+    ws = torch.exp2(torch.randint(-6, -3, (E, ref.groups(shape[1]), ref.groups(shape[2])),
+                                  generator=g).float())
+    pre = torch.full((total, N), 7.0, dtype=torch.bfloat16, device=DEV)
+    y = epl.expert_product_fp8(x.to(DEV), torch.ones(total, 2, device=DEV), w.to(DEV),
+                               ws.to(DEV), i32(starts), i32(counts), activation="swiglu", pre=pre,
+                               out_dtype=torch.float32, transposed=transposed).cpu().double()
+    for e, (s, m) in enumerate(zip(starts, counts)):
+        v = ref.decode(w[e]) * ref.weight_scales(ws, *shape[1:])[e]
+        z = ref.decode(x[s:s + m]) @ (v if transposed else v.t())
+        assert torch.equal(pre[s:s + m].cpu(), z.bfloat16())
+        gate, up = z.chunk(2, 1)
+        own = 32 * 2.0 ** -24 * gate.abs().clamp(min=1)
+        want = gate * torch.sigmoid(gate) * up
+        assert ((y[s:s + m] - want).abs() <= own * up.abs() + 2 * 2.0 ** -24 * want.abs()).all()
